@@ -1,0 +1,396 @@
+// Norms of queries and keys per head with the position rotation in the same pass, their
+// backward, and the append of keys and values to a paged cache.
+//
+//   y = x w / sqrt(mean(x^2) + eps), then (a, b) -> (a cos - b sin, a sin + b cos) on each pair
+//
+// Bound by memory: a token's heads are read once and written once. A head's pairs need one
+// angle each, the same for all heads of a token, so a workgroup takes the cosines and sines of
+// its tokens into LDS first (one evaluation per token and pair) and then walks the heads. The
+// angle is formed in fp64 and reduced to a part of a turn before it is rounded: at position
+// 100,000 an fp32 angle would be off by 4e-3 radians.
+#include "history_device.h"
+
+namespace dlrm {
+namespace {
+
+constexpr int kThreads = 256;
+
+// A head of D elements is D / (2 V) lanes of two 16-byte pieces (V elements each), chosen so that
+// the pairs of the rotation lie in one lane: lane p < rot / (2 V) holds pairs V p .. V p + V - 1,
+// the other lanes what is not rotated.
+template <int DT, int D>
+struct Split {
+  static constexpr int V = Storage<DT>::per16;
+  static constexpr int lanes = D / (2 * V);  // per head: 2 .. 32
+  static constexpr int groups = kThreads / lanes;
+  int at[2];  // first element of each piece
+  bool rotated;
+
+  __device__ __forceinline__ Split(int lane, int rot, bool interleaved) {
+    const int turned = rot / (2 * V);
+    rotated = lane < turned;
+    if (rotated && !interleaved) {
+      at[0] = lane * V;
+      at[1] = rot / 2 + lane * V;
+    } else {  // neighbours: 2 V elements in a row, also where nothing is rotated
+      at[0] = 2 * lane * V;
+      at[1] = at[0] + V;
+    }
+  }
+};
+
+// cos and sin of the angles of tokens t0 .. t0 + count, [count][rot / 2] pairs in LDS.
+__device__ __forceinline__ void angles(const Rotation& r, long long t0, int count, float2* cs) {
+  const int pairs = r.rot / 2;
+  if (pairs == 0) return;
+  for (int i = threadIdx.x; i < count * pairs; i += kThreads) {
+    const int t = i / pairs, j = i - t * pairs;
+    int axis = 0;
+    while (j >= r.section_end[axis]) ++axis;  // the last section ends at pairs
+    const double turn = static_cast<double>(r.positions[axis * r.pos_stride + t0 + t]) *
+                        static_cast<double>(r.inv_freq[j]) * 0.15915494309189535;
+    float s, c;
+    sincospif(static_cast<float>(2.0 * (turn - rint(turn))), &s, &c);
+    cs[i] = make_float2(c, s);
+  }
+}
+
+// x: V elements of piece 0, then V of piece 1. dir = 1 turns by the angles, -1 turns back.
+template <int V>
+__device__ __forceinline__ void rotate(float* x, const float2* cs, bool interleaved, float dir) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float c = cs[i].x, s = dir * cs[i].y, a = x[2 * i], b = x[2 * i + 1];
+      x[2 * i] = a * c - b * s;
+      x[2 * i + 1] = a * s + b * c;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float c = cs[i].x, s = dir * cs[i].y, a = x[i], b = x[V + i];
+      x[i] = a * c - b * s;
+      x[V + i] = a * s + b * c;
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ const char* head_at(const Heads& x, long long token, int head) {
+  return static_cast<const char*>(x.ptr) + (token * x.stride + head * x.head_stride) * Storage<DT>::bytes;
+}
+
+// The (token, head) items of a workgroup's tokens, one to a group of lanes, groups apart.
+struct Items {
+  int t, h;
+  const int heads, dt, dh;
+  __device__ __forceinline__ Items(int group, int groups, int heads_)
+      : t(group / heads_), h(group - t * heads_), heads(heads_), dt(groups / heads_), dh(groups - dt * heads_) {}
+  __device__ __forceinline__ void next() {
+    t += dt;
+    h += dh;
+    if (h >= heads) {
+      h -= heads;
+      ++t;
+    }
+  }
+};
+
+// One kind of head (queries, keys or values) of the workgroup's tokens. Without slots it goes to
+// out, contiguous [n][heads][D]; else to the cache: slots holds the element offset of each token's
+// slot in head 0 of its page, or -1 for a token that is not stored.
+template <int DT, int D, bool TURN>
+__device__ __forceinline__ void walk(const NormRopeArgs& a, const Heads& x, int heads, const float* w, long long t0,
+                                     int count, const float2* cs, void* out, const long long* slots) {
+  using S = Split<DT, D>;
+  constexpr int V = S::V;
+  const int lane = threadIdx.x % S::lanes;
+  const S split(lane, TURN ? a.rope.rot : 0, a.rope.interleaved);
+  float wv[2 * V];
+  if (w) {
+#pragma unroll
+    for (int i = 0; i < 2 * V; ++i) wv[i] = w[split.at[i / V] + i % V];
+  }
+  const int pairs = a.rope.rot / 2;
+  if (heads == 0) return;
+  for (Items it(threadIdx.x / S::lanes, S::groups, heads); it.t < count; it.next()) {
+    const int t = it.t, h = it.h;
+    const char* from = head_at<DT>(x, t0 + t, h);
+    uint4 piece[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      piece[i] = *reinterpret_cast<const uint4*>(from + split.at[i] * Storage<DT>::bytes);
+    if constexpr (TURN) {
+      float y[2 * V];
+      widen<DT>(piece[0], y);
+      widen<DT>(piece[1], y + V);
+      if (w) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) sum = fmaf(y[i], y[i], sum);
+        sum = group_sum<S::lanes>(sum);
+        const float r = rsqrtf(sum * (1.f / D) + a.eps);
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) y[i] = y[i] * r * wv[i];
+      }
+      if (split.rotated) rotate<V>(y, cs + t * pairs + lane * V, a.rope.interleaved, 1.f);
+      piece[0] = narrow<DT>(y);
+      piece[1] = narrow<DT>(y + V);
+    }
+    char* to;
+    if (slots) {
+      const long long slot = slots[t];
+      if (slot < 0) continue;
+      to = static_cast<char*>(out) + (slot + h * a.paged.head_stride) * Storage<DT>::bytes;
+    } else {
+      to = static_cast<char*>(out) + ((t0 + t) * heads + h) * D * Storage<DT>::bytes;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(to + split.at[i] * Storage<DT>::bytes) = piece[i];
+  }
+}
+
+constexpr int kMaxTokens = 8;  // tokens of a workgroup
+
+// Cache slots of tokens t0 .. t0 + count, one wave each.
+template <int D>
+__device__ __forceinline__ void find_slots(const Paged& p, long long n, long long t0, int count, long long* slots) {
+  const int lane = threadIdx.x & (kWave - 1);
+  for (int t = threadIdx.x / kWave; t < count; t += kThreads / kWave) {
+    const int token = static_cast<int>(t0) + t;
+    const int seq = wave_upper_bound(p.q_offsets, p.seqs + 1, token) - 1;
+    long long slot = -1;
+    if (seq >= 0 && seq < p.seqs) {  // else the token is past the last sequence
+      const int first = p.q_offsets[seq], last = p.q_offsets[seq + 1];
+      const int held = p.kv_lens[seq];
+      const long long room = static_cast<long long>(p.table_width) << p.page_shift;
+      bool bad = first < 0 || last > n || token < first || token >= last;
+      const long long at = static_cast<long long>(held) - last + token;
+      bad |= at < 0 || at >= room || held < 0 || held > room;
+      if (bad) {
+        if (lane == 0) flag(p.status, DLRM_STATUS_BAD_OFFSETS);
+      } else {
+        const int page = p.page_table[seq * p.table_stride + (at >> p.page_shift)];
+        if (page < 0 || page >= p.num_pages) {
+          if (lane == 0) flag(p.status, DLRM_STATUS_BAD_PAGE);
+        } else {
+          slot = page * p.page_stride + (at & ((1LL << p.page_shift) - 1)) * D;
+        }
+      }
+    }
+    if (lane == 0) slots[t] = slot;
+  }
+}
+
+template <int DT, int D, bool APPEND>
+__global__ __launch_bounds__(kThreads) void norm_rope_kernel(NormRopeArgs a, int per_group) {
+  __shared__ float2 cs[kMaxTokens * D / 2];
+  __shared__ long long slots[APPEND ? kMaxTokens : 1];
+  const long long t0 = static_cast<long long>(blockIdx.x) * per_group;
+  const int count = static_cast<int>(a.n - t0 < per_group ? a.n - t0 : per_group);
+  angles(a.rope, t0, count, cs);
+  if constexpr (APPEND) find_slots<D>(a.paged, a.n, t0, count, slots);
+  __syncthreads();
+  walk<DT, D, true>(a, a.q, a.q_heads, a.w_q, t0, count, cs, a.q_out, nullptr);
+  if constexpr (APPEND) {
+    walk<DT, D, true>(a, a.k, a.kv_heads, a.w_k, t0, count, cs, a.k_cache, slots);
+    walk<DT, D, false>(a, a.v, a.kv_heads, nullptr, t0, count, cs, a.v_cache, slots);
+  } else {
+    walk<DT, D, true>(a, a.k, a.kv_heads, a.w_k, t0, count, cs, a.k_out, nullptr);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+constexpr int kBwdGroups = 1024;  // workgroups that share the tokens; one row of partial weight gradients each
+constexpr int kBwdTokens = 4;     // tokens whose angles are held at once
+
+template <int DT, int D>
+__device__ __forceinline__ void walk_bwd(const NormRopeBwdArgs& a, const Heads& dy, const Heads& x, int heads,
+                                         const float* w, long long t0, int count, const float2* cs, void* out,
+                                         float* dw) {
+  using S = Split<DT, D>;
+  constexpr int V = S::V;
+  const int lane = threadIdx.x % S::lanes;
+  const S split(lane, a.rope.rot, a.rope.interleaved);
+  float wv[2 * V];
+  if (w) {
+#pragma unroll
+    for (int i = 0; i < 2 * V; ++i) wv[i] = w[split.at[i / V] + i % V];
+  }
+  const int pairs = a.rope.rot / 2;
+  for (Items it(threadIdx.x / S::lanes, S::groups, heads); it.t < count; it.next()) {
+    const int t = it.t, h = it.h;
+    const char* from = head_at<DT>(dy, t0 + t, h);
+    float g[2 * V];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      widen<DT>(*reinterpret_cast<const uint4*>(from + split.at[i] * Storage<DT>::bytes), g + i * V);
+    if (split.rotated) rotate<V>(g, cs + t * pairs + lane * V, a.rope.interleaved, -1.f);
+    if (w) {
+      const char* in = head_at<DT>(x, t0 + t, h);
+      float u[2 * V];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        widen<DT>(*reinterpret_cast<const uint4*>(in + split.at[i] * Storage<DT>::bytes), u + i * V);
+      float sq = 0.f, dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i) {
+        sq = fmaf(u[i], u[i], sq);
+        dot = fmaf(g[i] * wv[i], u[i], dot);
+      }
+      sq = group_sum<S::lanes>(sq);
+      dot = group_sum<S::lanes>(dot);
+      const float r = rsqrtf(sq * (1.f / D) + a.eps);
+      const float mean = dot * r * (1.f / D);  // mean of g w u r
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i) {
+        u[i] *= r;
+        dw[i] = fmaf(g[i], u[i], dw[i]);
+        g[i] = r * (g[i] * wv[i] - u[i] * mean);
+      }
+    }
+    char* to = static_cast<char*>(out) + ((t0 + t) * heads + h) * D * Storage<DT>::bytes;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint4*>(to + split.at[i] * Storage<DT>::bytes) = narrow<DT>(g + i * V);
+  }
+}
+
+// Sums dw over the groups of the workgroup into row[D], in a fixed order.
+template <int DT, int D>
+__device__ __forceinline__ void join(const Rotation& rope, const float* dw, float* lds, float* row) {
+  using S = Split<DT, D>;
+  constexpr int V = S::V;
+  const int lane = threadIdx.x % S::lanes;
+  const S split(lane, rope.rot, rope.interleaved);
+  __syncthreads();  // lds is free again
+#pragma unroll
+  for (int i = 0; i < 2 * V; ++i) {
+    float v = dw[i];
+#pragma unroll
+    for (int m = S::lanes; m < kWave; m *= 2) v += __shfl_xor(v, m);  // lanes that hold the same element
+    if (threadIdx.x % kWave < S::lanes) lds[threadIdx.x / kWave * D + split.at[i / V] + i % V] = v;
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += kThreads) row[d] = lds[d] + lds[D + d] + lds[2 * D + d] + lds[3 * D + d];
+}
+
+template <int DT, int D>
+__global__ __launch_bounds__(kThreads) void norm_rope_bwd_kernel(NormRopeBwdArgs a) {
+  constexpr int V = Storage<DT>::per16;
+  __shared__ float2 cs[kBwdTokens * D / 2];
+  __shared__ float lds[kThreads / kWave * D];
+  float dq[2 * V] = {}, dk[2 * V] = {};
+  const long long step = static_cast<long long>(gridDim.x) * kBwdTokens;
+  for (long long t0 = static_cast<long long>(blockIdx.x) * kBwdTokens; t0 < a.n; t0 += step) {
+    const int count = static_cast<int>(a.n - t0 < kBwdTokens ? a.n - t0 : kBwdTokens);
+    __syncthreads();  // the angles of the tokens before are no longer read
+    angles(a.rope, t0, count, cs);
+    __syncthreads();
+    walk_bwd<DT, D>(a, a.dq_out, a.q, a.q_heads, a.w_q, t0, count, cs, a.d_q, dq);
+    walk_bwd<DT, D>(a, a.dk_out, a.k, a.kv_heads, a.w_k, t0, count, cs, a.d_k, dk);
+  }
+  if (a.w_q) {
+    float* row = a.partials + static_cast<long long>(blockIdx.x) * 2 * D;
+    join<DT, D>(a.rope, dq, lds, row);
+    join<DT, D>(a.rope, dk, lds, row + D);
+  }
+}
+
+// Columns of the partial weight gradients [rows][2 D] summed in a fixed order, in fp64: 32 columns
+// to a workgroup, eight threads to a column.
+__global__ __launch_bounds__(kThreads) void norm_rope_dw_kernel(const float* __restrict__ partials, int rows, int dim,
+                                                                float* d_w_q, float* d_w_k) {
+  __shared__ double lds[8][32];
+  const int col = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32;
+  double sum = 0.;
+  for (int r = part; r < rows; r += 8) sum += partials[static_cast<long long>(r) * 2 * dim + col];
+  lds[part][threadIdx.x % 32] = sum;
+  __syncthreads();
+  if (part == 0) {
+    for (int i = 1; i < 8; ++i) sum += lds[i][threadIdx.x];
+    (col < dim ? d_w_q + col : d_w_k + (col - dim))[0] = static_cast<float>(sum);
+  }
+}
+
+// Tokens of a workgroup: as many as leave four workgroups to each CU, so that the angles of a
+// token are shared by all its heads and small calls still spread over the chip.
+int tokens_per_group(long long n) {
+  long long t = n / 1024;
+  return static_cast<int>(t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t);
+}
+
+template <int DT, int D, bool APPEND>
+hipError_t run(const NormRopeArgs& a, hipStream_t s) {
+  const int per = tokens_per_group(a.n);
+  hipLaunchKernelGGL((norm_rope_kernel<DT, D, APPEND>), dim3(static_cast<unsigned>((a.n + per - 1) / per)),
+                     dim3(kThreads), 0, s, a, per);
+  return hipGetLastError();
+}
+
+template <int DT, bool APPEND>
+hipError_t run_dim(const NormRopeArgs& a, hipStream_t s) {
+  switch (a.dim) {
+    case 32: return run<DT, 32, APPEND>(a, s);
+    case 64: return run<DT, 64, APPEND>(a, s);
+    case 128: return run<DT, 128, APPEND>(a, s);
+    default: return run<DT, 256, APPEND>(a, s);
+  }
+}
+
+int bwd_groups(long long n) {
+  const long long g = (n + kBwdTokens - 1) / kBwdTokens;
+  return static_cast<int>(g < kBwdGroups ? g : kBwdGroups);
+}
+
+template <int DT, int D>
+hipError_t run_bwd(const NormRopeBwdArgs& a, hipStream_t s) {
+  const int groups = bwd_groups(a.n);
+  if (groups > 0) hipLaunchKernelGGL((norm_rope_bwd_kernel<DT, D>), dim3(groups), dim3(kThreads), 0, s, a);
+  if (a.w_q)
+    hipLaunchKernelGGL(norm_rope_dw_kernel, dim3(2 * D / 32), dim3(kThreads), 0, s, a.partials, groups, D, a.d_w_q,
+                       a.d_w_k);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t run_bwd_dim(const NormRopeBwdArgs& a, hipStream_t s) {
+  switch (a.dim) {
+    case 32: return run_bwd<DT, 32>(a, s);
+    case 64: return run_bwd<DT, 64>(a, s);
+    case 128: return run_bwd<DT, 128>(a, s);
+    default: return run_bwd<DT, 256>(a, s);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_norm_rope(const NormRopeArgs& a, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  switch (a.dtype) {
+    case DLRM_F32: return run_dim<DLRM_F32, false>(a, s);
+    case DLRM_F16: return run_dim<DLRM_F16, false>(a, s);
+    default: return run_dim<DLRM_BF16, false>(a, s);
+  }
+}
+
+hipError_t launch_kv_append(const NormRopeArgs& a, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  return a.dtype == DLRM_F16 ? run_dim<DLRM_F16, true>(a, s) : run_dim<DLRM_BF16, true>(a, s);
+}
+
+size_t norm_rope_bwd_workspace(int64_t n, int dim, bool norm) {
+  return norm ? static_cast<size_t>(bwd_groups(n)) * 2 * dim * sizeof(float) : 0;
+}
+
+hipError_t launch_norm_rope_bwd(const NormRopeBwdArgs& a, hipStream_t s) {
+  switch (a.dtype) {
+    case DLRM_F32: return run_bwd_dim<DLRM_F32>(a, s);
+    case DLRM_F16: return run_bwd_dim<DLRM_F16>(a, s);
+    default: return run_bwd_dim<DLRM_BF16>(a, s);
+  }
+}
+
+}  // namespace dlrm

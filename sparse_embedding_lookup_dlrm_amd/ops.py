@@ -1,4 +1,5 @@
-"""Thin ctypes binding over libdlrm_embbag.so (C ABI: include/dlrm_embbag.h).
+"""Thin ctypes binding over libdlrm_embbag.so (C ABI: include/dlrm_embbag.h and, for the
+attention over user histories, include/dlrm_history.h).
 
 Only argument marshalling happens here: torch supplies device memory and the
 current HIP stream; every step of the computation runs in the library's HIP
@@ -16,19 +17,27 @@ import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdlrm_embbag.so")
 INCLUDE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
-HEADERS = [os.path.join(INCLUDE, "dlrm_embbag.h"), os.path.join(INCLUDE, "dlrm_probe.h")]
+HEADERS = [os.path.join(INCLUDE, "dlrm_embbag.h"), os.path.join(INCLUDE, "dlrm_probe.h"),
+           os.path.join(INCLUDE, "dlrm_history.h")]
 
 DLRM_F32, DLRM_F16, DLRM_BF16 = 0, 1, 2
 PAIRS_SELF, WITH_EMBEDDINGS = 1, 2  # interaction layout bits
 STATUS_BAD_INDEX = 1
 STATUS_BAD_OFFSETS = 2
+STATUS_BAD_PAGE = 4
 MAX_TABLES = 128
+MAX_AXES = 8
 
 _TORCH_DT = {torch.float32: DLRM_F32, torch.float16: DLRM_F16, torch.bfloat16: DLRM_BF16}
 
 _c_void_p = ctypes.c_void_p
 _i32, _i64, _f32, _size_t = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _P = ctypes.POINTER
+
+# argument groups of dlrm_history.h: a tensor of heads (address, token and head stride), and the
+# rotation and norm (positions .. interleaved)
+_HEADS = [_c_void_p, _i64, _i64]
+_TURN = [_c_void_p, _i64, _i32, _P(_i32), _c_void_p, _c_void_p, _c_void_p, _f32, _i32]
 
 _SIGNATURES = {
     "dlrm_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -68,6 +77,20 @@ _SIGNATURES = {
                                                       _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p, _f32,
                                                       _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                                       _c_void_p, _c_void_p]),
+    "dlrm_qk_norm_rope": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, *_HEADS, *_HEADS, *_TURN, _c_void_p,
+                                         _c_void_p, _c_void_p]),
+    "dlrm_qk_norm_rope_bwd_workspace_bytes": (ctypes.c_int, [_i64, _i32, _i32, _P(_size_t)]),
+    "dlrm_qk_norm_rope_bwd": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, *_HEADS, *_HEADS, *_HEADS, *_HEADS,
+                                             *_TURN, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size_t,
+                                             _c_void_p]),
+    "dlrm_kv_append": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, *_HEADS, *_HEADS, *_HEADS, *_TURN,
+                                      _c_void_p, _c_void_p, _c_void_p, _i64, _i32, _i32, _i64, _i64, _i64, _c_void_p,
+                                      _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "dlrm_paged_attn_workspace_bytes": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                                       _P(_size_t)]),
+    "dlrm_paged_attn": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, *_HEADS, _c_void_p, _c_void_p, _i32, _i64,
+                                       _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _i64, _i32, _i32, _i32, _f32, _i32,
+                                       _i32, _c_void_p, _c_void_p, _c_void_p, _size_t, _c_void_p, _c_void_p]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -550,3 +573,275 @@ class BwdPlan:
 
     def run(self):
         _check(self._fn(*self._args), self._name)
+
+
+# Attention over user histories (include/dlrm_history.h).
+
+
+def _heads_of(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None, heads: Optional[int] = None):
+    """Checks a tensor of heads [tokens, heads, dim], the elements of a head contiguous; like: the tensor
+    whose tokens, dim, dtype and device it has to share. Returns its address and strides."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(t.shape)}")
+    if like is None:
+        if t.dtype not in _TORCH_DT:
+            raise ValueError(f"unsupported dtype {t.dtype} of {name}")
+    else:
+        if t.dtype != like.dtype:
+            raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
+        if t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]:
+            raise ValueError(f"{name} is {tuple(t.shape)}, needs [{like.shape[0]}, heads, {like.shape[2]}]")
+        if t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if heads is not None and t.shape[1] != heads:
+        raise ValueError(f"{name} has {t.shape[1]} heads, needs {heads}")
+    a, b, c = t.stride()
+    if c != 1 and t.shape[2] != 1:
+        raise ValueError(f"the elements of a head of {name} must be contiguous")
+    return t.data_ptr(), a, b
+
+
+def _same_device(like: torch.Tensor, **ts) -> None:
+    dev = like.device
+    for name, t in ts.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _contiguous(**ts) -> None:
+    for name, t in ts.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _turn_args(like, positions, inv_freq, w_q, w_k, eps, sections, interleaved, tokens: int, dim: int):
+    """rot, and the arguments from positions to interleaved."""
+    if inv_freq is None:
+        rot, pos, stride, axes, secs, freq = 0, None, 0, 0, None, None
+    else:
+        rot = 2 * inv_freq.numel()
+        _expect(inv_freq, "inv_freq", torch.float32, rot // 2)
+        if positions is None or positions.dtype != torch.int32 or positions.dim() not in (1, 2):
+            raise ValueError("positions must be torch.int32 [tokens] or [axes, tokens]")
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        if positions.shape[-1] != tokens or (tokens > 1 and positions.stride(-1) != 1):
+            raise ValueError(f"positions must be [axes, {tokens}] with the tokens contiguous, got "
+                             f"{tuple(positions.shape)} with strides {positions.stride()}")
+        if sections is None:
+            if axes != 1:
+                raise ValueError("sections are needed with more than one axis of positions")
+            sections = (rot // 2,)
+        if len(sections) != axes:
+            raise ValueError(f"{len(sections)} sections for {axes} axes of positions")
+        stride = positions.stride(0) if positions.dim() == 2 else 0
+        secs, pos, freq = (_i32 * axes)(*sections), positions.data_ptr(), inv_freq.data_ptr()
+    if (w_q is None) != (w_k is None):
+        raise ValueError("w_q and w_k come together")
+    _expect(w_q, "w_q", torch.float32, dim)
+    _expect(w_k, "w_k", torch.float32, dim)
+    _contiguous(inv_freq=inv_freq, w_q=w_q, w_k=w_k)
+    _same_device(like, positions=positions, inv_freq=inv_freq, w_q=w_q, w_k=w_k)
+    return rot, (pos, stride, axes, secs, freq, _ptr(w_q), _ptr(w_k), eps, 1 if interleaved else 0)
+
+
+class _on:
+    """The device and stream a call works on: buffers made within belong to that stream, so that one
+    freed on return is not handed out again before the stream has passed the call."""
+
+    def __init__(self, device: torch.device, stream):
+        if device.type != "cuda":
+            raise ValueError("device tensors must be CUDA (HIP) tensors")
+        self._outer = None
+        if stream is not None:
+            self._outer = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != device.index:
+            self._outer = torch.cuda.device(device)
+        self._stream = stream
+
+    def __enter__(self) -> int:
+        if self._outer is not None:
+            self._outer.__enter__()
+        return (torch.cuda.current_stream() if self._stream is None else self._stream).cuda_stream
+
+    def __exit__(self, *exc):
+        if self._outer is not None:
+            self._outer.__exit__(*exc)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor],
+                 inv_freq: Optional[torch.Tensor], w_q: Optional[torch.Tensor] = None,
+                 w_k: Optional[torch.Tensor] = None, *, eps: float = 1e-6, sections: Optional[Sequence[int]] = None,
+                 interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Norm of each head of q [N, Hq, D] and k [N, Hk, D] (with w_q, w_k fp32 [D]) and the position
+    rotation of its first 2 * len(inv_freq) elements (dlrm_qk_norm_rope); returns contiguous (q, k).
+    positions is int32 [N] or, with `sections` pairs to each axis, [axes, N]; inv_freq None: no rotation."""
+    N, Hq, D = q.shape if q.dim() == 3 else (0, 0, 0)
+    qa = _heads_of(q, "q")
+    ka = _heads_of(k, "k", like=q)
+    Hk = k.shape[1]
+    rot, turn = _turn_args(q, positions, inv_freq, w_q, w_k, eps, sections, interleaved, N, D)
+    _expect(q_out, "q_out", q.dtype, N * Hq * D)
+    _expect(k_out, "k_out", q.dtype, N * Hk * D)
+    _contiguous(q_out=q_out, k_out=k_out)
+    _same_device(q, q_out=q_out, k_out=k_out)
+    with _on(q.device, stream) as s:
+        if q_out is None:
+            q_out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
+        if k_out is None:
+            k_out = torch.empty((N, Hk, D), dtype=q.dtype, device=q.device)
+        _check(lib().dlrm_qk_norm_rope(N, Hq, Hk, D, rot, _TORCH_DT[q.dtype], *qa, *ka, *turn, q_out.data_ptr(),
+                                       k_out.data_ptr(), s), "dlrm_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                     positions: Optional[torch.Tensor], inv_freq: Optional[torch.Tensor],
+                     w_q: Optional[torch.Tensor] = None, w_k: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
+                     sections: Optional[Sequence[int]] = None, interleaved: bool = False,
+                     workspace: Optional[torch.Tensor] = None, stream=None
+                     ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradients of qk_norm_rope from those of its outputs (dlrm_qk_norm_rope_bwd); q, k and what
+    follows as in the forward. Returns (d_q, d_k, d_w_q, d_w_k), the weights' fp32, None without a norm."""
+    N, Hq, D = q.shape if q.dim() == 3 else (0, 0, 0)
+    qa = _heads_of(q, "q")
+    ka = _heads_of(k, "k", like=q)
+    Hk = k.shape[1]
+    dqa = _heads_of(d_q_out, "d_q_out", like=q, heads=Hq)
+    dka = _heads_of(d_k_out, "d_k_out", like=q, heads=Hk)
+    rot, turn = _turn_args(q, positions, inv_freq, w_q, w_k, eps, sections, interleaved, N, D)
+    need = _size_t(0)
+    _check(lib().dlrm_qk_norm_rope_bwd_workspace_bytes(N, D, 0 if w_q is None else 1, ctypes.byref(need)),
+           "dlrm_qk_norm_rope_bwd_workspace_bytes")
+    _expect(workspace, "workspace", torch.uint8, need.value, at_least=True)
+    _contiguous(workspace=workspace)
+    _same_device(q, workspace=workspace)
+    dev = q.device
+    with _on(dev, stream) as s:
+        d_q = torch.empty((N, Hq, D), dtype=q.dtype, device=dev)
+        d_k = torch.empty((N, Hk, D), dtype=q.dtype, device=dev)
+        d_w_q = d_w_k = None
+        if w_q is not None:
+            d_w_q = torch.empty(D, dtype=torch.float32, device=dev)
+            d_w_k = torch.empty(D, dtype=torch.float32, device=dev)
+            if workspace is None:
+                workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        _check(lib().dlrm_qk_norm_rope_bwd(N, Hq, Hk, D, rot, _TORCH_DT[q.dtype], *dqa, *dka, *qa, *ka, *turn,
+                                           d_q.data_ptr(), d_k.data_ptr(), _ptr(d_w_q), _ptr(d_w_k), _ptr(workspace),
+                                           0 if workspace is None else workspace.numel(), s),
+               "dlrm_qk_norm_rope_bwd")
+    return d_q, d_k, d_w_q, d_w_k
+
+
+def _paged_args(like, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk: int, D: int):
+    """Checks the cache and the sequences. Returns (seqs, page, pages, page and head stride)."""
+    if k_cache.dim() != 4 or k_cache.shape[1] != Hk or k_cache.shape[3] != D:
+        raise ValueError(f"k_cache must be [pages, {Hk}, page, {D}], got {tuple(k_cache.shape)}")
+    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+        raise ValueError("v_cache must have k_cache's shape and strides")
+    if k_cache.dtype != like.dtype or v_cache.dtype != like.dtype:
+        raise ValueError(f"the caches must be {like.dtype}, got {k_cache.dtype} and {v_cache.dtype}")
+    if page_table.dim() != 2 or page_table.dtype != torch.int32:
+        raise ValueError("page_table must be torch.int32 [sequences, pages]")
+    S, width = page_table.shape
+    if width > 1 and page_table.stride(1) != 1:
+        raise ValueError("the entries of a row of page_table must be contiguous")
+    _expect(q_offsets, "q_offsets", torch.int32, S + 1)
+    _expect(kv_lens, "kv_lens", torch.int32, S)
+    _expect(status, "status", torch.int32, 1, at_least=True)
+    _contiguous(q_offsets=q_offsets, kv_lens=kv_lens, status=status)
+    _same_device(like, k_cache=k_cache, v_cache=v_cache, q_offsets=q_offsets, kv_lens=kv_lens, page_table=page_table,
+                 status=status)
+    pages, _, page, _ = k_cache.shape
+    by_page, by_head, by_slot, by_elem = k_cache.stride()
+    if pages > 0 and (by_slot != D or by_elem != 1):
+        raise ValueError("a page's entries of a head must be contiguous in the caches")
+    return S, page, pages, by_page, by_head
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              q_offsets: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor, *,
+              q: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+              inv_freq: Optional[torch.Tensor] = None, w_q: Optional[torch.Tensor] = None,
+              w_k: Optional[torch.Tensor] = None, eps: float = 1e-6, sections: Optional[Sequence[int]] = None,
+              interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Appends k (normed and rotated as by qk_norm_rope) and v, [N, Hk, D], to the paged caches
+    [pages, Hk, page, D] in place, and norms and rotates q in the same launch (dlrm_kv_append).
+    Sequence s has tokens q_offsets[s] .. q_offsets[s + 1], the last entries of its kv_lens[s].
+    Returns the new q, contiguous, or None without q (then w_q is not taken)."""
+    N, Hk, D = k.shape if k.dim() == 3 else (0, 0, 0)
+    ka = _heads_of(k, "k")
+    va = _heads_of(v, "v", like=k, heads=Hk)
+    Hq, qa = 0, (None, 0, 0)
+    if q is not None:
+        qa = _heads_of(q, "q", like=k)
+        Hq = q.shape[1]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    elif w_q is not None:
+        raise ValueError("w_q without q")
+    rot, turn = _turn_args(k, positions, inv_freq, w_k if q is None else w_q, w_k, eps, sections, interleaved, N, D)
+    if q is None:
+        turn = turn[:5] + (None,) + turn[6:]
+    S, page, pages, by_page, by_head = _paged_args(k, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk, D)
+    _expect(q_out, "q_out", k.dtype, N * Hq * D)
+    _contiguous(q_out=q_out)
+    _same_device(k, q_out=q_out)
+    with _on(k.device, stream) as s:
+        if q is not None and q_out is None:
+            q_out = torch.empty((N, Hq, D), dtype=k.dtype, device=k.device)
+        _check(lib().dlrm_kv_append(N, S, Hq, Hk, D, rot, _TORCH_DT[k.dtype], *qa, *ka, *va, *turn,
+                                    q_offsets.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
+                                    page_table.stride(0), page_table.shape[1], page, pages, by_page, by_head,
+                                    k_cache.data_ptr(), v_cache.data_ptr(), _ptr(q_out), _ptr(status), s),
+               "dlrm_kv_append")
+    return q_out
+
+
+def paged_attn_workspace_bytes(N: int, S: int, Hq: int, Hk: int, D: int, causal: bool, window: int, max_q: int,
+                               max_kv: int) -> int:
+    out = _size_t(0)
+    _check(lib().dlrm_paged_attn_workspace_bytes(N, S, Hq, Hk, D, 1 if causal else 0, window, max_q, max_kv,
+                                                 ctypes.byref(out)), "dlrm_paged_attn_workspace_bytes")
+    return out.value
+
+
+def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, q_offsets: torch.Tensor,
+               kv_lens: torch.Tensor, page_table: torch.Tensor, *, causal: bool = True, window: int = 0,
+               scale: Optional[float] = None, max_q: Optional[int] = None, max_kv: Optional[int] = None,
+               want_lse: bool = False, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Attention of the new tokens q [N, Hq, D] over the paged caches [pages, Hk, page, D]
+    (dlrm_paged_attn); the sequences as in kv_append. window > 0 (with causal): a token sees the last
+    `window` entries up to its own. max_q, max_kv: the most new tokens and the longest history of a
+    sequence, for how the work is cut; without them N and the page table's width are taken. Returns
+    out [N, Hq, D], or (out, lse [N, Hq] fp32) with want_lse."""
+    N, Hq, D = q.shape if q.dim() == 3 else (0, 0, 0)
+    qa = _heads_of(q, "q")
+    Hk = k_cache.shape[1] if k_cache.dim() == 4 else 0
+    S, page, pages, by_page, by_head = _paged_args(q, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk, D)
+    max_q = N if max_q is None else max_q
+    max_kv = page_table.shape[1] * page if max_kv is None else max_kv
+    scale = D ** -0.5 if scale is None and D > 0 else scale
+    need = paged_attn_workspace_bytes(N, S, Hq, Hk, D, causal, window, max_q, max_kv)
+    _expect(out, "out", q.dtype, N * Hq * D)
+    _expect(lse, "lse", torch.float32, N * Hq)
+    _expect(workspace, "workspace", torch.uint8, need, at_least=True)
+    _contiguous(out=out, lse=lse, workspace=workspace)
+    _same_device(q, out=out, lse=lse, workspace=workspace)
+    dev = q.device
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((N, Hq, D), dtype=q.dtype, device=dev)
+        if lse is None and want_lse:
+            lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(lib().dlrm_paged_attn(N, S, Hq, Hk, D, _TORCH_DT[q.dtype], *qa, k_cache.data_ptr(), v_cache.data_ptr(),
+                                     page, pages, by_page, by_head, q_offsets.data_ptr(), kv_lens.data_ptr(),
+                                     page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
+                                     1 if causal else 0, window, scale, max_q, max_kv, out.data_ptr(), _ptr(lse),
+                                     _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(status), s),
+               "dlrm_paged_attn")
+    return (out, lse) if want_lse else out
