@@ -39,11 +39,17 @@ __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f3
                                                   0);
 }
 
-// Whether one of the two 16-bit values of a dword is infinite or NaN.
+// All bits of those of the two 16-bit values of a dword that are infinite or NaN.
 template <int DT>
-__device__ __forceinline__ bool not_finite(uint32_t w) {
+__device__ __forceinline__ uint32_t not_finite_halves(uint32_t w) {
   constexpr uint32_t e = DT == DLRM_BF16 ? 0x7f80u : 0x7c00u;
-  return (w & e) == e || (w >> 16 & e) == e;
+  return ((w & e) == e ? 0xffffu : 0u) | ((w >> 16 & e) == e ? 0xffff0000u : 0u);
+}
+
+// A word that is the same for the whole wave, read by the scalar unit: no wait for it holds up vector
+// loads on the way. Nothing writes the arrays read so while a kernel runs.
+__device__ __forceinline__ int scalar_load(const int32_t* p, long long i) {
+  return ((const __attribute__((address_space(4))) int32_t*)p)[i];
 }
 
 // A sequence of the call: its tokens and its history, checked.
@@ -53,8 +59,8 @@ struct Seq {
 
 __device__ __forceinline__ Seq load_seq(const Paged& p, long long n, int seq) {
   Seq s;
-  const int a = p.q_offsets[seq], b = p.q_offsets[seq + 1];
-  const int held = p.kv_lens[seq], room = p.table_width << p.page_shift;
+  const int a = scalar_load(p.q_offsets, seq), b = scalar_load(p.q_offsets, seq + 1LL);
+  const int held = scalar_load(p.kv_lens, seq), room = p.table_width << p.page_shift;
   const bool bad = a < 0 || b < a || b > n;
   s.first = bad ? 0 : a;
   s.tokens = bad ? 0 : b - a;
@@ -104,10 +110,10 @@ struct Reach {
   int lo, hi;          // some row sees these
   int all_lo, all_hi;  // every row sees these
   int first, part, parts;
-  __device__ __forceinline__ Reach(const Seq& s, long long row0, long long row_end, int group, int causal, int window,
+  __device__ __forceinline__ Reach(const Seq& s, int row0, int row_end, int group, int causal, int window,
                                    const Cut& cut) {
-    tok0 = static_cast<int>(row0 / group);
-    tok1 = static_cast<int>((row_end - 1) / group);
+    tok0 = row0 / group;
+    tok1 = (row_end - 1) / group;
     const Span s0 = seen_by(s, tok0, causal, window), s1 = seen_by(s, tok1, causal, window);
     lo = s0.lo;
     hi = s1.hi;
@@ -116,7 +122,7 @@ struct Reach {
     first = lo & ~31;
     const int span = hi > first ? hi - first : 0;
     part = cut.part;
-    if (span > static_cast<long long>(part) * cut.splits) part = static_cast<int>(((static_cast<long long>(span) + cut.splits - 1) / cut.splits + 31) & ~31LL);
+    if (span > static_cast<long long>(part) * cut.splits) part = static_cast<int>(((static_cast<long long>(span) + cut.splits - 1) / cut.splits + 63) & ~63LL);
     parts = span > part ? static_cast<int>((static_cast<long long>(span) + part - 1) / part) : 1;
   }
 };
@@ -153,13 +159,14 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, Cut cut
     rest /= cut.splits;
     const int seq = static_cast<int>(rest / cut.q_tiles);
     const Seq sq = load_seq(pg, a.n, seq);
-    const long long rows = static_cast<long long>(sq.tokens) * group;
+    const int rows = sq.tokens * group;
     const uint16_t* kh = static_cast<const uint16_t*>(a.k_cache) + head * pg.head_stride;
     const uint16_t* vh = static_cast<const uint16_t*>(a.v_cache) + head * pg.head_stride;
     const int32_t* table = pg.page_table + seq * pg.table_stride;
 
-    for (long long row0 = rest % cut.q_tiles * Rows; row0 < rows; row0 += static_cast<long long>(cut.q_tiles) * Rows) {
-      const long long row_end = row0 + Rows < rows ? row0 + Rows : rows;
+    for (long long first_row = rest % cut.q_tiles * Rows; first_row < rows;
+         first_row += static_cast<long long>(cut.q_tiles) * Rows) {
+      const int row0 = static_cast<int>(first_row), row_end = rows - row0 > Rows ? row0 + Rows : rows;
       const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut);
       if (split >= rc.parts) continue;
       const int tok0 = rc.tok0, tok1 = rc.tok1, lo = rc.lo;
@@ -170,13 +177,13 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, Cut cut
       int row_lo[RT], row_hi[RT], row_tok[RT];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        const long long row = row0 + rt * 16 + c16;
+        const int row = row0 + rt * 16 + c16;
         row_lo[rt] = row_hi[rt] = 0;
         row_tok[rt] = -1;
 #pragma unroll
         for (int f = 0; f < F; ++f) qf[rt][f] = u32x4{0, 0, 0, 0};
         if (row < row_end) {
-          const int tok = static_cast<int>(row / group), gi = static_cast<int>(row - static_cast<long long>(tok) * group);
+          const int tok = row / group, gi = row - tok * group;
           const Span s = seen_by(sq, tok, a.causal, a.window);
           row_lo[rt] = s.lo;
           row_hi[rt] = s.hi;
@@ -209,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, Cut cut
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int key = k0 + 16 * i < hi ? k0 + 16 * i : hi - 1;
-          const int page = table[key >> pg.page_shift];
+          const int page = scalar_load(table, key >> pg.page_shift);
           t.good[i] = page >= 0 && page < pg.num_pages;
           if (!t.good[i] && k0 + 16 * i + 16 > lo && lane == 0) flag(pg.status, DLRM_STATUS_BAD_PAGE);
           t.at[i] = (t.good[i] ? page : 0) * pg.page_stride + (key & page_mask & ~15) * D;
@@ -307,7 +314,7 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, Cut cut
 #pragma unroll
           for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) apart |= not_finite<DT>(v[j][i]);
+            for (int i = 0; i < E / 2; ++i) apart |= not_finite_halves<DT>(v[j][i]) != 0;
           apart = __ballot(apart) != 0;
         }
         for (int tok = apart ? tok0 : tok1; tok <= tok1; ++tok) {
@@ -361,7 +368,7 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, Cut cut
         constexpr int Pieces = D / 8;
         for (int i = threadIdx.x; i < 16 * Pieces; i += kThreads) {
           const int r16 = i / Pieces, at = i % Pieces * 8;
-          const long long row = row0 + rt * 16 + r16;
+          const int row = row0 + rt * 16 + r16;
           if (row >= row_end) continue;
           float mt = -INFINITY, lt = 0.f;
 #pragma unroll
@@ -378,7 +385,7 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, Cut cut
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) x[d] += lds_o[w][r16 * Pitch + at + d];
           }
-          const int tok = static_cast<int>(row / group), gi = static_cast<int>(row - static_cast<long long>(tok) * group);
+          const int tok = row / group, gi = row - tok * group;
           const long long to = static_cast<long long>(sq.first + tok) * a.q_heads + head * group + gi;
           if (rc.parts == 1) {
             finish<DT>(a, to, at, x, mt, lt);
@@ -390,6 +397,378 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, Cut cut
           }
         }
         __syncthreads();
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tile kernel: 128 rows of one head to a workgroup, 32 to a wave. Tiles of K entries go straight
+// from global memory to LDS (16 bytes a lane), one tile ahead, and every wave reads all of a tile.
+// The products are 32x32x16: the score of row lane % 32 with entries 8 i + 4 h + j (h = lane / 32,
+// i, j = 0 .. 3) lies in one lane, which again is the second product's right operand as it stands.
+// Its left operand V^T is read by the transposing LDS load: sixteen lanes take a block of 4 entries
+// x 16 elements and get one element of the 4 entries each.
+//
+// A row of D elements is D / 8 pieces of 16 bytes; piece c of entry r lies at place c ^ swizzle(r),
+// so that the lanes that LDS serves together fall on different banks. The copy to LDS writes places
+// in order and picks the piece for each.
+// ---------------------------------------------------------------------------
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <int DT>
+__device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f32x16& c) {
+  if constexpr (DT == DLRM_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+
+// Keys are read as rows (32 entries, the same piece): neighbours differ in every place bit.
+template <int D>
+__device__ __forceinline__ int key_swizzle(int r) {
+  return D == 32 ? r >> 1 & 3 : D == 64 ? r & 7 : r & 15;
+}
+// Values are read as blocks of 4 entries x 2 (or, with the neighbouring lanes, 4) pieces.
+template <int D>
+__device__ __forceinline__ int value_swizzle(int r) {
+  return D == 32 ? r & 2 : D == 64 ? (r & 1) << 2 | (r & 2) : (r & 1) << 2 | (r & 2) | (r & 2) << 2;
+}
+
+constexpr int kTileKeys = 64;
+
+// The larger of a lane and the one 32 away.
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// 16 bytes a lane from `from` + off to LDS: lane i's go to `to` + 16 i; from and to are the same in
+// every lane. Written out because after the builtin the compiler holds every LDS read back until the
+// copy has landed, also reads of the other tile. No register receives anything; the kernel itself waits
+// (wait_copies) before the barrier that publishes the tile.
+__device__ __forceinline__ void copy16(const char* from, uint32_t off, const uint16_t* to) {
+  const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+      (const __attribute__((address_space(3))) uint16_t*)to));
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(lds), "v"(off), "s"(from)
+      : "memory", "m0");
+}
+
+// Waits for this wave's copies to LDS; a barrier makes those of the other waves visible too.
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <int DT, int D>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(AttnArgs a, Cut cut) {
+  constexpr int K = kTileKeys;
+  constexpr int T = K / 32;          // score blocks of a tile
+  constexpr int Q = D / 16;          // steps of the first product
+  constexpr int C = D / 32;          // 32-wide pieces of O
+  constexpr int P = D / 8;           // pieces of a row
+  constexpr int Rows = 32 * kWaves;
+  constexpr int CopyRows = kWave / P;  // entries that a wave copies at once, 16 bytes a lane
+  constexpr int Copy = 16 / CopyRows;  // copies for the 16 entries that a wave brings of each tile
+  static_assert(K == 16 * kWaves, "a wave brings 16 entries, which lie in one page");
+  __shared__ __align__(16) uint16_t lds_k[2][K * D];
+  __shared__ __align__(16) uint16_t lds_v[2][K * D];
+  const int lane = threadIdx.x & (kWave - 1), h = lane >> 5, c32 = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int group = a.q_heads / a.kv_heads;
+  const float c = a.scale * kLog2e;
+  const Paged& pg = a.paged;
+  const int page_mask = (1 << pg.page_shift) - 1;
+  // what this lane copies: byte offsets in the 16 entries
+  uint32_t copy_k[Copy];
+#pragma unroll
+  for (int i = 0; i < Copy; ++i) {
+    const int r = i * CopyRows + lane / P;
+    copy_k[i] = 2 * (r * D + (lane % P ^ key_swizzle<D>(r)) * 8);
+  }
+  const uint32_t copy_v = 2 * (lane / P * D + (lane % P ^ value_swizzle<D>(lane / P)) * 8);
+  static_assert(CopyRows % 4 == 0 || D == 256, "the swizzle of values repeats after CopyRows entries");
+
+  for (long long unit = blockIdx.x; unit < cut.units; unit += gridDim.x) {
+    const int head = static_cast<int>(unit % a.kv_heads);
+    long long rest = unit / a.kv_heads;
+    const int split = static_cast<int>(rest % cut.splits);
+    rest /= cut.splits;
+    const int seq = static_cast<int>(rest / cut.q_tiles);
+    const Seq sq = load_seq(pg, a.n, seq);
+    const int rows = sq.tokens * group;
+    const uint16_t* kh = static_cast<const uint16_t*>(a.k_cache) + head * pg.head_stride;
+    const uint16_t* vh = static_cast<const uint16_t*>(a.v_cache) + head * pg.head_stride;
+    const int32_t* table = pg.page_table + seq * pg.table_stride;
+
+    for (long long first_row = rest % cut.q_tiles * Rows; first_row < rows;
+         first_row += static_cast<long long>(cut.q_tiles) * Rows) {
+      const int row0 = static_cast<int>(first_row), row_end = rows - row0 > Rows ? row0 + Rows : rows;
+      const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut);
+      if (split >= rc.parts) continue;
+      const int k_first = rc.first + split * rc.part;
+      const int hi = rc.hi < k_first + rc.part ? rc.hi : k_first + rc.part;
+      // what this wave's rows see: some of them [w_lo, w_hi), all of them [w_all_lo, w_all_hi)
+      const int w0 = row0 + 32 * wave, w1 = w0 + 32 < row_end ? w0 + 32 : row_end;
+      int tok0 = 0, tok1 = -1, w_lo = 0, w_hi = 0, w_all_lo = 0, w_all_hi = 0;
+      if (w0 < w1) {
+        tok0 = w0 / group;
+        tok1 = (w1 - 1) / group;
+        const Span s0 = seen_by(sq, tok0, a.causal, a.window), s1 = seen_by(sq, tok1, a.causal, a.window);
+        w_lo = s0.lo;
+        w_hi = s1.hi;
+        w_all_lo = s1.lo;
+        w_all_hi = s0.hi;
+      }
+      const int row = w0 + c32;
+      int row_lo = 0, row_hi = 0, row_tok = -1;
+      long long to = 0;  // row of the output
+      u32x4 qf[Q];
+#pragma unroll
+      for (int s = 0; s < Q; ++s) qf[s] = u32x4{0, 0, 0, 0};
+      if (row < w1) {
+        row_tok = row / group;
+        const int gi = row - row_tok * group;
+        const Span s = seen_by(sq, row_tok, a.causal, a.window);
+        row_lo = s.lo;
+        row_hi = s.hi;
+        to = static_cast<long long>(sq.first + row_tok) * a.q_heads + head * group + gi;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q.ptr) + (sq.first + row_tok) * a.q.stride +
+                            (head * group + gi) * a.q.head_stride + h * 8;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) qf[i] = *reinterpret_cast<const u32x4*>(q + i * 16);
+      }
+
+      float m = -INFINITY, l = 0.f;
+      f32x16 o[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
+
+      // Pages of the four 16-entry blocks of the tile at k0 (past the end: of the last entry).
+      struct Pages {
+        int of[4];
+      };
+      const auto look_up = [&](int k0) {
+        Pages p;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) p.of[t] = scalar_load(table, (k0 + 16 * t < hi ? k0 + 16 * t : hi - 1) >> pg.page_shift);
+        return p;
+      };
+      // Bit t: the page of block t is good.
+      const auto good_pages = [&](const Pages& p) {
+        int good = 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) good |= (p.of[t] >= 0 && p.of[t] < pg.num_pages ? 1 : 0) << t;
+        return good;
+      };
+      // Brings this wave's 16 entries of the tile at k0 to LDS. Past the end and in place of a bad page
+      // other entries of the cache are read, and masked.
+      const auto copy_tile = [&](int k0, const Pages& p, int buf) {
+        const int key = k0 + 16 * wave, known = key < hi ? key : hi - 1;
+        int page = wave == 0 ? p.of[0] : wave == 1 ? p.of[1] : wave == 2 ? p.of[2] : p.of[3];
+        if (page < 0 || page >= pg.num_pages) page = 0;
+        const long long at = page * pg.page_stride + (known & page_mask & ~15) * D;
+        const char* kp = reinterpret_cast<const char*>(kh + at);
+        const char* vp = reinterpret_cast<const char*>(vh + at);
+        const uint16_t* to_k = lds_k[buf] + 16 * wave * D;
+        const uint16_t* to_v = lds_v[buf] + 16 * wave * D;
+#pragma unroll
+        for (int i = 0; i < Copy; ++i) {
+          copy16(kp, copy_k[i], to_k + i * CopyRows * D);
+          const uint32_t off = D == 256 ? copy_v ^ (i & 1 ? 16u * (value_swizzle<D>(2) ^ value_swizzle<D>(0)) : 0u) : copy_v;
+          copy16(vp + i * CopyRows * D * 2, off, to_v + i * CopyRows * D);
+        }
+      };
+      constexpr int kAllGood = (1 << (K / 16)) - 1;
+
+      __syncthreads();  // the tiles of the rows before are no longer read
+      Pages pages, ahead;  // of the tile that is copied next, and of the one after it
+      int good_next = kAllGood;
+      if (k_first < hi) {
+        pages = look_up(k_first);
+        ahead = look_up(k_first + K < hi ? k_first + K : k_first);
+        copy_tile(k_first, pages, 0);
+        good_next = good_pages(pages);
+      }
+      for (int k0 = k_first, buf = 0; k0 < hi; k0 += K, buf ^= 1) {
+        wait_copies();
+        __syncthreads();  // this tile is in LDS, and the other one is no longer read
+        const int good = good_next;
+        if (k0 + K < hi) {
+          pages = ahead;
+          copy_tile(k0 + K, pages, buf ^ 1);
+          good_next = good_pages(pages);
+          ahead = look_up(k0 + 2 * K < hi ? k0 + 2 * K : k0);
+        }
+        if (good != kAllGood && threadIdx.x == 0) {
+          for (int t = 0; t < K / 16; ++t)
+            if (!(good >> t & 1) && k0 + 16 * t < hi && k0 + 16 * t + 16 > rc.lo) flag(pg.status, DLRM_STATUS_BAD_PAGE);
+        }
+        if (k0 >= w_hi || k0 + K <= w_lo) continue;  // nothing of the tile is seen by this wave's rows
+
+        f32x16 s[T];
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[t][r] = 0.f;
+#pragma unroll
+          for (int i = 0; i < Q; ++i) {
+            const int r = 32 * t + c32, place = (2 * i + h) ^ key_swizzle<D>(r);
+            const u32x4 kf = *reinterpret_cast<const u32x4*>(lds_k[buf] + r * D + place * 8);
+            s[t] = mfma32<DT>(kf, qf[i], s[t]);
+          }
+        }
+        const bool edge = k0 < w_all_lo || k0 + K > w_all_hi || k0 + K > hi || good != kAllGood;
+        if (edge) {
+#pragma unroll
+          for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int e = 32 * t + 8 * (r / 4) + 4 * h + r % 4, key = k0 + e;
+              if (key < row_lo || key >= row_hi || key >= hi || !(good >> (e / 16) & 1)) s[t][r] = -INFINITY;
+            }
+        }
+
+        float top = s[0][0];
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
+        top = max_halves(top);
+        const float next = fmaxf(m, top);
+        // O and l stay relative to an older maximum until a row's grows by 2^8: weights are then at most
+        // 2^8 (2^16 with the lift of fp16 would not fit, so there 2^7)
+        if (__any((next - m) * c > (DT == DLRM_F16 ? 7.f : 8.f))) {
+          const float keep = m == -INFINITY ? 0.f : exp2f((m - next) * c);
+          m = next;
+          l *= keep;
+#pragma unroll
+          for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[i][r] *= keep;
+        }
+        const float base = m == -INFINITY ? 0.f : m * c - kLift<DT>;
+        u32x4 pw[2 * T];
+        float sum = 0.f;
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; r += 2) {
+            const float p0 = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -base));
+            const float p1 = __builtin_amdgcn_exp2f(fmaf(s[t][r + 1], c, -base));
+            sum += p0 + p1;
+            pw[2 * t + r / 8][r % 8 / 2] = pack2<DT>(p0, p1);
+          }
+        l += sum;
+
+        // V^T of 16 entries (step) and 32 elements (piece): entries 4 h .. and 8 + 4 h .. of the step
+        const auto values = [&](int step, int piece) {
+          u32x4 w;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int r = 16 * step + 8 * n + 4 * h + (lane & 15) / 4;
+            const int place = (piece * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1)) ^ value_swizzle<D>(r);
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(lds_v[buf] + r * D + place * 8 + (lane & 1) * 4));
+            const uint2 u = __builtin_bit_cast(uint2, x);
+            w[2 * n] = u.x;
+            w[2 * n + 1] = u.y;
+          }
+          return w;
+        };
+        if (!edge) {
+#pragma unroll
+          for (int step = 0; step < K / 16; ++step)
+#pragma unroll
+            for (int i = 0; i < C; ++i) o[i] = mfma32<DT>(values(step, i), pw[step], o[i]);
+        } else {
+          // Entries that no row of the wave sees count as zero, whatever they hold. If one that only some
+          // rows see holds an infinity or NaN, it counts as zero in the product too, and is added after it
+          // to the rows that see it.
+          bool special = false;
+#pragma unroll
+          for (int step = 0; step < K / 16; ++step) {
+            uint32_t see[4];  // for the eight entries of a lane
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              see[j] = 0;
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const int key = k0 + 16 * step + 8 * (j / 2) + 4 * h + 2 * (j % 2) + b;
+                if (key >= w_lo && key < w_hi && key < hi && (good >> step & 1)) see[j] |= 0xffffu << (16 * b);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+              u32x4 w = values(step, i);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                w[j] &= see[j];
+                const uint32_t odd = not_finite_halves<DT>(w[j]);
+                special |= odd != 0;
+                w[j] &= ~odd;
+              }
+              o[i] = mfma32<DT>(w, pw[step], o[i]);
+            }
+          }
+          if (__any(special)) {
+#pragma unroll 1
+            for (int e = 0; e < K; ++e) {
+              const int key = k0 + e;
+              if (key >= hi || !(good >> (e / 16) & 1)) continue;
+              const bool mine = key >= row_lo && key < row_hi;
+#pragma unroll
+              for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const int place = (4 * i + q) ^ value_swizzle<D>(e);
+                  const uint2 w = *reinterpret_cast<const uint2*>(lds_v[buf] + e * D + place * 8 + 4 * h);
+                  const uint32_t u[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const float x = DT == DLRM_BF16 ? bf16_lo(u[j]) : f16_lo(u[j]);
+                    if (mine && not_finite_halves<DT>(u[j])) o[i][4 * q + j] += x;
+                  }
+                }
+            }
+          }
+        }
+      }
+
+      l = add_halves(l);
+      if (row < w1) {
+        const bool part = rc.parts > 1;
+        const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int at = 32 * i + 8 * q + 4 * h;
+            const float x0 = o[i][4 * q] * inv, x1 = o[i][4 * q + 1] * inv, x2 = o[i][4 * q + 2] * inv,
+                        x3 = o[i][4 * q + 3] * inv;
+            if (part)
+              *reinterpret_cast<float4*>(cut.o + (split * a.n * a.q_heads + to) * D + at) = make_float4(x0, x1, x2, x3);
+            else
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to * D + at) =
+                  make_uint2(pack2<DT>(x0, x1), pack2<DT>(x2, x3));
+          }
+        if (h == 0) {
+          if (part)
+            cut.ml[to * cut.splits + split] = make_float2(m, l);
+          else if (a.lse)
+            a.lse[to] = l == 0.f ? -INFINITY : fmaf(m, a.scale, logf(l) - kLift<DT> * kLn2);
+        }
       }
     }
   }
@@ -414,14 +793,14 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, Cut cut
     const int head = static_cast<int>(unit % a.kv_heads);
     const long long rest = unit / a.kv_heads;
     const Seq sq = load_seq(a.paged, a.n, static_cast<int>(rest / cut.q_tiles));
-    const long long rows = static_cast<long long>(sq.tokens) * group;
-    for (long long row0 = rest % cut.q_tiles * tile_rows; row0 < rows;
-         row0 += static_cast<long long>(cut.q_tiles) * tile_rows) {
-      const long long row_end = row0 + tile_rows < rows ? row0 + tile_rows : rows;
+    const int rows = sq.tokens * group;
+    for (long long first_row = rest % cut.q_tiles * tile_rows; first_row < rows;
+         first_row += static_cast<long long>(cut.q_tiles) * tile_rows) {
+      const int row0 = static_cast<int>(first_row), row_end = rows - row0 > tile_rows ? row0 + tile_rows : rows;
       const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut);
       if (rc.parts == 1) continue;
-      for (long long row = row0 + blockIdx.y; row < row_end; row += gridDim.y) {
-        const int tok = static_cast<int>(row / group), gi = static_cast<int>(row - static_cast<long long>(tok) * group);
+      for (int row = row0 + blockIdx.y; row < row_end; row += gridDim.y) {
+        const int tok = row / group, gi = row - tok * group;
         const long long to = static_cast<long long>(sq.first + tok) * a.q_heads + head * group + gi;
         const float2* ml = cut.ml + to * cut.splits;
         float m = -INFINITY;
@@ -472,26 +851,29 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, Cut cut
   }
 }
 
-// Sizes of a call's cut. A tile of one token's rows is bound by memory and its history is split into
-// parts of at least kPart entries until there are kWanted workgroups: 16 for each place on the chip, so
-// that histories of unequal length even out (64 histories of up to 16k entries: 270 us against 380 with
-// 2048; one of 131k: 33.6 us with parts of 1024, 35.3 with 512, 39.7 with 256).
+// Rows of a tile: 16 for the rows kernel (one wave's matrix instruction), 128 for the tile kernel.
+int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
+
+// A call with few tiles splits each one's history into parts of at least kPart entries until there are
+// kWanted workgroups: 16 for each place on the chip, so that histories of unequal length even out (64
+// histories of up to 16k entries: 270 us against 380 with 2048; one of 131k: 33.6 us with parts of 1024,
+// 35.3 with 512, 39.7 with 256).
 constexpr int kWanted = 8192, kPart = 1024;
 
-Cut cut_rows(int rows_per_tile, long long max_rows, int seqs, int kv_heads, int causal, int window, int max_q,
-             int max_kv) {
+Cut cut_call(long long max_rows, int seqs, int kv_heads, int causal, int window, int max_q, int max_kv) {
   Cut c;
-  const long long tiles = max_rows > rows_per_tile ? (max_rows + rows_per_tile - 1) / rows_per_tile : 1;
+  const int rows = tile_rows(max_rows);
+  const long long tiles = max_rows > rows ? (max_rows + rows - 1) / rows : 1;
   c.q_tiles = static_cast<int>(tiles);
   const long long whole = tiles * seqs * kv_heads;
   long long span = max_kv > 0 ? max_kv : 1;
   if (causal && window && span > static_cast<long long>(window) + max_q + 32) span = static_cast<long long>(window) + max_q + 32;
-  long long splits = tiles > 1 ? 1 : kWanted / (whole > 0 ? whole : 1);
+  long long splits = (rows == 16 ? kWanted : 512) / (whole > 0 ? whole : 1);
   const long long most = (span + kPart - 1) / kPart;
   splits = splits < 1 ? 1 : splits > most ? most : splits;
   if (splits > kMaxSplits) splits = kMaxSplits;
   c.splits = static_cast<int>(splits);
-  c.part = static_cast<int>(((span + splits - 1) / splits + 31) & ~31LL);
+  c.part = static_cast<int>(((span + splits - 1) / splits + 63) & ~63LL);
   c.units = whole * splits;
   c.o = nullptr;
   c.ml = nullptr;
@@ -508,29 +890,27 @@ size_t cut_bytes(const Cut& c, int64_t n, int q_heads, int dim) {
 
 constexpr long long kMaxGrid = 1 << 22;
 
-template <int DT, int D, int RT>
-hipError_t run_rows(const AttnArgs& a, hipStream_t s) {
+template <int DT, int D>
+hipError_t run(const AttnArgs& a, hipStream_t s) {
   const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
-  Cut cut = cut_rows(16 * RT, rows, a.paged.seqs, a.kv_heads, a.causal, a.window, a.max_q, a.max_kv);
+  Cut cut = cut_call(rows, a.paged.seqs, a.kv_heads, a.causal, a.window, a.max_q, a.max_kv);
   cut.o = static_cast<float*>(a.workspace);
   cut.ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) +
                                      round256(static_cast<size_t>(a.n) * a.q_heads * cut.splits * D * sizeof(float)));
-  hipLaunchKernelGGL((attn_rows_kernel<DT, D, RT>),
-                     dim3(static_cast<unsigned>(cut.units < kMaxGrid ? cut.units : kMaxGrid)), dim3(kThreads), 0, s, a,
-                     cut);
+  const dim3 grid(static_cast<unsigned>(cut.units < kMaxGrid ? cut.units : kMaxGrid));
+  const int tile = tile_rows(rows);
+  if (tile == 16)
+    hipLaunchKernelGGL((attn_rows_kernel<DT, D, 1>), grid, dim3(kThreads), 0, s, a, cut);
+  else
+    hipLaunchKernelGGL((attn_tile_kernel<DT, D>), grid, dim3(kThreads), 0, s, a, cut);
   if (cut.splits > 1) {
     const long long units = cut.units / cut.splits;
     hipLaunchKernelGGL((attn_join_kernel<DT, D>),
                        dim3(static_cast<unsigned>(units < kMaxGrid ? units : kMaxGrid),
-                            static_cast<unsigned>(rows < 1 ? 1 : rows < 16 * RT ? rows : 16 * RT)),
-                       dim3(kThreads), 0, s, a, cut, 16 * RT);
+                            static_cast<unsigned>(rows < 1 ? 1 : rows < tile ? rows : tile)),
+                       dim3(kThreads), 0, s, a, cut, tile);
   }
   return hipGetLastError();
-}
-
-template <int DT, int D>
-hipError_t run(const AttnArgs& a, hipStream_t s) {
-  return run_rows<DT, D, 1>(a, s);
 }
 
 template <int DT>
@@ -548,8 +928,8 @@ hipError_t run_dim(const AttnArgs& a, hipStream_t s) {
 size_t attn_workspace(int64_t n, int seqs, int q_heads, int kv_heads, int dim, int causal, int window, int max_q,
                       int max_kv) {
   if (n == 0 || seqs == 0) return 0;
-  return cut_bytes(cut_rows(16, static_cast<long long>(max_q) * (q_heads / kv_heads), seqs, kv_heads, causal, window,
-                            max_q, max_kv),
+  return cut_bytes(cut_call(static_cast<long long>(max_q) * (q_heads / kv_heads), seqs, kv_heads, causal, window, max_q,
+                            max_kv),
                    n, q_heads, dim);
 }
 
