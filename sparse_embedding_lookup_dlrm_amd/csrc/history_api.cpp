@@ -78,7 +78,7 @@ int check_paged(int64_t n, int32_t seqs, int32_t kv_heads, int32_t dim, int dtyp
   if (n > 0 && num_pages > 0 && (!k_cache || !v_cache)) return DLRM_E_INVAL;
   if (page < 16 || page > 65536 || (page & (page - 1))) return DLRM_E_UNSUPPORTED;
   // entries are counted in int32, with room for a tile past the last one
-  if (static_cast<int64_t>(table_width) * page > kI32Max - 65536) return DLRM_E_UNSUPPORTED;
+  if (static_cast<int64_t>(table_width) * page > kI32Max - (1 << 17)) return DLRM_E_UNSUPPORTED;
   const int64_t per16 = 16 / bytes_of(dtype);
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || page_stride % per16 || head_stride % per16) return DLRM_E_ALIGN;
   if (!aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(page_table, 4) || !aligned(status, 4))

@@ -450,24 +450,36 @@ __device__ __forceinline__ float add_halves(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// 16 bytes a lane from `from` + off to LDS: lane i's go to `to` + 16 i; from and to are the same in
-// every lane. Written out because after the builtin the compiler holds every LDS read back until the
-// copy has landed, also reads of the other tile. No register receives anything; the kernel itself waits
-// (wait_copies) before the barrier that publishes the tile.
-__device__ __forceinline__ void copy16(const char* from, uint32_t off, const uint16_t* to) {
+// N copies of 16 bytes a lane to LDS: copy i brings from `from` + off[i] + 1024 i, lane j's bytes to
+// `to` + 1024 i + 16 j; from and to are the same in every lane. Written out because after the builtin
+// the compiler holds every LDS read back until the copy has landed, also reads of the other tile. No
+// register receives anything; the kernel itself waits (wait_copies) before the barrier that publishes
+// the tile. The offset of the instruction counts on both sides.
+template <int N>
+__device__ __forceinline__ void copy16(const char* from, const uint32_t (&off)[N], const uint16_t* to) {
   const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
       (const __attribute__((address_space(3))) uint16_t*)to));
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %1, %2"
-      :
-      : "s"(lds), "v"(off), "s"(from)
-      : "memory", "m0");
+  if constexpr (N == 1)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :: "s"(lds), "v"(off[0]), "s"(from) : "memory", "m0");
+  else if constexpr (N == 2)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
+                 "global_load_lds_dwordx4 %2, %3 offset:1024"
+                 :: "s"(lds), "v"(off[0]), "v"(off[1]), "s"(from) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
+                 "global_load_lds_dwordx4 %2, %5 offset:1024\n\tglobal_load_lds_dwordx4 %3, %5 offset:2048\n\t"
+                 "global_load_lds_dwordx4 %4, %5 offset:3072"
+                 :: "s"(lds), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(from) : "memory", "m0");
 }
 
-// Waits for this wave's copies to LDS; a barrier makes those of the other waves visible too.
-__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Waits for this wave's copies to LDS (vmcnt 0, the other counts open); a barrier makes those of the
+// other waves visible too. The builtin tells the compiler that its own loads are in as well.
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+  asm volatile("" ::: "memory");
+}
 
 template <int DT, int D>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(AttnArgs a, Cut cut) {
@@ -488,15 +500,16 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
   const float c = a.scale * kLog2e;
   const Paged& pg = a.paged;
   const int page_mask = (1 << pg.page_shift) - 1;
-  // what this lane copies: byte offsets in the 16 entries
-  uint32_t copy_k[Copy];
+  // what this lane copies: byte offsets in the 16 entries, less the copy's own 1024 i. They repeat after
+  // four entries (values) or sixteen (keys).
+  constexpr int Group = Copy < 4 ? Copy : 4;
+  uint32_t copy_k[Copy / Group][Group], copy_v[Group];
 #pragma unroll
   for (int i = 0; i < Copy; ++i) {
     const int r = i * CopyRows + lane / P;
-    copy_k[i] = 2 * (r * D + (lane % P ^ key_swizzle<D>(r)) * 8);
+    copy_k[i / Group][i % Group] = 2 * (lane / P * D + (lane % P ^ key_swizzle<D>(r)) * 8);
+    if (i < Group) copy_v[i] = 2 * (lane / P * D + (lane % P ^ value_swizzle<D>(r)) * 8);
   }
-  const uint32_t copy_v = 2 * (lane / P * D + (lane % P ^ value_swizzle<D>(lane / P)) * 8);
-  static_assert(CopyRows % 4 == 0 || D == 256, "the swizzle of values repeats after CopyRows entries");
 
   for (long long unit = blockIdx.x; unit < cut.units; unit += gridDim.x) {
     const int head = static_cast<int>(unit % a.kv_heads);
@@ -555,82 +568,96 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
 
-      // Pages of the four 16-entry blocks of the tile at k0 (past the end: of the last entry).
-      struct Pages {
-        int of[4];
-      };
+      // Pages of 64 blocks of 16 entries (16 tiles) at a time, one to a lane, read 16 tiles ahead; past
+      // the end: of the last entry.
       const auto look_up = [&](int k0) {
-        Pages p;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) p.of[t] = scalar_load(table, (k0 + 16 * t < hi ? k0 + 16 * t : hi - 1) >> pg.page_shift);
-        return p;
+        const int key = k0 + 16 * lane;
+        return table[(key < hi ? key : hi - 1) >> pg.page_shift];
       };
-      // Bit t: the page of block t is good.
-      const auto good_pages = [&](const Pages& p) {
-        int good = 0;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) good |= (p.of[t] >= 0 && p.of[t] < pg.num_pages ? 1 : 0) << t;
-        return good;
+      // Bit i: the page of block i is good.
+      const auto good_pages = [&](int k0, int page) {
+        const bool good = static_cast<uint32_t>(page) < static_cast<uint32_t>(pg.num_pages);
+        if (!good && k0 + 16 * lane < hi && k0 + 16 * lane + 16 > rc.lo) flag(pg.status, DLRM_STATUS_BAD_PAGE);
+        return __ballot(good);
       };
-      // Brings this wave's 16 entries of the tile at k0 to LDS. Past the end and in place of a bad page
-      // other entries of the cache are read, and masked.
-      const auto copy_tile = [&](int k0, const Pages& p, int buf) {
+      // Brings this wave's 16 entries of the tile at k0, block 4 at + wave of the pages at hand, to LDS.
+      // Past the end and in place of a bad page other entries of the cache are read, and masked.
+      const auto copy_tile = [&](int k0, int pages, uint64_t good, int at, int buf) {
         const int key = k0 + 16 * wave, known = key < hi ? key : hi - 1;
-        int page = wave == 0 ? p.of[0] : wave == 1 ? p.of[1] : wave == 2 ? p.of[2] : p.of[3];
-        if (page < 0 || page >= pg.num_pages) page = 0;
-        const long long at = page * pg.page_stride + (known & page_mask & ~15) * D;
-        const char* kp = reinterpret_cast<const char*>(kh + at);
-        const char* vp = reinterpret_cast<const char*>(vh + at);
-        const uint16_t* to_k = lds_k[buf] + 16 * wave * D;
-        const uint16_t* to_v = lds_v[buf] + 16 * wave * D;
+        const int block = 4 * at + wave;
+        const int page = good >> block & 1 ? __builtin_amdgcn_readlane(pages, block) : 0;
+        const long long from = 2 * (page * pg.page_stride + (known & page_mask & ~15) * D);
+        const char* kp = reinterpret_cast<const char*>(kh) + from;
+        const char* vp = reinterpret_cast<const char*>(vh) + from;
 #pragma unroll
-        for (int i = 0; i < Copy; ++i) {
-          copy16(kp, copy_k[i], to_k + i * CopyRows * D);
-          const uint32_t off = D == 256 ? copy_v ^ (i & 1 ? 16u * (value_swizzle<D>(2) ^ value_swizzle<D>(0)) : 0u) : copy_v;
-          copy16(vp + i * CopyRows * D * 2, off, to_v + i * CopyRows * D);
+        for (int i = 0; i < Copy / Group; ++i) {
+          copy16(kp + i * 4096, copy_k[i], lds_k[buf] + 16 * wave * D + i * 2048);
+          copy16(vp + i * 4096, copy_v, lds_v[buf] + 16 * wave * D + i * 2048);
         }
       };
       constexpr int kAllGood = (1 << (K / 16)) - 1;
 
       __syncthreads();  // the tiles of the rows before are no longer read
-      Pages pages, ahead;  // of the tile that is copied next, and of the one after it
-      int good_next = kAllGood;
+      int pages = 0, pages_next = 0, at = 0, good_next = 0;
+      uint64_t good64 = 0;
       if (k_first < hi) {
         pages = look_up(k_first);
-        ahead = look_up(k_first + K < hi ? k_first + K : k_first);
-        copy_tile(k_first, pages, 0);
-        good_next = good_pages(pages);
+        pages_next = look_up(k_first + 16 * K < hi ? k_first + 16 * K : k_first);
+        good64 = good_pages(k_first, pages);
+        copy_tile(k_first, pages, good64, 0, 0);
+        good_next = static_cast<int>(good64) & kAllGood;
       }
       for (int k0 = k_first, buf = 0; k0 < hi; k0 += K, buf ^= 1) {
         wait_copies();
         __syncthreads();  // this tile is in LDS, and the other one is no longer read
         const int good = good_next;
         if (k0 + K < hi) {
-          pages = ahead;
-          copy_tile(k0 + K, pages, buf ^ 1);
-          good_next = good_pages(pages);
-          ahead = look_up(k0 + 2 * K < hi ? k0 + 2 * K : k0);
+          at = (at + 1) & 15;
+          if (at == 0) {
+            pages = pages_next;
+            good64 = good_pages(k0 + K, pages);
+            pages_next = look_up(k0 + 17 * K < hi ? k0 + 17 * K : k0);
+          }
+          copy_tile(k0 + K, pages, good64, at, buf ^ 1);
+          good_next = static_cast<int>(good64 >> (4 * at)) & kAllGood;
         }
-        if (good != kAllGood && threadIdx.x == 0) {
-          for (int t = 0; t < K / 16; ++t)
-            if (!(good >> t & 1) && k0 + 16 * t < hi && k0 + 16 * t + 16 > rc.lo) flag(pg.status, DLRM_STATUS_BAD_PAGE);
+        // A tile that some rows do not see whole: a value that is infinite or NaN would reach the rows that
+        // do not see it as 0 x inf, so it counts as zero in the product, and is added after it to the rows
+        // that see it.
+        bool special = false;
+        if (k0 < rc.all_lo || k0 + K > rc.all_hi || k0 + K > hi || good != kAllGood) {
+          bool found = false;
+#pragma unroll
+          for (int i = 0; i < K * P / kThreads; ++i) {
+            uint4* piece = reinterpret_cast<uint4*>(lds_v[buf]) + i * kThreads + threadIdx.x;
+            uint4 w = *piece;
+            const uint4 odd = make_uint4(not_finite_halves<DT>(w.x), not_finite_halves<DT>(w.y),
+                                         not_finite_halves<DT>(w.z), not_finite_halves<DT>(w.w));
+            if (odd.x | odd.y | odd.z | odd.w) {
+              *piece = make_uint4(w.x & ~odd.x, w.y & ~odd.y, w.z & ~odd.z, w.w & ~odd.w);
+              found = true;
+            }
+          }
+          special = __syncthreads_or(found) != 0;
         }
         if (k0 >= w_hi || k0 + K <= w_lo) continue;  // nothing of the tile is seen by this wave's rows
 
+        const auto key_frag = [&](int t, int i) {
+          const int r = 32 * t + c32, place = (2 * i + h) ^ key_swizzle<D>(r);
+          return *reinterpret_cast<const u32x4*>(lds_k[buf] + r * D + place * 8);
+        };
         f32x16 s[T];
 #pragma unroll
         for (int t = 0; t < T; ++t) {
+          u32x4 kf[Q];
+#pragma unroll
+          for (int i = 0; i < Q; ++i) kf[i] = key_frag(t, i);
 #pragma unroll
           for (int r = 0; r < 16; ++r) s[t][r] = 0.f;
 #pragma unroll
-          for (int i = 0; i < Q; ++i) {
-            const int r = 32 * t + c32, place = (2 * i + h) ^ key_swizzle<D>(r);
-            const u32x4 kf = *reinterpret_cast<const u32x4*>(lds_k[buf] + r * D + place * 8);
-            s[t] = mfma32<DT>(kf, qf[i], s[t]);
-          }
+          for (int i = 0; i < Q; ++i) s[t] = mfma32<DT>(kf[i], qf[i], s[t]);
         }
-        const bool edge = k0 < w_all_lo || k0 + K > w_all_hi || k0 + K > hi || good != kAllGood;
-        if (edge) {
+        if (k0 < w_all_lo || k0 + K > w_all_hi || k0 + K > hi || good != kAllGood) {
 #pragma unroll
           for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -648,7 +675,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
         top = max_halves(top);
         const float next = fmaxf(m, top);
         // O and l stay relative to an older maximum until a row's grows by 2^8: weights are then at most
-        // 2^8 (2^16 with the lift of fp16 would not fit, so there 2^7)
+        // 2^8 (fp16: 2^15 with its lift)
         if (__any((next - m) * c > (DT == DLRM_F16 ? 7.f : 8.f))) {
           const float keep = m == -INFINITY ? 0.f : exp2f((m - next) * c);
           m = next;
@@ -660,20 +687,21 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
         }
         const float base = m == -INFINITY ? 0.f : m * c - kLift<DT>;
         u32x4 pw[2 * T];
-        float sum = 0.f;
+        float sum[4] = {};
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
           for (int r = 0; r < 16; r += 2) {
             const float p0 = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -base));
             const float p1 = __builtin_amdgcn_exp2f(fmaf(s[t][r + 1], c, -base));
-            sum += p0 + p1;
+            sum[r % 4] += p0;
+            sum[r % 4 + 1] += p1;
             pw[2 * t + r / 8][r % 8 / 2] = pack2<DT>(p0, p1);
           }
-        l += sum;
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 
         // V^T of 16 entries (step) and 32 elements (piece): entries 4 h .. and 8 + 4 h .. of the step
-        const auto values = [&](int step, int piece) {
+        const auto value_frag = [&](int step, int piece) {
           u32x4 w;
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
@@ -687,60 +715,28 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
           }
           return w;
         };
-        if (!edge) {
 #pragma unroll
-          for (int step = 0; step < K / 16; ++step)
+        for (int step = 0; step < K / 16; ++step)
 #pragma unroll
-            for (int i = 0; i < C; ++i) o[i] = mfma32<DT>(values(step, i), pw[step], o[i]);
-        } else {
-          // Entries that no row of the wave sees count as zero, whatever they hold. If one that only some
-          // rows see holds an infinity or NaN, it counts as zero in the product too, and is added after it
-          // to the rows that see it.
-          bool special = false;
+          for (int i = 0; i < C; ++i) o[i] = mfma32<DT>(value_frag(step, i), pw[step], o[i]);
+
+        if (special) {
+#pragma unroll 1
+          for (int e = 0; e < K; ++e) {
+            const int key = k0 + e;
+            const int page = key < hi ? scalar_load(table, key >> pg.page_shift) : -1;
+            if (page < 0 || page >= pg.num_pages) continue;
+            const uint16_t* v = vh + page * pg.page_stride + static_cast<long long>(key & page_mask) * D + 4 * h;
+            const bool mine = key >= row_lo && key < row_hi;
 #pragma unroll
-          for (int step = 0; step < K / 16; ++step) {
-            uint32_t see[4];  // for the eight entries of a lane
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              see[j] = 0;
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const int key = k0 + 16 * step + 8 * (j / 2) + 4 * h + 2 * (j % 2) + b;
-                if (key >= w_lo && key < w_hi && key < hi && (good >> step & 1)) see[j] |= 0xffffu << (16 * b);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-              u32x4 w = values(step, i);
+            for (int i = 0; i < 4 * C; ++i) {
+              const uint2 w = *reinterpret_cast<const uint2*>(v + 8 * i);
+              const uint32_t u[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                w[j] &= see[j];
-                const uint32_t odd = not_finite_halves<DT>(w[j]);
-                special |= odd != 0;
-                w[j] &= ~odd;
+                const float x = DT == DLRM_BF16 ? bf16_lo(u[j]) : f16_lo(u[j]);
+                o[i / 4][4 * (i % 4) + j] += mine && not_finite_halves<DT>(u[j]) ? x : 0.f;
               }
-              o[i] = mfma32<DT>(w, pw[step], o[i]);
-            }
-          }
-          if (__any(special)) {
-#pragma unroll 1
-            for (int e = 0; e < K; ++e) {
-              const int key = k0 + e;
-              if (key >= hi || !(good >> (e / 16) & 1)) continue;
-              const bool mine = key >= row_lo && key < row_hi;
-#pragma unroll
-              for (int i = 0; i < C; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const int place = (4 * i + q) ^ value_swizzle<D>(e);
-                  const uint2 w = *reinterpret_cast<const uint2*>(lds_v[buf] + e * D + place * 8 + 4 * h);
-                  const uint32_t u[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const float x = DT == DLRM_BF16 ? bf16_lo(u[j]) : f16_lo(u[j]);
-                    if (mine && not_finite_halves<DT>(u[j])) o[i][4 * q + j] += x;
-                  }
-                }
             }
           }
         }
