@@ -481,12 +481,21 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("" ::: "memory");
 }
 
+// Heads of 256 elements take two waves for the same 32 rows, each with half of O: all of it beside the
+// queries would leave one wave to a SIMD, and nothing to run while it waits. Both form all scores.
+template <int D>
+constexpr int kHalves = D == 256 ? 2 : 1;
+template <int D>
+constexpr int kTileThreads = kThreads * kHalves<D>;
+
 template <int DT, int D>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(AttnArgs a, Cut cut) {
+__global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs a, Cut cut) {
   constexpr int K = kTileKeys;
-  constexpr int T = K / 32;          // score blocks of a tile
+  constexpr int T = D == 256 ? 1 : K / 32;  // 32-entry blocks of scores held at once
+  constexpr int Part = 32 * T;       // entries worked on at once
   constexpr int Q = D / 16;          // steps of the first product
-  constexpr int C = D / 32;          // 32-wide pieces of O
+  constexpr int H = kHalves<D>;
+  constexpr int C = D / 32 / H;      // 32-wide pieces of O
   constexpr int P = D / 8;           // pieces of a row
   constexpr int Rows = 32 * kWaves;
   constexpr int CopyRows = kWave / P;  // entries that a wave copies at once, 16 bytes a lane
@@ -494,8 +503,15 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
   static_assert(K == 16 * kWaves, "a wave brings 16 entries, which lie in one page");
   __shared__ __align__(16) uint16_t lds_k[2][K * D];
   __shared__ __align__(16) uint16_t lds_v[2][K * D];
+#ifdef WPRIO
+  if (__builtin_amdgcn_s_getreg(6148) & 1) __builtin_amdgcn_s_setprio(WPRIO);
+#endif
+#ifdef BPRIO
+  if ((blockIdx.x >> BPRIO) & 1) __builtin_amdgcn_s_setprio(2);
+#endif
   const int lane = threadIdx.x & (kWave - 1), h = lane >> 5, c32 = lane & 31;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave % kWaves);
+  const int half = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);  // of O
   const int group = a.q_heads / a.kv_heads;
   const float c = a.scale * kLog2e;
   const Paged& pg = a.paged;
@@ -591,8 +607,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
         const char* vp = reinterpret_cast<const char*>(vh) + from;
 #pragma unroll
         for (int i = 0; i < Copy / Group; ++i) {
-          copy16(kp + i * 4096, copy_k[i], lds_k[buf] + 16 * wave * D + i * 2048);
-          copy16(vp + i * 4096, copy_v, lds_v[buf] + 16 * wave * D + i * 2048);
+          if (H == 1 || half == 0) copy16(kp + i * 4096, copy_k[i], lds_k[buf] + 16 * wave * D + i * 2048);
+          if (H == 1 || half == 1) copy16(vp + i * 4096, copy_v, lds_v[buf] + 16 * wave * D + i * 2048);
         }
       };
       constexpr int kAllGood = (1 << (K / 16)) - 1;
@@ -628,8 +644,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
         if (k0 < rc.all_lo || k0 + K > rc.all_hi || k0 + K > hi || good != kAllGood) {
           bool found = false;
 #pragma unroll
-          for (int i = 0; i < K * P / kThreads; ++i) {
-            uint4* piece = reinterpret_cast<uint4*>(lds_v[buf]) + i * kThreads + threadIdx.x;
+          for (int i = 0; i < K * P / (kThreads * H); ++i) {
+            uint4* piece = reinterpret_cast<uint4*>(lds_v[buf]) + i * kThreads * H + threadIdx.x;
             uint4 w = *piece;
             const uint4 odd = make_uint4(not_finite_halves<DT>(w.x), not_finite_halves<DT>(w.y),
                                          not_finite_halves<DT>(w.z), not_finite_halves<DT>(w.w));
@@ -640,32 +656,59 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
           }
           special = __syncthreads_or(found) != 0;
         }
-        if (k0 >= w_hi || k0 + K <= w_lo) continue;  // nothing of the tile is seen by this wave's rows
 
+        constexpr int KW = Q < 8 ? Q : 8, VW = 2 * T * C < 8 ? 2 * T * C : 8;
+#pragma unroll 1
+        for (int p0 = 0; p0 < K; p0 += Part) {
+        if (k0 + p0 >= w_hi || k0 + p0 + Part <= w_lo) continue;  // this wave's rows see none of these entries
         const auto key_frag = [&](int t, int i) {
-          const int r = 32 * t + c32, place = (2 * i + h) ^ key_swizzle<D>(r);
+          const int r = p0 + 32 * t + c32, place = (2 * i + h) ^ key_swizzle<D>(r);
           return *reinterpret_cast<const u32x4*>(lds_k[buf] + r * D + place * 8);
         };
         f32x16 s[T];
+        // pieces of keys and values are read KW and VW ahead of the matrix unit
+        u32x4 kf[KW];
+#pragma unroll
+        for (int i = 0; i < KW; ++i) kf[i] = key_frag(i / Q, i % Q);
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-          u32x4 kf[Q];
-#pragma unroll
-          for (int i = 0; i < Q; ++i) kf[i] = key_frag(t, i);
 #pragma unroll
           for (int r = 0; r < 16; ++r) s[t][r] = 0.f;
 #pragma unroll
-          for (int i = 0; i < Q; ++i) s[t] = mfma32<DT>(kf[i], qf[i], s[t]);
+          for (int i = 0; i < Q; ++i) {
+            const int n = t * Q + i, ahead = n + KW;
+            s[t] = mfma32<DT>(kf[n % KW], qf[i], s[t]);
+            if (ahead < T * Q) kf[n % KW] = key_frag(ahead / Q, ahead % Q);
+          }
         }
-        if (k0 < w_all_lo || k0 + K > w_all_hi || k0 + K > hi || good != kAllGood) {
+        if (k0 + p0 < w_all_lo || k0 + p0 + Part > w_all_hi || k0 + p0 + Part > hi || good != kAllGood) {
 #pragma unroll
           for (int t = 0; t < T; ++t)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-              const int e = 32 * t + 8 * (r / 4) + 4 * h + r % 4, key = k0 + e;
+              const int e = p0 + 32 * t + 8 * (r / 4) + 4 * h + r % 4, key = k0 + e;
               if (key < row_lo || key >= row_hi || key >= hi || !(good >> (e / 16) & 1)) s[t][r] = -INFINITY;
             }
         }
+
+        // V^T of 16 entries (step) and 32 elements (piece): entries 4 h .. and 8 + 4 h .. of the step
+        const auto value_frag = [&](int step, int piece) {
+          u32x4 w;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int r = p0 + 16 * step + 8 * n + 4 * h + (lane & 15) / 4;
+            const int place = ((half * C + piece) * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1)) ^ value_swizzle<D>(r);
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(lds_v[buf] + r * D + place * 8 + (lane & 1) * 4));
+            const uint2 u = __builtin_bit_cast(uint2, x);
+            w[2 * n] = u.x;
+            w[2 * n + 1] = u.y;
+          }
+          return w;
+        };
+        u32x4 vf[VW];
+#pragma unroll
+        for (int i = 0; i < VW; ++i) vf[i] = value_frag(i / C, i % C);
 
         float top = s[0][0];
 #pragma unroll
@@ -700,25 +743,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
           }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 
-        // V^T of 16 entries (step) and 32 elements (piece): entries 4 h .. and 8 + 4 h .. of the step
-        const auto value_frag = [&](int step, int piece) {
-          u32x4 w;
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int r = 16 * step + 8 * n + 4 * h + (lane & 15) / 4;
-            const int place = (piece * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1)) ^ value_swizzle<D>(r);
-            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)(lds_v[buf] + r * D + place * 8 + (lane & 1) * 4));
-            const uint2 u = __builtin_bit_cast(uint2, x);
-            w[2 * n] = u.x;
-            w[2 * n + 1] = u.y;
-          }
-          return w;
-        };
-#pragma unroll
-        for (int step = 0; step < K / 16; ++step)
-#pragma unroll
-          for (int i = 0; i < C; ++i) o[i] = mfma32<DT>(value_frag(step, i), pw[step], o[i]);
+        for (int n = 0; n < 2 * T * C; ++n) {
+          o[n % C] = mfma32<DT>(vf[n % VW], pw[n / C], o[n % C]);
+          if (n + VW < 2 * T * C) vf[n % VW] = value_frag((n + VW) / C, (n + VW) % C);
+        }
+        }  // parts
 
         if (special) {
 #pragma unroll 1
@@ -726,7 +756,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
             const int key = k0 + e;
             const int page = key < hi ? scalar_load(table, key >> pg.page_shift) : -1;
             if (page < 0 || page >= pg.num_pages) continue;
-            const uint16_t* v = vh + page * pg.page_stride + static_cast<long long>(key & page_mask) * D + 4 * h;
+            const uint16_t* v = vh + page * pg.page_stride + static_cast<long long>(key & page_mask) * D + half * 32 * C + 4 * h;
             const bool mine = key >= row_lo && key < row_hi;
 #pragma unroll
             for (int i = 0; i < 4 * C; ++i) {
@@ -750,7 +780,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
         for (int i = 0; i < C; ++i)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int at = 32 * i + 8 * q + 4 * h;
+            const int at = half * 32 * C + 32 * i + 8 * q + 4 * h;
             const float x0 = o[i][4 * q] * inv, x1 = o[i][4 * q + 1] * inv, x2 = o[i][4 * q + 2] * inv,
                         x3 = o[i][4 * q + 3] * inv;
             if (part)
@@ -759,7 +789,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
               *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to * D + at) =
                   make_uint2(pack2<DT>(x0, x1), pack2<DT>(x2, x3));
           }
-        if (h == 0) {
+        if (h == 0 && half == 0) {
           if (part)
             cut.ml[to * cut.splits + split] = make_float2(m, l);
           else if (a.lse)
@@ -771,80 +801,82 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_kernel(A
 }
 
 // ---------------------------------------------------------------------------
-// Joins the parts of split histories: a workgroup to a row, D / 8 lanes to a part.
+// Joins the parts of split histories: D / 8 lanes to a row, eight elements each. Slots > 1: the parts of
+// a row are shared between that many groups of lanes (a workgroup to a row), which is quicker where
+// there are many parts and so few rows.
 // ---------------------------------------------------------------------------
 constexpr int kMaxSplits = 512;
 
-template <int DT, int D>
+template <int DT, int D, int Slots>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, Cut cut, int tile_rows) {
-  constexpr int Lanes = D / 8, Slots = kThreads / Lanes;
-  __shared__ float weight[kMaxSplits];
-  __shared__ float red[kWaves];
-  __shared__ float lds_o[kWaves][D];
+  constexpr int Lanes = D / 8, Rows = kThreads / (Lanes * Slots);
+  __shared__ float lds_x[Slots > 1 ? Slots : 1][D];
+  __shared__ float2 lds_ml[Slots];
   const int group = a.q_heads / a.kv_heads;
   const float c = a.scale * kLog2e;
-  const long long units = cut.units / cut.splits;
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int head = static_cast<int>(unit % a.kv_heads);
-    const long long rest = unit / a.kv_heads;
-    const Seq sq = load_seq(a.paged, a.n, static_cast<int>(rest / cut.q_tiles));
-    const int rows = sq.tokens * group;
-    for (long long first_row = rest % cut.q_tiles * tile_rows; first_row < rows;
-         first_row += static_cast<long long>(cut.q_tiles) * tile_rows) {
-      const int row0 = static_cast<int>(first_row), row_end = rows - row0 > tile_rows ? row0 + tile_rows : rows;
-      const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut);
+  const int at = threadIdx.x % Lanes * 8, slot = threadIdx.x / Lanes % Slots;
+  for (int seq = blockIdx.y; seq < a.paged.seqs; seq += gridDim.y) {
+    const Seq sq = load_seq(a.paged, a.n, seq);
+    const int rows = sq.tokens * a.q_heads;
+    for (long long first = static_cast<long long>(blockIdx.x) * Rows; first < rows;
+         first += static_cast<long long>(gridDim.x) * Rows) {
+      const int row = static_cast<int>(first) + threadIdx.x / (Lanes * Slots);
+      if (row >= rows) continue;  // with Slots > 1 there is one row, and no thread leaves it
+      const int tok = row / a.q_heads, in_head = tok * group + (row - tok * a.q_heads) % group;
+      const int row0 = in_head / tile_rows * tile_rows, in_all = sq.tokens * group;
+      const Reach rc(sq, row0, in_all - row0 > tile_rows ? row0 + tile_rows : in_all, group, a.causal, a.window, cut);
       if (rc.parts == 1) continue;
-      for (int row = row0 + blockIdx.y; row < row_end; row += gridDim.y) {
-        const int tok = row / group, gi = row - tok * group;
-        const long long to = static_cast<long long>(sq.first + tok) * a.q_heads + head * group + gi;
-        const float2* ml = cut.ml + to * cut.splits;
-        float m = -INFINITY;
-        for (int i = threadIdx.x; i < rc.parts; i += kThreads) m = fmaxf(m, ml[i].x);
-        for (int d = 1; d < kWave; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
-        if (lane == 0) red[wave] = m;
-        __syncthreads();
-        m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        float l = 0.f;
-        for (int i = threadIdx.x; i < rc.parts; i += kThreads) {
-          const float2 p = ml[i];
-          const float w = p.x == -INFINITY ? 0.f : exp2f((p.x - m) * c);
-          weight[i] = w;
-          l = fmaf(p.y, w, l);
-        }
-        for (int d = 1; d < kWave; d *= 2) l += __shfl_xor(l, d);
-        __syncthreads();  // red was read
-        if (lane == 0) red[wave] = l;
-        __syncthreads();
-        l = red[0] + red[1] + red[2] + red[3];
-        const int at = threadIdx.x % Lanes * 8;
-        float x[8] = {};
-        const long long step = a.n * a.q_heads * D;
-        const float* o = cut.o + to * D + at;
+      const long long to = static_cast<long long>(sq.first) * a.q_heads + row;
+      const float2* ml = cut.ml + to * cut.splits;
+      const float* o = cut.o + to * D + at;
+      const long long step = a.n * a.q_heads * D;
+      float m = -INFINITY, l = 0.f, x[8] = {};
 #pragma unroll 4
-        for (int i = threadIdx.x / Lanes; i < rc.parts; i += Slots) {
-          const float4 u = *reinterpret_cast<const float4*>(o + i * step);
-          const float4 v = *reinterpret_cast<const float4*>(o + i * step + 4);
-          const float w = weight[i];
-          x[0] = fmaf(u.x, w, x[0]); x[1] = fmaf(u.y, w, x[1]); x[2] = fmaf(u.z, w, x[2]); x[3] = fmaf(u.w, w, x[3]);
-          x[4] = fmaf(v.x, w, x[4]); x[5] = fmaf(v.y, w, x[5]); x[6] = fmaf(v.z, w, x[6]); x[7] = fmaf(v.w, w, x[7]);
-        }
+      for (int i = slot; i < rc.parts; i += Slots) m = fmaxf(m, ml[i].x);
+#pragma unroll 4
+      for (int i = slot; i < rc.parts; i += Slots) {
+        const float4 u = *reinterpret_cast<const float4*>(o + i * step);
+        const float4 v = *reinterpret_cast<const float4*>(o + i * step + 4);
+        const float2 p = ml[i];
+        const float w = p.x == -INFINITY ? 0.f : exp2f((p.x - m) * c);
+        l = fmaf(p.y, w, l);
+        x[0] = fmaf(u.x, w, x[0]); x[1] = fmaf(u.y, w, x[1]); x[2] = fmaf(u.z, w, x[2]); x[3] = fmaf(u.w, w, x[3]);
+        x[4] = fmaf(v.x, w, x[4]); x[5] = fmaf(v.y, w, x[5]); x[6] = fmaf(v.z, w, x[6]); x[7] = fmaf(v.w, w, x[7]);
+      }
+      if constexpr (Slots == 1) {
+        finish<DT>(a, to, at, x, m, l);
+      } else {
+        __syncthreads();  // the row before was read
 #pragma unroll
-        for (int d = 0; d < 8; ++d) {
-#pragma unroll
-          for (int s = Lanes; s < kWave; s *= 2) x[d] += __shfl_xor(x[d], s);
-          if (lane < Lanes) lds_o[wave][at + d] = x[d];
-        }
+        for (int d = 0; d < 8; ++d) lds_x[slot][at + d] = x[d];
+        if (at == 0) lds_ml[slot] = make_float2(m, l);
         __syncthreads();
-        if (threadIdx.x < Lanes) {
+        if (slot == 0) {
+          for (int i = 1; i < Slots; ++i) m = fmaxf(m, lds_ml[i].x);
+          l = 0.f;
 #pragma unroll
-          for (int d = 0; d < 8; ++d) x[d] = lds_o[0][at + d] + lds_o[1][at + d] + lds_o[2][at + d] + lds_o[3][at + d];
+          for (int d = 0; d < 8; ++d) x[d] = 0.f;
+          for (int i = 0; i < Slots; ++i) {
+            const float2 p = lds_ml[i];
+            const float w = p.x == -INFINITY ? 0.f : exp2f((p.x - m) * c);
+            l = fmaf(p.y, w, l);
+#pragma unroll
+            for (int d = 0; d < 8; ++d) x[d] = fmaf(lds_x[i][at + d], w, x[d]);
+          }
           finish<DT>(a, to, at, x, m, l);
         }
-        __syncthreads();
       }
     }
   }
+}
+
+template <int DT, int D, int Slots>
+void join(const AttnArgs& a, const Cut& cut, int tile_rows, hipStream_t s) {
+  constexpr int Rows = kThreads / (D / 8 * Slots);
+  const long long rows = static_cast<long long>(a.max_q) * a.q_heads, groups = (rows + Rows - 1) / Rows;
+  const unsigned x = static_cast<unsigned>(groups < 1 ? 1 : groups < 65535 ? groups : 65535);
+  const unsigned y = static_cast<unsigned>(a.paged.seqs < 65535 / 8 ? a.paged.seqs : 65535 / 8);
+  hipLaunchKernelGGL((attn_join_kernel<DT, D, Slots>), dim3(x, y), dim3(kThreads), 0, s, a, cut, tile_rows);
 }
 
 // Rows of a tile: 16 for the rows kernel (one wave's matrix instruction), 128 for the tile kernel.
@@ -864,8 +896,13 @@ Cut cut_call(long long max_rows, int seqs, int kv_heads, int causal, int window,
   const long long whole = tiles * seqs * kv_heads;
   long long span = max_kv > 0 ? max_kv : 1;
   if (causal && window && span > static_cast<long long>(window) + max_q + 32) span = static_cast<long long>(window) + max_q + 32;
-  long long splits = (rows == 16 ? kWanted : 512) / (whole > 0 ? whole : 1);
-  const long long most = (span + kPart - 1) / kPart;
+#ifndef TWANT
+#define TWANT 512
+#define TPART 1024
+#endif
+  const int least = rows == 16 ? kPart : TPART;
+  long long splits = (rows == 16 ? kWanted : TWANT) / (whole > 0 ? whole : 1);
+  const long long most = (span + least - 1) / least;
   splits = splits < 1 ? 1 : splits > most ? most : splits;
   if (splits > kMaxSplits) splits = kMaxSplits;
   c.splits = static_cast<int>(splits);
@@ -898,14 +935,11 @@ hipError_t run(const AttnArgs& a, hipStream_t s) {
   if (tile == 16)
     hipLaunchKernelGGL((attn_rows_kernel<DT, D, 1>), grid, dim3(kThreads), 0, s, a, cut);
   else
-    hipLaunchKernelGGL((attn_tile_kernel<DT, D>), grid, dim3(kThreads), 0, s, a, cut);
-  if (cut.splits > 1) {
-    const long long units = cut.units / cut.splits;
-    hipLaunchKernelGGL((attn_join_kernel<DT, D>),
-                       dim3(static_cast<unsigned>(units < kMaxGrid ? units : kMaxGrid),
-                            static_cast<unsigned>(rows < 1 ? 1 : rows < tile ? rows : tile)),
-                       dim3(kThreads), 0, s, a, cut, tile);
-  }
+    hipLaunchKernelGGL((attn_tile_kernel<DT, D>), grid, dim3(kTileThreads<D>), 0, s, a, cut);
+  if (cut.splits > 16)
+    join<DT, D, kThreads / (D / 8)>(a, cut, tile, s);
+  else if (cut.splits > 1)
+    join<DT, D, 1>(a, cut, tile, s);
   return hipGetLastError();
 }
 
