@@ -72,13 +72,13 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
-// Number of entries of off[0 .. count) that are <= x (off ascending), found by the whole wave:
-// each step splits the range into 64 parts with one load per lane, so 4096 sequences take two
-// loads in a row. Never reads outside off[0 .. count), also where off is not ascending.
+// Number of entries of off[0 .. count) that are <= x (off ascending), found by the whole wave: up to 256
+// entries are looked at at once, more in parts: each step splits the range into 64 with one load per
+// lane. Never reads outside off[0 .. count), also where off is not ascending.
 __device__ __forceinline__ int wave_upper_bound(const int32_t* __restrict__ off, int count, int x) {
   int lo = 0, len = count;  // entries before lo are <= x, entries from lo + len on are > x
   const int lane = threadIdx.x & (kWave - 1);
-  while (len > 0) {
+  while (len > 4 * kWave) {
     const int step = (len + kWave - 1) / kWave;
     const long long i = static_cast<long long>(lane) * step + step - 1;  // last entry of this lane's part
     const bool below = i < len && off[lo + i] <= x;
@@ -86,9 +86,13 @@ __device__ __forceinline__ int wave_upper_bound(const int32_t* __restrict__ off,
     const long long skip = static_cast<long long>(parts) * step;
     lo += static_cast<int>(skip);
     len = static_cast<int>(skip + step - 1 < len ? step - 1 : len - skip);
-    if (len < 0) len = 0;
   }
-  return lo;
+  int v[4], found = lo;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = lane + k * kWave < len ? off[lo + lane + k * kWave] : 0x7fffffff;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) found += __builtin_popcountll(__ballot(lane + k * kWave < len && v[k] <= x));
+  return found;
 }
 
 }  // namespace dlrm

@@ -96,14 +96,19 @@ struct Items {
   }
 };
 
-// One kind of head (queries, keys or values) of the workgroup's tokens. Without slots it goes to
+// One kind of head (queries, keys or values) of the workgroup's tokens. `before` shifts which group of
+// lanes begins: the keys begin where the queries ended, so that in a small call each kind has groups of
+// its own and waits for its loads beside the others. Without slots it goes to
 // out, contiguous [n][heads][D]; else to the cache: slots holds the element offset of each token's
 // slot in head 0 of its page, or -1 for a token that is not stored.
 template <int DT, int D, bool TURN>
 __device__ __forceinline__ void walk(const NormRopeArgs& a, const Heads& x, int heads, const float* w, long long t0,
-                                     int count, const float2* cs, void* out, const long long* slots) {
+                                     int count, const float2* cs, void* out, const long long* slots, int before) {
   using S = Split<DT, D>;
   constexpr int V = S::V;
+  if (heads == 0) return;
+  Items it((threadIdx.x / S::lanes + before) % S::groups, S::groups, heads);
+  if (it.t >= count) return;
   const int lane = threadIdx.x % S::lanes;
   const S split(lane, TURN ? a.rope.rot : 0, a.rope.interleaved);
   float wv[2 * V];
@@ -112,8 +117,7 @@ __device__ __forceinline__ void walk(const NormRopeArgs& a, const Heads& x, int 
     for (int i = 0; i < 2 * V; ++i) wv[i] = w[split.at[i / V] + i % V];
   }
   const int pairs = a.rope.rot / 2;
-  if (heads == 0) return;
-  for (Items it(threadIdx.x / S::lanes, S::groups, heads); it.t < count; it.next()) {
+  for (; it.t < count; it.next()) {
     const int t = it.t, h = it.h;
     const char* from = head_at<DT>(x, t0 + t, h);
     uint4 piece[2];
@@ -152,11 +156,12 @@ __device__ __forceinline__ void walk(const NormRopeArgs& a, const Heads& x, int 
 
 constexpr int kMaxTokens = 8;  // tokens of a workgroup
 
-// Cache slots of tokens t0 .. t0 + count, one wave each.
+// Cache slots of tokens t0 .. t0 + count, one wave each, the last wave first: the first ones have the
+// angles to form.
 template <int D>
 __device__ __forceinline__ void find_slots(const Paged& p, long long n, long long t0, int count, long long* slots) {
   const int lane = threadIdx.x & (kWave - 1);
-  for (int t = threadIdx.x / kWave; t < count; t += kThreads / kWave) {
+  for (int t = kThreads / kWave - 1 - threadIdx.x / kWave; t < count; t += kThreads / kWave) {
     const int token = static_cast<int>(t0) + t;
     const int seq = wave_upper_bound(p.q_offsets, p.seqs + 1, token) - 1;
     long long slot = -1;
@@ -191,12 +196,14 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(NormRopeArgs a, int
   angles(a.rope, t0, count, cs);
   if constexpr (APPEND) find_slots<D>(a.paged, a.n, t0, count, slots);
   __syncthreads();
-  walk<DT, D, true>(a, a.q, a.q_heads, a.w_q, t0, count, cs, a.q_out, nullptr);
+  constexpr int G = Split<DT, D>::groups;
+  const int after_q = G - count * a.q_heads % G, after_k = after_q + G - count * a.kv_heads % G;
+  walk<DT, D, true>(a, a.q, a.q_heads, a.w_q, t0, count, cs, a.q_out, nullptr, 0);
   if constexpr (APPEND) {
-    walk<DT, D, true>(a, a.k, a.kv_heads, a.w_k, t0, count, cs, a.k_cache, slots);
-    walk<DT, D, false>(a, a.v, a.kv_heads, nullptr, t0, count, cs, a.v_cache, slots);
+    walk<DT, D, true>(a, a.k, a.kv_heads, a.w_k, t0, count, cs, a.k_cache, slots, after_q);
+    walk<DT, D, false>(a, a.v, a.kv_heads, nullptr, t0, count, cs, a.v_cache, slots, after_k);
   } else {
-    walk<DT, D, true>(a, a.k, a.kv_heads, a.w_k, t0, count, cs, a.k_out, nullptr);
+    walk<DT, D, true>(a, a.k, a.kv_heads, a.w_k, t0, count, cs, a.k_out, nullptr, after_q);
   }
 }
 
@@ -299,20 +306,24 @@ __global__ __launch_bounds__(kThreads) void norm_rope_bwd_kernel(NormRopeBwdArgs
   }
 }
 
-// Columns of the partial weight gradients [rows][2 D] summed in a fixed order, in fp64: 32 columns
-// to a workgroup, eight threads to a column.
-__global__ __launch_bounds__(kThreads) void norm_rope_dw_kernel(const float* __restrict__ partials, int rows, int dim,
-                                                                float* d_w_q, float* d_w_k) {
-  __shared__ double lds[8][32];
-  const int col = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32;
+// Columns of the partial weight gradients [rows][2 D] summed in a fixed order, in fp64: 32 columns to a
+// workgroup, 32 threads to a column (1024 rows: 4 us; with eight threads and no loads ahead it was 38).
+constexpr int kDwThreads = 1024;
+__global__ __launch_bounds__(kDwThreads) void norm_rope_dw_kernel(const float* __restrict__ partials, int rows, int dim,
+                                                                  float* d_w_q, float* d_w_k) {
+  __shared__ double lds[kDwThreads / 32][33];
+  const int c = threadIdx.x % 32, col = blockIdx.x * 32 + c, part = threadIdx.x / 32;
   double sum = 0.;
-  for (int r = part; r < rows; r += 8) sum += partials[static_cast<long long>(r) * 2 * dim + col];
-  lds[part][threadIdx.x % 32] = sum;
+#pragma unroll 8
+  for (int r = part; r < rows; r += kDwThreads / 32) sum += partials[static_cast<long long>(r) * 2 * dim + col];
+  lds[part][c] = sum;
   __syncthreads();
-  if (part == 0) {
-    for (int i = 1; i < 8; ++i) sum += lds[i][threadIdx.x];
-    (col < dim ? d_w_q + col : d_w_k + (col - dim))[0] = static_cast<float>(sum);
-  }
+  // 32 lanes to a column
+  double v = lds[c][part];
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) v += __shfl_xor(v, m, 32);
+  const int to = blockIdx.x * 32 + part;
+  if (c == 0) (to < dim ? d_w_q + to : d_w_k + (to - dim))[0] = static_cast<float>(v);
 }
 
 // Tokens of a workgroup: as many as leave four workgroups to each CU, so that the angles of a
@@ -350,7 +361,7 @@ hipError_t run_bwd(const NormRopeBwdArgs& a, hipStream_t s) {
   const int groups = bwd_groups(a.n);
   if (groups > 0) hipLaunchKernelGGL((norm_rope_bwd_kernel<DT, D>), dim3(groups), dim3(kThreads), 0, s, a);
   if (a.w_q)
-    hipLaunchKernelGGL(norm_rope_dw_kernel, dim3(2 * D / 32), dim3(kThreads), 0, s, a.partials, groups, D, a.d_w_q,
+    hipLaunchKernelGGL(norm_rope_dw_kernel, dim3(2 * D / 32), dim3(kDwThreads), 0, s, a.partials, groups, D, a.d_w_q,
                        a.d_w_k);
   return hipGetLastError();
 }

@@ -503,12 +503,6 @@ __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs 
   static_assert(K == 16 * kWaves, "a wave brings 16 entries, which lie in one page");
   __shared__ __align__(16) uint16_t lds_k[2][K * D];
   __shared__ __align__(16) uint16_t lds_v[2][K * D];
-#ifdef WPRIO
-  if (__builtin_amdgcn_s_getreg(6148) & 1) __builtin_amdgcn_s_setprio(WPRIO);
-#endif
-#ifdef BPRIO
-  if ((blockIdx.x >> BPRIO) & 1) __builtin_amdgcn_s_setprio(2);
-#endif
   const int lane = threadIdx.x & (kWave - 1), h = lane >> 5, c32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave % kWaves);
   const int half = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);  // of O
@@ -539,7 +533,8 @@ __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs 
     const uint16_t* vh = static_cast<const uint16_t*>(a.v_cache) + head * pg.head_stride;
     const int32_t* table = pg.page_table + seq * pg.table_stride;
 
-    for (long long first_row = rest % cut.q_tiles * Rows; first_row < rows;
+    // the last rows of a causal chunk see the most: they start first
+    for (long long first_row = (cut.q_tiles - 1 - rest % cut.q_tiles) * Rows; first_row < rows;
          first_row += static_cast<long long>(cut.q_tiles) * Rows) {
       const int row0 = static_cast<int>(first_row), row_end = rows - row0 > Rows ? row0 + Rows : rows;
       const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut);
@@ -882,13 +877,15 @@ void join(const AttnArgs& a, const Cut& cut, int tile_rows, hipStream_t s) {
 // Rows of a tile: 16 for the rows kernel (one wave's matrix instruction), 128 for the tile kernel.
 int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
 
-// A call with few tiles splits each one's history into parts of at least kPart entries until there are
-// kWanted workgroups: 16 for each place on the chip, so that histories of unequal length even out (64
-// histories of up to 16k entries: 270 us against 380 with 2048; one of 131k: 33.6 us with parts of 1024,
-// 35.3 with 512, 39.7 with 256).
-constexpr int kWanted = 8192, kPart = 1024;
-
-Cut cut_call(long long max_rows, int seqs, int kv_heads, int causal, int window, int max_q, int max_kv) {
+// Where the workgroups of a call would not fill the chip, every history is split into parts of at least
+// `least` entries until there are `wanted` workgroups.
+// Rows kernel: 16 for each place on the chip, so that histories of unequal length even out (64 histories
+// of up to 16k entries: 241 us against 330 with 2048; one of 131k: 33 us with parts of 1024, 35 with 512,
+// 40 with 256).
+// Tile kernel: as many as there are places. 24 sequences of up to 257 x 1500, 288 workgroups: 25.5 us
+// against 29 unsplit; 432 workgroups of 256-wide heads, one to a CU: 86 us unsplit against 118 in two
+// parts, since the parts wait for a place and their sums are written and read.
+Cut cut_call(long long max_rows, int seqs, int kv_heads, int dim, int causal, int window, int max_q, int max_kv) {
   Cut c;
   const int rows = tile_rows(max_rows);
   const long long tiles = max_rows > rows ? (max_rows + rows - 1) / rows : 1;
@@ -896,12 +893,9 @@ Cut cut_call(long long max_rows, int seqs, int kv_heads, int causal, int window,
   const long long whole = tiles * seqs * kv_heads;
   long long span = max_kv > 0 ? max_kv : 1;
   if (causal && window && span > static_cast<long long>(window) + max_q + 32) span = static_cast<long long>(window) + max_q + 32;
-#ifndef TWANT
-#define TWANT 512
-#define TPART 1024
-#endif
-  const int least = rows == 16 ? kPart : TPART;
-  long long splits = (rows == 16 ? kWanted : TWANT) / (whole > 0 ? whole : 1);
+  const int wanted = rows == 16 ? 8192 : dim == 256 ? 256 : dim == 128 ? 512 : 768;
+  const int least = rows == 16 ? 1024 : 512;
+  long long splits = wanted / (whole > 0 ? whole : 1);
   const long long most = (span + least - 1) / least;
   splits = splits < 1 ? 1 : splits > most ? most : splits;
   if (splits > kMaxSplits) splits = kMaxSplits;
@@ -926,7 +920,7 @@ constexpr long long kMaxGrid = 1 << 22;
 template <int DT, int D>
 hipError_t run(const AttnArgs& a, hipStream_t s) {
   const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
-  Cut cut = cut_call(rows, a.paged.seqs, a.kv_heads, a.causal, a.window, a.max_q, a.max_kv);
+  Cut cut = cut_call(rows, a.paged.seqs, a.kv_heads, D, a.causal, a.window, a.max_q, a.max_kv);
   cut.o = static_cast<float*>(a.workspace);
   cut.ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) +
                                      round256(static_cast<size_t>(a.n) * a.q_heads * cut.splits * D * sizeof(float)));
@@ -958,7 +952,7 @@ hipError_t run_dim(const AttnArgs& a, hipStream_t s) {
 size_t attn_workspace(int64_t n, int seqs, int q_heads, int kv_heads, int dim, int causal, int window, int max_q,
                       int max_kv) {
   if (n == 0 || seqs == 0) return 0;
-  return cut_bytes(cut_call(static_cast<long long>(max_q) * (q_heads / kv_heads), seqs, kv_heads, causal, window, max_q,
+  return cut_bytes(cut_call(static_cast<long long>(max_q) * (q_heads / kv_heads), seqs, kv_heads, dim, causal, window, max_q,
                             max_kv),
                    n, q_heads, dim);
 }

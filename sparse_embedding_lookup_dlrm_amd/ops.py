@@ -9,6 +9,7 @@ cannot be loaded, every call raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import List, Optional, Sequence, Tuple
@@ -648,20 +649,24 @@ class _on:
     """The device and stream a call works on: buffers made within belong to that stream, so that one
     freed on return is not handed out again before the stream has passed the call."""
 
+    __slots__ = ("_outer", "_raw")
+
     def __init__(self, device: torch.device, stream):
         if device.type != "cuda":
             raise ValueError("device tensors must be CUDA (HIP) tensors")
         self._outer = None
         if stream is not None:
             self._outer = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self._outer = torch.cuda.device(device)
-        self._stream = stream
+            self._raw = stream.cuda_stream
+        else:
+            if torch.cuda.current_device() != device.index:
+                self._outer = torch.cuda.device(device)
+            self._raw = torch._C._cuda_getCurrentRawStream(device.index)
 
     def __enter__(self) -> int:
         if self._outer is not None:
             self._outer.__enter__()
-        return (torch.cuda.current_stream() if self._stream is None else self._stream).cuda_stream
+        return self._raw
 
     def __exit__(self, *exc):
         if self._outer is not None:
@@ -799,6 +804,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     return q_out
 
 
+@functools.lru_cache(maxsize=1024)
 def paged_attn_workspace_bytes(N: int, S: int, Hq: int, Hk: int, D: int, causal: bool, window: int, max_q: int,
                                max_kv: int) -> int:
     out = _size_t(0)
