@@ -98,61 +98,82 @@ struct Items {
 
 // One kind of head (queries, keys or values) of the workgroup's tokens. `before` shifts which group of
 // lanes begins: the keys begin where the queries ended, so that in a small call each kind has groups of
-// its own and waits for its loads beside the others. Without slots it goes to
-// out, contiguous [n][heads][D]; else to the cache: slots holds the element offset of each token's
-// slot in head 0 of its page, or -1 for a token that is not stored.
+// its own. The first item and the weights are asked for when the walk is made, before the workgroup has
+// its angles and slots, and every further item while the one before it is worked on.
 template <int DT, int D, bool TURN>
-__device__ __forceinline__ void walk(const NormRopeArgs& a, const Heads& x, int heads, const float* w, long long t0,
-                                     int count, const float2* cs, void* out, const long long* slots, int before) {
+struct Walk {
   using S = Split<DT, D>;
-  constexpr int V = S::V;
-  if (heads == 0) return;
-  Items it((threadIdx.x / S::lanes + before) % S::groups, S::groups, heads);
-  if (it.t >= count) return;
-  const int lane = threadIdx.x % S::lanes;
-  const S split(lane, TURN ? a.rope.rot : 0, a.rope.interleaved);
-  float wv[2 * V];
-  if (w) {
-#pragma unroll
-    for (int i = 0; i < 2 * V; ++i) wv[i] = w[split.at[i / V] + i % V];
-  }
-  const int pairs = a.rope.rot / 2;
-  for (; it.t < count; it.next()) {
-    const int t = it.t, h = it.h;
+  static constexpr int V = S::V;
+  const Heads x;
+  const int heads, count;
+  const long long t0;
+  Items it;
+  const int lane;
+  const S split;
+  const bool norm;
+  float wv[TURN ? 2 * V : 1];
+  uint4 piece[2];
+
+  __device__ __forceinline__ void load(int t, int h) {
     const char* from = head_at<DT>(x, t0 + t, h);
-    uint4 piece[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      piece[i] = *reinterpret_cast<const uint4*>(from + split.at[i] * Storage<DT>::bytes);
-    if constexpr (TURN) {
-      float y[2 * V];
-      widen<DT>(piece[0], y);
-      widen<DT>(piece[1], y + V);
-      if (w) {
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2 * V; ++i) sum = fmaf(y[i], y[i], sum);
-        sum = group_sum<S::lanes>(sum);
-        const float r = rsqrtf(sum * (1.f / D) + a.eps);
-#pragma unroll
-        for (int i = 0; i < 2 * V; ++i) y[i] = y[i] * r * wv[i];
-      }
-      if (split.rotated) rotate<V>(y, cs + t * pairs + lane * V, a.rope.interleaved, 1.f);
-      piece[0] = narrow<DT>(y);
-      piece[1] = narrow<DT>(y + V);
-    }
-    char* to;
-    if (slots) {
-      const long long slot = slots[t];
-      if (slot < 0) continue;
-      to = static_cast<char*>(out) + (slot + h * a.paged.head_stride) * Storage<DT>::bytes;
-    } else {
-      to = static_cast<char*>(out) + ((t0 + t) * heads + h) * D * Storage<DT>::bytes;
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(to + split.at[i] * Storage<DT>::bytes) = piece[i];
+    for (int i = 0; i < 2; ++i) piece[i] = *reinterpret_cast<const uint4*>(from + split.at[i] * Storage<DT>::bytes);
   }
-}
+
+  __device__ __forceinline__ Walk(const NormRopeArgs& a, const Heads& x_, int heads_, const float* w, long long t0_,
+                                  int count_, int before)
+      : x(x_), heads(heads_), count(heads_ ? count_ : 0), t0(t0_),
+        it((threadIdx.x / S::lanes + before) % S::groups, S::groups, heads_ ? heads_ : 1), lane(threadIdx.x % S::lanes),
+        split(lane, TURN ? a.rope.rot : 0, a.rope.interleaved), norm(w != nullptr) {
+    if (it.t >= count) return;
+    load(it.t, it.h);
+    if constexpr (TURN) {
+      if (norm) {
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) wv[i] = w[split.at[i / V] + i % V];
+      }
+    }
+  }
+
+  // Without slots the result goes to out, contiguous [n][heads][D]; else to the cache: slots holds the
+  // element offset of each token's slot in head 0 of its page, or -1 for a token that is not stored.
+  __device__ __forceinline__ void run(const NormRopeArgs& a, const float2* cs, void* out, const long long* slots) {
+    const int pairs = a.rope.rot / 2;
+    while (it.t < count) {
+      const int t = it.t, h = it.h;
+      uint4 now[2] = {piece[0], piece[1]};
+      it.next();
+      if (it.t < count) load(it.t, it.h);
+      if constexpr (TURN) {
+        float y[2 * V];
+        widen<DT>(now[0], y);
+        widen<DT>(now[1], y + V);
+        if (norm) {
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 2 * V; ++i) sum = fmaf(y[i], y[i], sum);
+          sum = group_sum<S::lanes>(sum);
+          const float r = rsqrtf(sum * (1.f / D) + a.eps);
+#pragma unroll
+          for (int i = 0; i < 2 * V; ++i) y[i] = y[i] * r * wv[i];
+        }
+        if (split.rotated) rotate<V>(y, cs + t * pairs + lane * V, a.rope.interleaved, 1.f);
+        now[0] = narrow<DT>(y);
+        now[1] = narrow<DT>(y + V);
+      }
+      char* to;
+      if (slots) {
+        const long long slot = slots[t];
+        if (slot < 0) continue;
+        to = static_cast<char*>(out) + (slot + h * a.paged.head_stride) * Storage<DT>::bytes;
+      } else {
+        to = static_cast<char*>(out) + ((t0 + t) * heads + h) * D * Storage<DT>::bytes;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(to + split.at[i] * Storage<DT>::bytes) = now[i];
+    }
+  }
+};
 
 constexpr int kMaxTokens = 8;  // tokens of a workgroup
 
@@ -193,17 +214,23 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(NormRopeArgs a, int
   __shared__ long long slots[APPEND ? kMaxTokens : 1];
   const long long t0 = static_cast<long long>(blockIdx.x) * per_group;
   const int count = static_cast<int>(a.n - t0 < per_group ? a.n - t0 : per_group);
-  angles(a.rope, t0, count, cs);
-  if constexpr (APPEND) find_slots<D>(a.paged, a.n, t0, count, slots);
-  __syncthreads();
   constexpr int G = Split<DT, D>::groups;
   const int after_q = G - count * a.q_heads % G, after_k = after_q + G - count * a.kv_heads % G;
-  walk<DT, D, true>(a, a.q, a.q_heads, a.w_q, t0, count, cs, a.q_out, nullptr, 0);
+  Walk<DT, D, true> q(a, a.q, a.q_heads, a.w_q, t0, count, 0);
+  Walk<DT, D, true> k(a, a.k, a.kv_heads, a.w_k, t0, count, after_q);
   if constexpr (APPEND) {
-    walk<DT, D, true>(a, a.k, a.kv_heads, a.w_k, t0, count, cs, a.k_cache, slots, after_q);
-    walk<DT, D, false>(a, a.v, a.kv_heads, nullptr, t0, count, cs, a.v_cache, slots, after_k);
+    Walk<DT, D, false> v(a, a.v, a.kv_heads, nullptr, t0, count, after_k);
+    angles(a.rope, t0, count, cs);
+    find_slots<D>(a.paged, a.n, t0, count, slots);
+    __syncthreads();
+    q.run(a, cs, a.q_out, nullptr);
+    k.run(a, cs, a.k_cache, slots);
+    v.run(a, cs, a.v_cache, slots);
   } else {
-    walk<DT, D, true>(a, a.k, a.kv_heads, a.w_k, t0, count, cs, a.k_out, nullptr, after_q);
+    angles(a.rope, t0, count, cs);
+    __syncthreads();
+    q.run(a, cs, a.q_out, nullptr);
+    k.run(a, cs, a.k_out, nullptr);
   }
 }
 
