@@ -579,70 +579,79 @@ class BwdPlan:
 # Attention over user histories (include/dlrm_history.h).
 
 
-def _heads_of(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None, heads: Optional[int] = None):
-    """Checks a tensor of heads [tokens, heads, dim], the elements of a head contiguous; like: the tensor
-    whose tokens, dim, dtype and device it has to share. Returns its address and strides."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(t.shape)}")
+# The checks of these calls cost more host time than a small launch takes on the GPU, so they read each
+# property of a tensor once and compare devices by number (-1: a host tensor).
+_I32_ARRAY = [_i32 * n for n in range(MAX_AXES + 1)]
+
+
+def _heads_of(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None, shape=None,
+              heads: Optional[int] = None):
+    """Checks a tensor of heads [tokens, heads, dim], the elements of a head contiguous; like, shape: the
+    tensor whose tokens, dim, dtype and device it has to share, and its shape. Returns its shape, and its
+    address and strides."""
+    own = t.shape
+    if len(own) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(own)}")
     if like is None:
         if t.dtype not in _TORCH_DT:
             raise ValueError(f"unsupported dtype {t.dtype} of {name}")
     else:
         if t.dtype != like.dtype:
             raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
-        if t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]:
-            raise ValueError(f"{name} is {tuple(t.shape)}, needs [{like.shape[0]}, heads, {like.shape[2]}]")
-        if t.device != like.device:
+        if own[0] != shape[0] or own[2] != shape[2]:
+            raise ValueError(f"{name} is {tuple(own)}, needs [{shape[0]}, heads, {shape[2]}]")
+        if t.get_device() != like.get_device():
             raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    if heads is not None and t.shape[1] != heads:
-        raise ValueError(f"{name} has {t.shape[1]} heads, needs {heads}")
+    if heads is not None and own[1] != heads:
+        raise ValueError(f"{name} has {own[1]} heads, needs {heads}")
     a, b, c = t.stride()
-    if c != 1 and t.shape[2] != 1:
+    if c != 1 and own[2] != 1:
         raise ValueError(f"the elements of a head of {name} must be contiguous")
-    return t.data_ptr(), a, b
+    return own, (t.data_ptr(), a, b)
 
 
-def _same_device(like: torch.Tensor, **ts) -> None:
-    dev = like.device
-    for name, t in ts.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _plain(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: int, dev: int, at_least: bool = False):
+    """Checks a contiguous tensor's dtype, size and device; returns its address, None for None."""
+    if t is None:
+        return None
+    n = t.numel()
+    if t.dtype != dtype or ((n < numel) if at_least else (n != numel)):
+        _expect(t, name, dtype, numel, at_least)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on device {dev}")
+    return t.data_ptr()
 
 
-def _contiguous(**ts) -> None:
-    for name, t in ts.items():
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-
-
-def _turn_args(like, positions, inv_freq, w_q, w_k, eps, sections, interleaved, tokens: int, dim: int):
+def _turn_args(dev, positions, inv_freq, w_q, w_k, eps, sections, interleaved, tokens: int, dim: int):
     """rot, and the arguments from positions to interleaved."""
     if inv_freq is None:
         rot, pos, stride, axes, secs, freq = 0, None, 0, 0, None, None
     else:
-        rot = 2 * inv_freq.numel()
-        _expect(inv_freq, "inv_freq", torch.float32, rot // 2)
+        half = inv_freq.numel()
+        rot, freq = 2 * half, _plain(inv_freq, "inv_freq", torch.float32, half, dev)
         if positions is None or positions.dtype != torch.int32 or positions.dim() not in (1, 2):
             raise ValueError("positions must be torch.int32 [tokens] or [axes, tokens]")
-        axes = positions.shape[0] if positions.dim() == 2 else 1
-        if positions.shape[-1] != tokens or (tokens > 1 and positions.stride(-1) != 1):
+        shape, strides = positions.shape, positions.stride()
+        axes, stride = (shape[0], strides[0]) if len(shape) == 2 else (1, 0)
+        if shape[-1] != tokens or (tokens > 1 and strides[-1] != 1):
             raise ValueError(f"positions must be [axes, {tokens}] with the tokens contiguous, got "
-                             f"{tuple(positions.shape)} with strides {positions.stride()}")
+                             f"{tuple(shape)} with strides {strides}")
+        if positions.get_device() != dev:
+            raise ValueError(f"positions is on {positions.device}, not on device {dev}")
         if sections is None:
             if axes != 1:
                 raise ValueError("sections are needed with more than one axis of positions")
-            sections = (rot // 2,)
+            sections = (half,)
         if len(sections) != axes:
             raise ValueError(f"{len(sections)} sections for {axes} axes of positions")
-        stride = positions.stride(0) if positions.dim() == 2 else 0
-        secs, pos, freq = (_i32 * axes)(*sections), positions.data_ptr(), inv_freq.data_ptr()
+        secs = (_I32_ARRAY[axes] if axes <= MAX_AXES else _i32 * axes)(*sections)
+        pos = positions.data_ptr()
     if (w_q is None) != (w_k is None):
         raise ValueError("w_q and w_k come together")
-    _expect(w_q, "w_q", torch.float32, dim)
-    _expect(w_k, "w_k", torch.float32, dim)
-    _contiguous(inv_freq=inv_freq, w_q=w_q, w_k=w_k)
-    _same_device(like, positions=positions, inv_freq=inv_freq, w_q=w_q, w_k=w_k)
-    return rot, (pos, stride, axes, secs, freq, _ptr(w_q), _ptr(w_k), eps, 1 if interleaved else 0)
+    return rot, (pos, stride, axes, secs, freq, _plain(w_q, "w_q", torch.float32, dim, dev),
+                 _plain(w_k, "w_k", torch.float32, dim, dev), eps, 1 if interleaved else 0)
 
 
 class _on:
@@ -681,23 +690,29 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
     """Norm of each head of q [N, Hq, D] and k [N, Hk, D] (with w_q, w_k fp32 [D]) and the position
     rotation of its first 2 * len(inv_freq) elements (dlrm_qk_norm_rope); returns contiguous (q, k).
     positions is int32 [N] or, with `sections` pairs to each axis, [axes, N]; inv_freq None: no rotation."""
-    N, Hq, D = q.shape if q.dim() == 3 else (0, 0, 0)
-    qa = _heads_of(q, "q")
-    ka = _heads_of(k, "k", like=q)
-    Hk = k.shape[1]
-    rot, turn = _turn_args(q, positions, inv_freq, w_q, w_k, eps, sections, interleaved, N, D)
-    _expect(q_out, "q_out", q.dtype, N * Hq * D)
-    _expect(k_out, "k_out", q.dtype, N * Hk * D)
-    _contiguous(q_out=q_out, k_out=k_out)
-    _same_device(q, q_out=q_out, k_out=k_out)
-    with _on(q.device, stream) as s:
+    shape, qa = _heads_of(q, "q")
+    (_, Hk, _), ka = _heads_of(k, "k", q, shape)
+    N, Hq, D = shape
+    dt, dev, where = q.dtype, q.get_device(), q.device
+    rot, turn = _turn_args(dev, positions, inv_freq, w_q, w_k, eps, sections, interleaved, N, D)
+    _plain(q_out, "q_out", dt, N * Hq * D, dev)
+    _plain(k_out, "k_out", dt, N * Hk * D, dev)
+    with _on(where, stream) as s:
         if q_out is None:
-            q_out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
+            q_out = torch.empty(shape, dtype=dt, device=where)
         if k_out is None:
-            k_out = torch.empty((N, Hk, D), dtype=q.dtype, device=q.device)
-        _check(lib().dlrm_qk_norm_rope(N, Hq, Hk, D, rot, _TORCH_DT[q.dtype], *qa, *ka, *turn, q_out.data_ptr(),
+            k_out = torch.empty((N, Hk, D), dtype=dt, device=where)
+        _check(lib().dlrm_qk_norm_rope(N, Hq, Hk, D, rot, _TORCH_DT[dt], *qa, *ka, *turn, q_out.data_ptr(),
                                        k_out.data_ptr(), s), "dlrm_qk_norm_rope")
     return q_out, k_out
+
+
+@functools.lru_cache(maxsize=1024)
+def qk_norm_rope_bwd_workspace_bytes(N: int, D: int, norm: bool) -> int:
+    out = _size_t(0)
+    _check(lib().dlrm_qk_norm_rope_bwd_workspace_bytes(N, D, 1 if norm else 0, ctypes.byref(out)),
+           "dlrm_qk_norm_rope_bwd_workspace_bytes")
+    return out.value
 
 
 def qk_norm_rope_bwd(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -708,60 +723,56 @@ def qk_norm_rope_bwd(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: torch.Tens
                      ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
     """Gradients of qk_norm_rope from those of its outputs (dlrm_qk_norm_rope_bwd); q, k and what
     follows as in the forward. Returns (d_q, d_k, d_w_q, d_w_k), the weights' fp32, None without a norm."""
-    N, Hq, D = q.shape if q.dim() == 3 else (0, 0, 0)
-    qa = _heads_of(q, "q")
-    ka = _heads_of(k, "k", like=q)
-    Hk = k.shape[1]
-    dqa = _heads_of(d_q_out, "d_q_out", like=q, heads=Hq)
-    dka = _heads_of(d_k_out, "d_k_out", like=q, heads=Hk)
-    rot, turn = _turn_args(q, positions, inv_freq, w_q, w_k, eps, sections, interleaved, N, D)
-    need = _size_t(0)
-    _check(lib().dlrm_qk_norm_rope_bwd_workspace_bytes(N, D, 0 if w_q is None else 1, ctypes.byref(need)),
-           "dlrm_qk_norm_rope_bwd_workspace_bytes")
-    _expect(workspace, "workspace", torch.uint8, need.value, at_least=True)
-    _contiguous(workspace=workspace)
-    _same_device(q, workspace=workspace)
-    dev = q.device
-    with _on(dev, stream) as s:
-        d_q = torch.empty((N, Hq, D), dtype=q.dtype, device=dev)
-        d_k = torch.empty((N, Hk, D), dtype=q.dtype, device=dev)
+    shape, qa = _heads_of(q, "q")
+    (_, Hk, _), ka = _heads_of(k, "k", q, shape)
+    N, Hq, D = shape
+    _, dqa = _heads_of(d_q_out, "d_q_out", q, shape, Hq)
+    _, dka = _heads_of(d_k_out, "d_k_out", q, shape, Hk)
+    dt, dev, where = q.dtype, q.get_device(), q.device
+    rot, turn = _turn_args(dev, positions, inv_freq, w_q, w_k, eps, sections, interleaved, N, D)
+    need = qk_norm_rope_bwd_workspace_bytes(N, D, w_q is not None)
+    _plain(workspace, "workspace", torch.uint8, need, dev, at_least=True)
+    with _on(where, stream) as s:
+        d_q = torch.empty(shape, dtype=dt, device=where)
+        d_k = torch.empty((N, Hk, D), dtype=dt, device=where)
         d_w_q = d_w_k = None
         if w_q is not None:
-            d_w_q = torch.empty(D, dtype=torch.float32, device=dev)
-            d_w_k = torch.empty(D, dtype=torch.float32, device=dev)
+            d_w_q = torch.empty(D, dtype=torch.float32, device=where)
+            d_w_k = torch.empty(D, dtype=torch.float32, device=where)
             if workspace is None:
-                workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        _check(lib().dlrm_qk_norm_rope_bwd(N, Hq, Hk, D, rot, _TORCH_DT[q.dtype], *dqa, *dka, *qa, *ka, *turn,
+                workspace = torch.empty(need, dtype=torch.uint8, device=where)
+        _check(lib().dlrm_qk_norm_rope_bwd(N, Hq, Hk, D, rot, _TORCH_DT[dt], *dqa, *dka, *qa, *ka, *turn,
                                            d_q.data_ptr(), d_k.data_ptr(), _ptr(d_w_q), _ptr(d_w_k), _ptr(workspace),
                                            0 if workspace is None else workspace.numel(), s),
                "dlrm_qk_norm_rope_bwd")
     return d_q, d_k, d_w_q, d_w_k
 
 
-def _paged_args(like, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk: int, D: int):
-    """Checks the cache and the sequences. Returns (seqs, page, pages, page and head stride)."""
-    if k_cache.dim() != 4 or k_cache.shape[1] != Hk or k_cache.shape[3] != D:
-        raise ValueError(f"k_cache must be [pages, {Hk}, page, {D}], got {tuple(k_cache.shape)}")
-    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+def _paged_args(dtype, dev: int, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk: int, D: int):
+    """Checks the cache and the sequences. Returns (seqs, page, pages, page and head stride, table stride and
+    width) and the addresses (q_offsets, kv_lens, page_table, status)."""
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape[1] != Hk or shape[3] != D:
+        raise ValueError(f"k_cache must be [pages, {Hk}, page, {D}], got {tuple(shape)}")
+    if v_cache.shape != shape or v_cache.stride() != strides:
         raise ValueError("v_cache must have k_cache's shape and strides")
-    if k_cache.dtype != like.dtype or v_cache.dtype != like.dtype:
-        raise ValueError(f"the caches must be {like.dtype}, got {k_cache.dtype} and {v_cache.dtype}")
-    if page_table.dim() != 2 or page_table.dtype != torch.int32:
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise ValueError(f"the caches must be {dtype}, got {k_cache.dtype} and {v_cache.dtype}")
+    table = page_table.shape
+    if len(table) != 2 or page_table.dtype != torch.int32:
         raise ValueError("page_table must be torch.int32 [sequences, pages]")
-    S, width = page_table.shape
-    if width > 1 and page_table.stride(1) != 1:
+    S, width = table
+    by_seq, by_entry = page_table.stride()
+    if width > 1 and by_entry != 1:
         raise ValueError("the entries of a row of page_table must be contiguous")
-    _expect(q_offsets, "q_offsets", torch.int32, S + 1)
-    _expect(kv_lens, "kv_lens", torch.int32, S)
-    _expect(status, "status", torch.int32, 1, at_least=True)
-    _contiguous(q_offsets=q_offsets, kv_lens=kv_lens, status=status)
-    _same_device(like, k_cache=k_cache, v_cache=v_cache, q_offsets=q_offsets, kv_lens=kv_lens, page_table=page_table,
-                 status=status)
-    pages, _, page, _ = k_cache.shape
-    by_page, by_head, by_slot, by_elem = k_cache.stride()
-    if pages > 0 and (by_slot != D or by_elem != 1):
+    where = (_plain(q_offsets, "q_offsets", torch.int32, S + 1, dev), _plain(kv_lens, "kv_lens", torch.int32, S, dev),
+             page_table.data_ptr(), _plain(status, "status", torch.int32, 1, dev, at_least=True))
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("page_table", page_table)):
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, not on device {dev}")
+    if shape[0] > 0 and (strides[2] != D or strides[3] != 1):
         raise ValueError("a page's entries of a head must be contiguous in the caches")
-    return S, page, pages, by_page, by_head
+    return (S, shape[2], shape[0], strides[0], strides[1], by_seq, width), where
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -775,32 +786,29 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     [pages, Hk, page, D] in place, and norms and rotates q in the same launch (dlrm_kv_append).
     Sequence s has tokens q_offsets[s] .. q_offsets[s + 1], the last entries of its kv_lens[s].
     Returns the new q, contiguous, or None without q (then w_q is not taken)."""
-    N, Hk, D = k.shape if k.dim() == 3 else (0, 0, 0)
-    ka = _heads_of(k, "k")
-    va = _heads_of(v, "v", like=k, heads=Hk)
+    shape, ka = _heads_of(k, "k")
+    N, Hk, D = shape
+    _, va = _heads_of(v, "v", k, shape, Hk)
     Hq, qa = 0, (None, 0, 0)
     if q is not None:
-        qa = _heads_of(q, "q", like=k)
-        Hq = q.shape[1]
+        (_, Hq, _), qa = _heads_of(q, "q", k, shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
     elif w_q is not None:
         raise ValueError("w_q without q")
-    rot, turn = _turn_args(k, positions, inv_freq, w_k if q is None else w_q, w_k, eps, sections, interleaved, N, D)
+    dt, dev, where = k.dtype, k.get_device(), k.device
+    rot, turn = _turn_args(dev, positions, inv_freq, w_k if q is None else w_q, w_k, eps, sections, interleaved, N, D)
     if q is None:
         turn = turn[:5] + (None,) + turn[6:]
-    S, page, pages, by_page, by_head = _paged_args(k, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk, D)
-    _expect(q_out, "q_out", k.dtype, N * Hq * D)
-    _contiguous(q_out=q_out)
-    _same_device(k, q_out=q_out)
-    with _on(k.device, stream) as s:
+    (S, page, pages, by_page, by_head, by_seq, width), (offsets_at, lens_at, table_at, status_at) = _paged_args(
+        dt, dev, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk, D)
+    _plain(q_out, "q_out", dt, N * Hq * D, dev)
+    with _on(where, stream) as s:
         if q is not None and q_out is None:
-            q_out = torch.empty((N, Hq, D), dtype=k.dtype, device=k.device)
-        _check(lib().dlrm_kv_append(N, S, Hq, Hk, D, rot, _TORCH_DT[k.dtype], *qa, *ka, *va, *turn,
-                                    q_offsets.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
-                                    page_table.stride(0), page_table.shape[1], page, pages, by_page, by_head,
-                                    k_cache.data_ptr(), v_cache.data_ptr(), _ptr(q_out), _ptr(status), s),
-               "dlrm_kv_append")
+            q_out = torch.empty((N, Hq, D), dtype=dt, device=where)
+        _check(lib().dlrm_kv_append(N, S, Hq, Hk, D, rot, _TORCH_DT[dt], *qa, *ka, *va, *turn, offsets_at, lens_at,
+                                    table_at, by_seq, width, page, pages, by_page, by_head, k_cache.data_ptr(),
+                                    v_cache.data_ptr(), _ptr(q_out), status_at, s), "dlrm_kv_append")
     return q_out
 
 
@@ -823,31 +831,32 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, q_
     `window` entries up to its own. max_q, max_kv: the most new tokens and the longest history of a
     sequence, for how the work is cut; without them N and the page table's width are taken. Returns
     out [N, Hq, D], or (out, lse [N, Hq] fp32) with want_lse."""
-    N, Hq, D = q.shape if q.dim() == 3 else (0, 0, 0)
-    qa = _heads_of(q, "q")
+    shape, qa = _heads_of(q, "q")
+    N, Hq, D = shape
+    dt, dev, where = q.dtype, q.get_device(), q.device
     Hk = k_cache.shape[1] if k_cache.dim() == 4 else 0
-    S, page, pages, by_page, by_head = _paged_args(q, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk, D)
-    max_q = N if max_q is None else max_q
-    max_kv = page_table.shape[1] * page if max_kv is None else max_kv
-    scale = D ** -0.5 if scale is None and D > 0 else scale
+    (S, page, pages, by_page, by_head, by_seq, width), (offsets_at, lens_at, table_at, status_at) = _paged_args(
+        dt, dev, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk, D)
+    if max_q is None:
+        max_q = N
+    if max_kv is None:
+        max_kv = width * page
+    if scale is None:
+        scale = D ** -0.5 if D > 0 else 1.0
     need = paged_attn_workspace_bytes(N, S, Hq, Hk, D, causal, window, max_q, max_kv)
-    _expect(out, "out", q.dtype, N * Hq * D)
-    _expect(lse, "lse", torch.float32, N * Hq)
-    _expect(workspace, "workspace", torch.uint8, need, at_least=True)
-    _contiguous(out=out, lse=lse, workspace=workspace)
-    _same_device(q, out=out, lse=lse, workspace=workspace)
-    dev = q.device
-    with _on(dev, stream) as s:
+    _plain(out, "out", dt, N * Hq * D, dev)
+    _plain(lse, "lse", torch.float32, N * Hq, dev)
+    _plain(workspace, "workspace", torch.uint8, need, dev, at_least=True)
+    with _on(where, stream) as s:
         if out is None:
-            out = torch.empty((N, Hq, D), dtype=q.dtype, device=dev)
+            out = torch.empty(shape, dtype=dt, device=where)
         if lse is None and want_lse:
-            lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+            lse = torch.empty((N, Hq), dtype=torch.float32, device=where)
         if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        _check(lib().dlrm_paged_attn(N, S, Hq, Hk, D, _TORCH_DT[q.dtype], *qa, k_cache.data_ptr(), v_cache.data_ptr(),
-                                     page, pages, by_page, by_head, q_offsets.data_ptr(), kv_lens.data_ptr(),
-                                     page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
+            workspace = torch.empty(need, dtype=torch.uint8, device=where)
+        _check(lib().dlrm_paged_attn(N, S, Hq, Hk, D, _TORCH_DT[dt], *qa, k_cache.data_ptr(), v_cache.data_ptr(), page,
+                                     pages, by_page, by_head, offsets_at, lens_at, table_at, by_seq, width,
                                      1 if causal else 0, window, scale, max_q, max_kv, out.data_ptr(), _ptr(lse),
-                                     _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(status), s),
+                                     _ptr(workspace), 0 if workspace is None else workspace.numel(), status_at, s),
                "dlrm_paged_attn")
     return (out, lse) if want_lse else out
