@@ -11,6 +11,8 @@
 // its right operand when the order of the 32 entries in the sum is chosen to fit (lane group g
 // takes entries 4g .. 4g+3 of both halves): the weights never leave the lane, and m, l and the
 // rescale of O are one value per lane.
+#include <type_traits>
+
 #include "history_device.h"
 
 namespace dlrm {
@@ -37,6 +39,18 @@ __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f3
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                   0);
+}
+
+// The same with 16 steps instead of 32: four elements a lane.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16_half(const uint2& a, const uint2& b, const f32x4& c) {
+  if constexpr (DT == DLRM_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0, 0,
+                                                     0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, a), __builtin_bit_cast(f16x4, b), c, 0, 0, 0);
 }
 
 // All bits of those of the two 16-bit values of a dword that are infinite or NaN.
@@ -89,17 +103,30 @@ __device__ __forceinline__ Span seen_by(const Seq& s, int token, int causal, int
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
 
-// ---------------------------------------------------------------------------
-// Rows kernel: 16 RT rows of one head to a workgroup, the four waves take the 32-entry tiles of
-// the history in turn and join their (m, l, O) through LDS at the end. Keys and values go from
-// global memory to registers: each is used once. A lane takes D / 16 neighbouring elements of
-// eight values' rows, so that a load instruction covers whole rows, and the transposition that
-// the second product needs is 16-bit permutations in registers.
-// ---------------------------------------------------------------------------
-// How a call is cut: q_tiles tiles of rows per sequence and head, splits parts of a tile's entries.
+// The larger of a lane and the one 32 away.
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The same within pairs of sixteen lanes.
+__device__ __forceinline__ float max_quarters(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_quarters(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// How a call is cut: q_tiles tiles of rows per sequence and head, splits parts of a tile's entries. The
+// grid is heads x (tiles x parts) x sequences.
 struct Cut {
   int q_tiles, splits, part;  // part: entries of a part, unless the history is longer than announced
-  long long units;            // workgroups' worth of work: sequences x tiles x parts x heads
   float* o;                   // [splits][n][q_heads][dim], not yet divided by the sums
   float2* ml;                 // [n][q_heads][splits]: maximum and sum
 };
@@ -122,8 +149,10 @@ struct Reach {
     first = lo & ~31;
     const int span = hi > first ? hi - first : 0;
     part = cut.part;
-    if (span > static_cast<long long>(part) * cut.splits) part = static_cast<int>(((static_cast<long long>(span) + cut.splits - 1) / cut.splits + 63) & ~63LL);
-    parts = span > part ? static_cast<int>((static_cast<long long>(span) + part - 1) / part) : 1;
+    // spans stay below 2^31 - 2^17, so the sums below fit 32 bits
+    if (span > static_cast<long long>(part) * cut.splits)
+      part = ((static_cast<uint32_t>(span) + cut.splits - 1) / static_cast<uint32_t>(cut.splits) + 63) & ~63u;
+    parts = span > part ? (static_cast<uint32_t>(span) + part - 1) / static_cast<uint32_t>(part) : 1;
   }
 };
 
@@ -137,13 +166,29 @@ __device__ __forceinline__ void finish(const AttnArgs& a, long long to, int at, 
   if (at == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : fmaf(m, a.scale, logf(l) - kLift<DT> * kLn2);
 }
 
-template <int DT, int D, int RT>
-__global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, Cut cut) {
-  constexpr int F = D / 32;           // k steps of the first product
-  constexpr int E = D / 16;           // elements of a value row that a lane takes, and 16-wide pieces of O
-  constexpr int Rows = 16 * RT;
-  constexpr int Pitch = D + 4;        // floats; a row of O in LDS
-  __shared__ float lds_o[kWaves][16 * Pitch];
+// ---------------------------------------------------------------------------
+// Rows kernel: 16 rows of one head to a workgroup, the four waves take the tiles of 16 TT entries of the
+// history in turn and join their (m, l, O) through LDS at the end. Bound by memory: keys and values go from
+// global memory to registers, each is used once. A lane takes D / 16 neighbouring elements of four values'
+// rows of each 16, so that a load instruction covers whole rows, and the transposition that the second
+// product needs is 16-bit permutations in registers.
+// A wave has a tile of loads on the way all the time: the next tile's keys are asked for as soon as this
+// one's are used, its values likewise, without a second set of registers. TT is what the registers hold at
+// two waves to a SIMD (256-wide heads: 16 entries a tile, with the 16x16x16 product for the values).
+// ---------------------------------------------------------------------------
+template <int D>
+constexpr int kRowsBlocks = D == 256 ? 1 : D == 128 ? 2 : 4;
+
+template <int DT, int D>
+__global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Cut cut) {
+  constexpr int TT = kRowsBlocks<D>;  // blocks of 16 entries to a tile
+  constexpr int K = 16 * TT;
+  constexpr int F = D / 32;      // k steps of the first product
+  constexpr int E = D / 16;      // elements of a value row that a lane takes, and 16-wide pieces of O
+  constexpr int Rows = 16;
+  constexpr int Pitch = D + 4;   // floats; a row of O in LDS
+  constexpr int Ahead = 64 / TT; // tiles whose pages a wave holds
+  __shared__ float lds_o[kWaves][Rows * Pitch];
   __shared__ float2 lds_ml[kWaves][Rows];
   const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, c16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -151,253 +196,260 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, Cut cut
   const float c = a.scale * kLog2e;
   const Paged& pg = a.paged;
   const int page_mask = (1 << pg.page_shift) - 1;
+  const int head = blockIdx.x, split = blockIdx.y % cut.splits;
+  const uint16_t* kh = static_cast<const uint16_t*>(a.k_cache) + head * pg.head_stride + (c16 * D + g * 8);
+  const uint16_t* vh = static_cast<const uint16_t*>(a.v_cache) + head * pg.head_stride + (4 * g * D + c16 * E);
 
-  for (long long unit = blockIdx.x; unit < cut.units; unit += gridDim.x) {
-    const int head = static_cast<int>(unit % a.kv_heads);
-    long long rest = unit / a.kv_heads;
-    const int split = static_cast<int>(rest % cut.splits);
-    rest /= cut.splits;
-    const int seq = static_cast<int>(rest / cut.q_tiles);
+  for (int seq = blockIdx.z; seq < pg.seqs; seq += gridDim.z) {
     const Seq sq = load_seq(pg, a.n, seq);
     const int rows = sq.tokens * group;
-    const uint16_t* kh = static_cast<const uint16_t*>(a.k_cache) + head * pg.head_stride;
-    const uint16_t* vh = static_cast<const uint16_t*>(a.v_cache) + head * pg.head_stride;
     const int32_t* table = pg.page_table + seq * pg.table_stride;
 
-    for (long long first_row = rest % cut.q_tiles * Rows; first_row < rows;
+    for (long long first_row = static_cast<long long>(blockIdx.y / cut.splits) * Rows; first_row < rows;
          first_row += static_cast<long long>(cut.q_tiles) * Rows) {
       const int row0 = static_cast<int>(first_row), row_end = rows - row0 > Rows ? row0 + Rows : rows;
       const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut);
       if (split >= rc.parts) continue;
-      const int tok0 = rc.tok0, tok1 = rc.tok1, lo = rc.lo;
       const int k_first = rc.first + split * rc.part;
       const int hi = rc.hi < k_first + rc.part ? rc.hi : k_first + rc.part;
+      const int k_begin = k_first + K * wave;
 
-      u32x4 qf[RT][F];
-      int row_lo[RT], row_hi[RT], row_tok[RT];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const int row = row0 + rt * 16 + c16;
-        row_lo[rt] = row_hi[rt] = 0;
-        row_tok[rt] = -1;
-#pragma unroll
-        for (int f = 0; f < F; ++f) qf[rt][f] = u32x4{0, 0, 0, 0};
-        if (row < row_end) {
-          const int tok = row / group, gi = row - tok * group;
-          const Span s = seen_by(sq, tok, a.causal, a.window);
-          row_lo[rt] = s.lo;
-          row_hi[rt] = s.hi;
-          row_tok[rt] = tok;
-          const uint16_t* q = static_cast<const uint16_t*>(a.q.ptr) + (sq.first + tok) * a.q.stride +
-                              (head * group + gi) * a.q.head_stride + g * 8;
-#pragma unroll
-          for (int f = 0; f < F; ++f) qf[rt][f] = *reinterpret_cast<const u32x4*>(q + f * 32);
-        }
-      }
-
-      float m[RT], l[RT];
-      f32x4 o[RT][E];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        m[rt] = -INFINITY;
-        l[rt] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[rt][e] = f32x4{0, 0, 0, 0};
-      }
-
-      // Two 16-entry halves of a tile: where they are, and whether their pages are good. Past the end
-      // and in place of a bad page another page of the cache is read and masked.
-      struct Tile {
-        long long at[2];
-        bool good[2];
-      };
+      // Pages of the blocks of this wave's next Ahead tiles, one to a lane; past the end: of the last entry.
+      const auto key_of = [&](int k0, int block) { return k0 + block / TT * (K * kWaves) + block % TT * 16; };
       const auto look_up = [&](int k0) {
-        Tile t;
+        const int key = key_of(k0, lane);
+        return table[(key < hi ? key : hi - 1) >> pg.page_shift];
+      };
+      const auto good_pages = [&](int k0, int page) {  // bit i: the page of block i is good
+        const bool good = static_cast<uint32_t>(page) < static_cast<uint32_t>(pg.num_pages);
+        const int key = key_of(k0, lane);
+        if (!good && key < hi && key + 16 > rc.lo) flag(pg.status, DLRM_STATUS_BAD_PAGE);
+        return __ballot(good);
+      };
+      int pages = 0;
+      if (k_begin < hi) pages = look_up(k_begin);
+
+      u32x4 qf[F];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+      for (int f = 0; f < F; ++f) qf[f] = u32x4{0, 0, 0, 0};
+      const int row = row0 + c16;
+      int row_lo = 0, row_hi = 0, row_tok = -1;
+      if (row < row_end) {
+        row_tok = row / group;
+        const int gi = row - row_tok * group;
+        const Span s = seen_by(sq, row_tok, a.causal, a.window);
+        row_lo = s.lo;
+        row_hi = s.hi;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q.ptr) + (sq.first + row_tok) * a.q.stride +
+                            (head * group + gi) * a.q.head_stride + g * 8;
+#pragma unroll
+        for (int f = 0; f < F; ++f) qf[f] = *reinterpret_cast<const u32x4*>(q + f * 32);
+      }
+
+      float m = -INFINITY, l = 0.f;
+      f32x4 o[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = f32x4{0, 0, 0, 0};
+
+      // Where the blocks of a tile are, in elements, and whether their pages are good. Past the end and in
+      // place of a bad page another page of the cache is read and masked.
+      struct Tile {
+        long long at[TT];
+        int good;
+      };
+      uint64_t good64 = 0;
+      const auto find = [&](int k0, int index) {
+        Tile t;
+        t.good = static_cast<int>(good64 >> (index * TT)) & ((1 << TT) - 1);
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
           const int key = k0 + 16 * i < hi ? k0 + 16 * i : hi - 1;
-          const int page = scalar_load(table, key >> pg.page_shift);
-          t.good[i] = page >= 0 && page < pg.num_pages;
-          if (!t.good[i] && k0 + 16 * i + 16 > lo && lane == 0) flag(pg.status, DLRM_STATUS_BAD_PAGE);
-          t.at[i] = (t.good[i] ? page : 0) * pg.page_stride + (key & page_mask & ~15) * D;
+          const int page = t.good >> i & 1 ? __builtin_amdgcn_readlane(pages, index * TT + i) : 0;
+          t.at[i] = page * pg.page_stride + (key & page_mask & ~15) * D;
         }
         return t;
       };
-      u32x4 kf[2][F];
-      uint32_t v[8][E / 2];
+      u32x4 kf[TT][F];
+      uint32_t v[4 * TT][E / 2];
       const auto load_keys = [&](const Tile& t) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < TT; ++i)
 #pragma unroll
-          for (int f = 0; f < F; ++f)
-            kf[i][f] = *reinterpret_cast<const u32x4*>(kh + t.at[i] + (c16 * D + g * 8) + f * 32);
+          for (int f = 0; f < F; ++f) kf[i][f] = *reinterpret_cast<const u32x4*>(kh + t.at[i] + f * 32);
       };
       const auto load_values = [&](const Tile& t) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          __builtin_memcpy(v[j], __builtin_assume_aligned(vh + t.at[j / 4] + (4 * g * D + c16 * E) + j % 4 * D,
-                                                          E >= 8 ? 16 : 2 * E), 2 * E);
+        for (int j = 0; j < 4 * TT; ++j)
+          __builtin_memcpy(v[j], __builtin_assume_aligned(vh + t.at[j / 4] + j % 4 * D, E >= 8 ? 16 : 2 * E), 2 * E);
       };
 
-      // The next tile's keys are asked for as soon as this tile's are used, its values likewise, so
-      // that a wave has a tile of loads on the way all the time without a second set of registers.
-      const int k_begin = k_first + 32 * wave;
-      Tile tile, next;
-      if (k_begin < hi) {
-        tile = look_up(k_begin);
-        load_keys(tile);
-        load_values(tile);
-      }
-      for (int k0 = k_begin; k0 < hi; k0 += 32 * kWaves) {
-        const int k_next = k0 + 32 * kWaves;
-        if (k_next < hi) next = look_up(k_next);
-        f32x4 sc[RT][2];
+      // One tile at k0; with More, the loads of the next one at its places.
+      const auto work = [&](int k0, const Tile& tile, const Tile& next, auto more) {
+        constexpr bool More = decltype(more)::value;
+        f32x4 s[TT];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int t = 0; t < TT; ++t) {
+          s[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            sc[rt][t] = f32x4{0, 0, 0, 0};
+          for (int f = 0; f < F; ++f) s[t] = mfma16<DT>(kf[t][f], qf[f], s[t]);
+        }
+        if constexpr (More) load_keys(next);
+        const bool edge = k0 < rc.all_lo || k0 + K > rc.all_hi || k0 + K > hi || tile.good != (1 << TT) - 1;
+        if (edge) {
 #pragma unroll
-            for (int f = 0; f < F; ++f) sc[rt][t] = mfma16<DT>(kf[t][f], qf[rt][f], sc[rt][t]);
-          }
-        if (k_next < hi) load_keys(next);
-
-        u32x4 pw[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          f32x4(&s)[2] = sc[rt];
-          float top = -INFINITY;
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const int key = k0 + 16 * t + 4 * g + r;
-              if (!tile.good[t] || key < row_lo[rt] || key >= row_hi[rt] || key >= hi) s[t][r] = -INFINITY;
-              top = fmaxf(top, s[t][r]);
+              if (!(tile.good >> t & 1) || key < row_lo || key >= row_hi || key >= hi) s[t][r] = -INFINITY;
             }
-          top = fmaxf(top, __shfl_xor(top, 16));
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const float next = fmaxf(m[rt], top);
-          const float base = next == -INFINITY ? 0.f : next * c - kLift<DT>;
-          const float keep = exp2f(m[rt] == -INFINITY ? -INFINITY : (m[rt] - next) * c);
-          m[rt] = next;
-          float p[8], sum = 0.f;
+        }
+        float top = s[0][0];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            p[i] = exp2f(fmaf(s[i / 4][i % 4], c, -base));
-            sum += p[i];
-          }
-          l[rt] = fmaf(l[rt], keep, sum);
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[rt][e] *= keep;
+          for (int r = 0; r < 4; ++r) top = fmaxf(top, s[t][r]);
+        const float now = fmaxf(m, max_halves(max_quarters(top)));
+        // O and l stay relative to an older maximum until a row's grows by 2^8 (fp16, with its lift: 2^7)
+        if (__any((now - m) * c > (DT == DLRM_F16 ? 7.f : 8.f))) {
+          const float keep = m == -INFINITY ? 0.f : exp2f((m - now) * c);
+          m = now;
+          l *= keep;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) pw[rt][i] = pack2<DT>(p[2 * i], p[2 * i + 1]);
+          for (int e = 0; e < E; ++e) o[e] *= keep;
+        }
+        const float base = m == -INFINITY ? 0.f : m * c - kLift<DT>;
+        uint32_t pw[TT][2];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          float p[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) p[r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -base));
+          l += (p[0] + p[1]) + (p[2] + p[3]);
+          pw[t][0] = pack2<DT>(p[0], p[1]);
+          pw[t][1] = pack2<DT>(p[2], p[3]);
         }
 
-        // values that no row sees are zero, whatever they hold
-        if (k0 < lo || k0 + 32 > hi || !tile.good[0] || !tile.good[1]) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int key = k0 + 16 * (j / 4) + 4 * g + j % 4;
-            if (key < lo || key >= hi || !tile.good[j / 4]) {
-#pragma unroll
-              for (int i = 0; i < E / 2; ++i) v[j][i] = 0;
-            }
-          }
-        }
-
-        // entries that only some rows see: if one holds an infinity or NaN, the second product runs
-        // token by token, with what the token does not see set to zero, and only the token's own rows
-        // take the sum
+        // Entries that no row sees are zero, whatever they hold. If one that only some rows see holds an
+        // infinity or NaN, the second product runs token by token, with what the token does not see set to
+        // zero, and only the token's own rows take the sum.
         bool apart = false;
-        if (tok1 > tok0 && (k0 < rc.all_lo || k0 + 32 > rc.all_hi)) {
+        if (edge) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < E / 2; ++i) apart |= not_finite_halves<DT>(v[j][i]) != 0;
-          apart = __ballot(apart) != 0;
-        }
-        for (int tok = apart ? tok0 : tok1; tok <= tok1; ++tok) {
-          uint32_t see[8];
-          const Span s = seen_by(sq, tok, a.causal, a.window);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4 * TT; ++j) {
             const int key = k0 + 16 * (j / 4) + 4 * g + j % 4;
-            see[j] = !apart || (key >= s.lo && key < s.hi) ? 0xffffffffu : 0;
+            const bool none = key < rc.lo || key >= hi || !(tile.good >> (j / 4) & 1);
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+              if (none) v[j][i] = 0;
+              apart |= not_finite_halves<DT>(v[j][i]) != 0;
+            }
           }
+          apart = rc.tok1 > rc.tok0 && __any(apart);
+        }
+        const auto product = [&](auto seen, bool mine) {
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            u32x4 vt;
+            const uint32_t pick = e % 2 ? 0x07060302u : 0x05040100u;
+            f32x4 sum = o[e];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              vt[i] = __builtin_amdgcn_perm(v[2 * i + 1][e / 2] & see[2 * i + 1], v[2 * i][e / 2] & see[2 * i],
-                                            e % 2 ? 0x07060302u : 0x05040100u);
+            for (int t = 0; t < TT; t += 2) {
+              u32x4 vt = {0, 0, 0, 0};
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              const f32x4 sum = mfma16<DT>(vt, pw[rt], o[rt][e]);
-              if (!apart || row_tok[rt] == tok) o[rt][e] = sum;
+              for (int i = 0; i < (TT == 1 ? 2 : 4); ++i) {
+                const int j = 4 * t + 2 * i;
+                vt[i] = __builtin_amdgcn_perm(v[j + 1][e / 2] & seen(j + 1), v[j][e / 2] & seen(j), pick);
+              }
+              if constexpr (TT == 1)
+                sum = mfma16_half<DT>(make_uint2(vt[0], vt[1]), make_uint2(pw[0][0], pw[0][1]), sum);
+              else
+                sum = mfma16<DT>(vt, u32x4{pw[t][0], pw[t][1], pw[t + 1 < TT ? t + 1 : t][0], pw[t + 1 < TT ? t + 1 : t][1]}, sum);
             }
+            if (mine) o[e] = sum;
+          }
+        };
+        if (!apart) {
+          product([](int) { return 0xffffffffu; }, true);
+        } else {
+#pragma unroll 1
+          for (int tok = rc.tok0; tok <= rc.tok1; ++tok) {
+            const Span sp = seen_by(sq, tok, a.causal, a.window);
+            product([&](int j) {
+              const int key = k0 + 16 * (j / 4) + 4 * g + j % 4;
+              return key >= sp.lo && key < sp.hi ? 0xffffffffu : 0u;
+            }, row_tok == tok);
           }
         }
-        if (k_next < hi) {
-          load_values(next);
+        if constexpr (More) load_values(next);
+      };
+
+      if (k_begin < hi) {
+        good64 = good_pages(k_begin, pages);
+        int index = 0;
+        Tile tile = find(k_begin, 0);
+        load_keys(tile);
+        load_values(tile);
+        int k0 = k_begin;
+        for (; k0 + K * kWaves < hi; k0 += K * kWaves) {
+          const int k_next = k0 + K * kWaves;
+          if (++index == Ahead) {
+            index = 0;
+            pages = look_up(k_next);
+            good64 = good_pages(k_next, pages);
+          }
+          const Tile next = find(k_next, index);
+          work(k0, tile, next, std::true_type{});
           tile = next;
         }
+        work(k0, tile, tile, std::false_type{});
       }
 
       // join the waves
+      l = add_halves(add_quarters(l));
+      if (g == 0) lds_ml[wave][c16] = make_float2(m, l);
+      __syncthreads();
+      float top = -INFINITY;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        l[rt] += __shfl_xor(l[rt], 16);
-        l[rt] += __shfl_xor(l[rt], 32);
-        if (g == 0) lds_ml[wave][rt * 16 + c16] = make_float2(m[rt], l[rt]);
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_ml[w][c16].x);
+      const float keep = m == -INFINITY ? 0.f : exp2f((m - top) * c);
+      // lane (g, c16) holds elements 4 E g .. 4 E (g + 1) of its row, E at a time
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int e = 0; e < E; ++e) lds_o[wave][c16 * Pitch + (4 * g + r) * E + e] = o[e][r] * keep;
+      __syncthreads();
+      constexpr int Pieces = D / 8;
+      for (int i = threadIdx.x; i < Rows * Pieces; i += kThreads) {
+        const int r16 = i / Pieces, at = i % Pieces * 8;
+        const int out_row = row0 + r16;
+        if (out_row >= row_end) continue;
+        float mt = -INFINITY, lt = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) mt = fmaxf(mt, lds_ml[w][r16].x);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          const float2 ml = lds_ml[w][r16];
+          lt += ml.y * (ml.x == -INFINITY ? 0.f : exp2f((ml.x - mt) * c));
+        }
+        float x[8];
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          x[d] = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) x[d] += lds_o[w][r16 * Pitch + at + d];
+        }
+        const int tok = out_row / group, gi = out_row - tok * group;
+        const long long to = static_cast<long long>(sq.first + tok) * a.q_heads + head * group + gi;
+        if (rc.parts == 1) {
+          finish<DT>(a, to, at, x, mt, lt);
+        } else {
+          float* p = cut.o + (split * a.n * a.q_heads + to) * D + at;
+          *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+          if (at == 0) cut.ml[to * cut.splits + split] = make_float2(mt, lt);
+        }
       }
       __syncthreads();
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_ml[w][rt * 16 + c16].x);
-        const float keep = m[rt] == -INFINITY ? 0.f : exp2f((m[rt] - top) * c);
-        // lane (g, c16) holds elements 4 E g .. 4 E (g + 1) of its row, E at a time
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int e = 0; e < E; ++e) lds_o[wave][c16 * Pitch + (4 * g + r) * E + e] = o[rt][e][r] * keep;
-        __syncthreads();
-        constexpr int Pieces = D / 8;
-        for (int i = threadIdx.x; i < 16 * Pieces; i += kThreads) {
-          const int r16 = i / Pieces, at = i % Pieces * 8;
-          const int row = row0 + rt * 16 + r16;
-          if (row >= row_end) continue;
-          float mt = -INFINITY, lt = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w) mt = fmaxf(mt, lds_ml[w][rt * 16 + r16].x);
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w) {
-            const float2 ml = lds_ml[w][rt * 16 + r16];
-            lt += ml.y * (ml.x == -INFINITY ? 0.f : exp2f((ml.x - mt) * c));
-          }
-          float x[8];
-#pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            x[d] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) x[d] += lds_o[w][r16 * Pitch + at + d];
-          }
-          const int tok = row / group, gi = row - tok * group;
-          const long long to = static_cast<long long>(sq.first + tok) * a.q_heads + head * group + gi;
-          if (rc.parts == 1) {
-            finish<DT>(a, to, at, x, mt, lt);
-          } else {
-            float* p = cut.o + (split * a.n * a.q_heads + to) * D + at;
-            *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-            if (at == 0) cut.ml[to * cut.splits + split] = make_float2(mt, lt);
-          }
-        }
-        __syncthreads();
-      }
     }
   }
 }
@@ -415,7 +467,6 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a, Cut cut
 // in order and picks the piece for each.
 // ---------------------------------------------------------------------------
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 template <int DT>
 __device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f32x16& c) {
@@ -439,16 +490,6 @@ __device__ __forceinline__ int value_swizzle(int r) {
 }
 
 constexpr int kTileKeys = 64;
-
-// The larger of a lane and the one 32 away.
-__device__ __forceinline__ float max_halves(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-__device__ __forceinline__ float add_halves(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
 
 // N copies of 16 bytes a lane to LDS: copy i brings from `from` + off[i] + 1024 i, lane j's bytes to
 // `to` + 1024 i + 16 j; from and to are the same in every lane. Written out because after the builtin
@@ -521,12 +562,8 @@ __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs 
     if (i < Group) copy_v[i] = 2 * (lane / P * D + (lane % P ^ value_swizzle<D>(r)) * 8);
   }
 
-  for (long long unit = blockIdx.x; unit < cut.units; unit += gridDim.x) {
-    const int head = static_cast<int>(unit % a.kv_heads);
-    long long rest = unit / a.kv_heads;
-    const int split = static_cast<int>(rest % cut.splits);
-    rest /= cut.splits;
-    const int seq = static_cast<int>(rest / cut.q_tiles);
+  const int head = blockIdx.x, split = blockIdx.y % cut.splits;
+  for (int seq = blockIdx.z; seq < pg.seqs; seq += gridDim.z) {
     const Seq sq = load_seq(pg, a.n, seq);
     const int rows = sq.tokens * group;
     const uint16_t* kh = static_cast<const uint16_t*>(a.k_cache) + head * pg.head_stride;
@@ -534,7 +571,7 @@ __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs 
     const int32_t* table = pg.page_table + seq * pg.table_stride;
 
     // the last rows of a causal chunk see the most: they start first
-    for (long long first_row = (cut.q_tiles - 1 - rest % cut.q_tiles) * Rows; first_row < rows;
+    for (long long first_row = static_cast<long long>(cut.q_tiles - 1 - blockIdx.y / cut.splits) * Rows; first_row < rows;
          first_row += static_cast<long long>(cut.q_tiles) * Rows) {
       const int row0 = static_cast<int>(first_row), row_end = rows - row0 > Rows ? row0 + Rows : rows;
       const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut);
@@ -888,7 +925,8 @@ int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
 Cut cut_call(long long max_rows, int seqs, int kv_heads, int dim, int causal, int window, int max_q, int max_kv) {
   Cut c;
   const int rows = tile_rows(max_rows);
-  const long long tiles = max_rows > rows ? (max_rows + rows - 1) / rows : 1;
+  long long tiles = max_rows > rows ? (max_rows + rows - 1) / rows : 1;
+  if (tiles > 65535) tiles = 65535;  // a workgroup takes further tiles in turn
   c.q_tiles = static_cast<int>(tiles);
   const long long whole = tiles * seqs * kv_heads;
   long long span = max_kv > 0 ? max_kv : 1;
@@ -899,9 +937,9 @@ Cut cut_call(long long max_rows, int seqs, int kv_heads, int dim, int causal, in
   const long long most = (span + least - 1) / least;
   splits = splits < 1 ? 1 : splits > most ? most : splits;
   if (splits > kMaxSplits) splits = kMaxSplits;
+  if (splits > 65535 / tiles) splits = 65535 / tiles;
   c.splits = static_cast<int>(splits);
   c.part = static_cast<int>(((span + splits - 1) / splits + 63) & ~63LL);
-  c.units = whole * splits;
   c.o = nullptr;
   c.ml = nullptr;
   return c;
@@ -915,8 +953,6 @@ size_t cut_bytes(const Cut& c, int64_t n, int q_heads, int dim) {
   return round256(rows * dim * sizeof(float)) + rows * sizeof(float2);
 }
 
-constexpr long long kMaxGrid = 1 << 22;
-
 template <int DT, int D>
 hipError_t run(const AttnArgs& a, hipStream_t s) {
   const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
@@ -924,10 +960,10 @@ hipError_t run(const AttnArgs& a, hipStream_t s) {
   cut.o = static_cast<float*>(a.workspace);
   cut.ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) +
                                      round256(static_cast<size_t>(a.n) * a.q_heads * cut.splits * D * sizeof(float)));
-  const dim3 grid(static_cast<unsigned>(cut.units < kMaxGrid ? cut.units : kMaxGrid));
+  const dim3 grid(a.kv_heads, cut.q_tiles * cut.splits, a.paged.seqs < 65535 ? a.paged.seqs : 65535);
   const int tile = tile_rows(rows);
   if (tile == 16)
-    hipLaunchKernelGGL((attn_rows_kernel<DT, D, 1>), grid, dim3(kThreads), 0, s, a, cut);
+    hipLaunchKernelGGL((attn_rows_kernel<DT, D>), grid, dim3(kThreads), 0, s, a, cut);
   else
     hipLaunchKernelGGL((attn_tile_kernel<DT, D>), grid, dim3(kTileThreads<D>), 0, s, a, cut);
   if (cut.splits > 16)
