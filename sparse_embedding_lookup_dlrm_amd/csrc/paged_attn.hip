@@ -914,14 +914,19 @@ void join(const AttnArgs& a, const Cut& cut, int tile_rows, hipStream_t s) {
 // Rows of a tile: 16 for the rows kernel (one wave's matrix instruction), 128 for the tile kernel.
 int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
 
-// Where the workgroups of a call would not fill the chip, every history is split into parts of at least
-// `least` entries until there are `wanted` workgroups.
-// Rows kernel: 16 for each place on the chip, so that histories of unequal length even out (64 histories
-// of up to 16k entries: 241 us against 330 with 2048; one of 131k: 33 us with parts of 1024, 35 with 512,
-// 40 with 256).
-// Tile kernel: as many as there are places. 24 sequences of up to 257 x 1500, 288 workgroups: 25.5 us
-// against 29 unsplit; 432 workgroups of 256-wide heads, one to a CU: 86 us unsplit against 118 in two
-// parts, since the parts wait for a place and their sums are written and read.
+// Where the workgroups of a call would not fill the chip, or histories may be of unequal length, every
+// history is split into parts.
+// Rows kernel: parts of 128 KB of keys and as much of values (64 histories of up to 16k entries of 128:
+// 224 us; with half as much 231 us, with twice 242 us), smaller ones of at least 512 entries where that
+// leaves fewer than 512 workgroups, and at most 16k workgroups. One history of 131k: 33 us; with parts of
+// 256 entries 40 us.
+// Tile kernel: twice as many workgroups as there are places, in parts of at least 512 entries. 24 sequences
+// of up to 257 x 1500, 288 workgroups: 22.9 us against 29 unsplit; 8 sequences of 32 tokens over up to 32k:
+// 56 us, 71 with as many as places; but 432 workgroups of 256-wide heads, one to a CU: 81 us unsplit against
+// 118 in two parts, since the parts wait for a place and their sums are written and read.
+// The number of workgroups of a sequence is made odd where heads allow: workgroups go to the XCDs in turn,
+// and with 16 parts of 4 heads the first parts of all sequences, the ones that short histories fill, would
+// meet on the same four of eight (64 histories of up to 8k, 256-wide heads: 184 us, with 17 parts 151 us).
 Cut cut_call(long long max_rows, int seqs, int kv_heads, int dim, int causal, int window, int max_q, int max_kv) {
   Cut c;
   const int rows = tile_rows(max_rows);
@@ -931,12 +936,22 @@ Cut cut_call(long long max_rows, int seqs, int kv_heads, int dim, int causal, in
   const long long whole = tiles * seqs * kv_heads;
   long long span = max_kv > 0 ? max_kv : 1;
   if (causal && window && span > static_cast<long long>(window) + max_q + 32) span = static_cast<long long>(window) + max_q + 32;
-  const int wanted = rows == 16 ? 8192 : dim == 256 ? 256 : dim == 128 ? 512 : 768;
-  const int least = rows == 16 ? 1024 : 512;
-  long long splits = wanted / (whole > 0 ? whole : 1);
-  const long long most = (span + least - 1) / least;
-  splits = splits < 1 ? 1 : splits > most ? most : splits;
-  if (splits > kMaxSplits) splits = kMaxSplits;
+  long long splits;
+  const long long units = whole > 0 ? whole : 1;
+  if (rows == 16) {
+    const long long least = 131072 / dim, fill = 512 / units, finest = (span + 511) / 512, most = 16384 / units;
+    splits = (span + least - 1) / least;
+    if (splits < fill) splits = fill < finest ? fill : finest;
+    if (splits > most) splits = most;
+  } else {
+    const long long places = dim == 256 ? 256 : dim == 128 ? 512 : 768, most = (span + 511) / 512;
+    splits = 2 * places / units;
+    if (splits > most) splits = most;
+  }
+  if (splits < 1) splits = 1;
+  if (splits > 1) splits |= 1;
+  if (tiles > 1) c.q_tiles = static_cast<int>(tiles |= 1);
+  if (splits > kMaxSplits) splits = kMaxSplits - 1;
   if (splits > 65535 / tiles) splits = 65535 / tiles;
   c.splits = static_cast<int>(splits);
   c.part = static_cast<int>(((span + splits - 1) / splits + 63) & ~63LL);

@@ -589,25 +589,26 @@ def _heads_of(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None, s
     """Checks a tensor of heads [tokens, heads, dim], the elements of a head contiguous; like, shape: the
     tensor whose tokens, dim, dtype and device it has to share, and its shape. Returns its shape, and its
     address and strides."""
-    own = t.shape
+    own, strides = t.shape, t.stride()
     if len(own) != 3:
         raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(own)}")
+    n, many, width = own
     if like is None:
         if t.dtype not in _TORCH_DT:
             raise ValueError(f"unsupported dtype {t.dtype} of {name}")
     else:
-        if t.dtype != like.dtype:
+        if t.dtype is not like.dtype:
             raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
-        if own[0] != shape[0] or own[2] != shape[2]:
+        if n != shape[0] or width != shape[2]:
             raise ValueError(f"{name} is {tuple(own)}, needs [{shape[0]}, heads, {shape[2]}]")
         if t.get_device() != like.get_device():
             raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    if heads is not None and own[1] != heads:
-        raise ValueError(f"{name} has {own[1]} heads, needs {heads}")
-    a, b, c = t.stride()
-    if c != 1 and own[2] != 1:
+    if heads is not None and many != heads:
+        raise ValueError(f"{name} has {many} heads, needs {heads}")
+    a, b, c = strides
+    if c != 1 and width != 1:
         raise ValueError(f"the elements of a head of {name} must be contiguous")
-    return own, (t.data_ptr(), a, b)
+    return (n, many, width), (t.data_ptr(), a, b)
 
 
 def _plain(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: int, dev: int, at_least: bool = False):
@@ -654,32 +655,45 @@ def _turn_args(dev, positions, inv_freq, w_q, w_k, eps, sections, interleaved, t
                  _plain(w_k, "w_k", torch.float32, dim, dev), eps, 1 if interleaved else 0)
 
 
-class _on:
-    """The device and stream a call works on: buffers made within belong to that stream, so that one
-    freed on return is not handed out again before the stream has passed the call."""
+class _Here:
+    """The calling thread's current stream on a device that is already the current one."""
 
-    __slots__ = ("_outer", "_raw")
+    __slots__ = ("raw",)
 
-    def __init__(self, device: torch.device, stream):
-        if device.type != "cuda":
-            raise ValueError("device tensors must be CUDA (HIP) tensors")
-        self._outer = None
-        if stream is not None:
-            self._outer = torch.cuda.stream(stream)
-            self._raw = stream.cuda_stream
-        else:
-            if torch.cuda.current_device() != device.index:
-                self._outer = torch.cuda.device(device)
-            self._raw = torch._C._cuda_getCurrentRawStream(device.index)
+    def __init__(self, raw: int):
+        self.raw = raw
 
     def __enter__(self) -> int:
-        if self._outer is not None:
-            self._outer.__enter__()
-        return self._raw
+        return self.raw
 
     def __exit__(self, *exc):
-        if self._outer is not None:
-            self._outer.__exit__(*exc)
+        pass
+
+
+class _There:
+    """Another stream or device: buffers made within belong to that stream, so that one freed on return is
+    not handed out again before the stream has passed the call."""
+
+    def __init__(self, outer, raw):
+        self.outer, self.raw = outer, raw
+
+    def __enter__(self) -> int:
+        self.outer.__enter__()
+        return self.raw()
+
+    def __exit__(self, *exc):
+        self.outer.__exit__(*exc)
+
+
+def _on(dev: int, where: torch.device, stream):
+    """The device and stream a call works on, as a context that gives the stream's handle."""
+    if dev < 0:
+        raise ValueError("device tensors must be CUDA (HIP) tensors")
+    if stream is not None:
+        return _There(torch.cuda.stream(stream), lambda: stream.cuda_stream)
+    if torch.cuda.current_device() != dev:
+        return _There(torch.cuda.device(where), lambda: torch.cuda.current_stream(where).cuda_stream)
+    return _Here(torch._C._cuda_getCurrentRawStream(dev))
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor],
@@ -697,11 +711,11 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
     rot, turn = _turn_args(dev, positions, inv_freq, w_q, w_k, eps, sections, interleaved, N, D)
     _plain(q_out, "q_out", dt, N * Hq * D, dev)
     _plain(k_out, "k_out", dt, N * Hk * D, dev)
-    with _on(where, stream) as s:
+    with _on(dev, where, stream) as s:
         if q_out is None:
-            q_out = torch.empty(shape, dtype=dt, device=where)
+            q_out = q.new_empty(shape)
         if k_out is None:
-            k_out = torch.empty((N, Hk, D), dtype=dt, device=where)
+            k_out = q.new_empty((N, Hk, D))
         _check(lib().dlrm_qk_norm_rope(N, Hq, Hk, D, rot, _TORCH_DT[dt], *qa, *ka, *turn, q_out.data_ptr(),
                                        k_out.data_ptr(), s), "dlrm_qk_norm_rope")
     return q_out, k_out
@@ -732,9 +746,9 @@ def qk_norm_rope_bwd(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: torch.Tens
     rot, turn = _turn_args(dev, positions, inv_freq, w_q, w_k, eps, sections, interleaved, N, D)
     need = qk_norm_rope_bwd_workspace_bytes(N, D, w_q is not None)
     _plain(workspace, "workspace", torch.uint8, need, dev, at_least=True)
-    with _on(where, stream) as s:
-        d_q = torch.empty(shape, dtype=dt, device=where)
-        d_k = torch.empty((N, Hk, D), dtype=dt, device=where)
+    with _on(dev, where, stream) as s:
+        d_q = q.new_empty(shape)
+        d_k = q.new_empty((N, Hk, D))
         d_w_q = d_w_k = None
         if w_q is not None:
             d_w_q = torch.empty(D, dtype=torch.float32, device=where)
@@ -803,9 +817,9 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     (S, page, pages, by_page, by_head, by_seq, width), (offsets_at, lens_at, table_at, status_at) = _paged_args(
         dt, dev, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk, D)
     _plain(q_out, "q_out", dt, N * Hq * D, dev)
-    with _on(where, stream) as s:
+    with _on(dev, where, stream) as s:
         if q is not None and q_out is None:
-            q_out = torch.empty((N, Hq, D), dtype=dt, device=where)
+            q_out = k.new_empty((N, Hq, D))
         _check(lib().dlrm_kv_append(N, S, Hq, Hk, D, rot, _TORCH_DT[dt], *qa, *ka, *va, *turn, offsets_at, lens_at,
                                     table_at, by_seq, width, page, pages, by_page, by_head, k_cache.data_ptr(),
                                     v_cache.data_ptr(), _ptr(q_out), status_at, s), "dlrm_kv_append")
@@ -847,11 +861,11 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, q_
     _plain(out, "out", dt, N * Hq * D, dev)
     _plain(lse, "lse", torch.float32, N * Hq, dev)
     _plain(workspace, "workspace", torch.uint8, need, dev, at_least=True)
-    with _on(where, stream) as s:
+    with _on(dev, where, stream) as s:
         if out is None:
-            out = torch.empty(shape, dtype=dt, device=where)
+            out = q.new_empty(shape)
         if lse is None and want_lse:
-            lse = torch.empty((N, Hq), dtype=torch.float32, device=where)
+            lse = q.new_empty((N, Hq), dtype=torch.float32)
         if workspace is None and need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=where)
         _check(lib().dlrm_paged_attn(N, S, Hq, Hk, D, _TORCH_DT[dt], *qa, k_cache.data_ptr(), v_cache.data_ptr(), page,
