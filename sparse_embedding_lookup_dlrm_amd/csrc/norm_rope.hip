@@ -15,29 +15,44 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// A head of D elements is D / (2 V) lanes of two 16-byte pieces (V elements each), chosen so that
-// the pairs of the rotation lie in one lane: lane p < rot / (2 V) holds pairs V p .. V p + V - 1,
-// the other lanes what is not rotated.
+// A head of D elements is D / (2 V) lanes of two 16-byte pieces (V elements each), chosen so that the
+// pairs of the rotation lie in one lane and each piece of neighbouring lanes is contiguous. Pairs of
+// neighbours: the two halves of the head. Pairs (j, j + rot / 2): lane p < rot / (2 V) holds pairs V p ..
+// V p + V - 1, the other lanes the halves of what is not rotated.
 template <int DT, int D>
 struct Split {
   static constexpr int V = Storage<DT>::per16;
   static constexpr int lanes = D / (2 * V);  // per head: 2 .. 32
   static constexpr int groups = kThreads / lanes;
-  int at[2];  // first element of each piece
-  bool rotated;
+  int at[2];        // first element of each piece
+  int pair[2];      // first pair of each piece (of both, unless neighbours)
+  bool rotated[2];
 
   __device__ __forceinline__ Split(int lane, int rot, bool interleaved) {
-    const int turned = rot / (2 * V);
-    rotated = lane < turned;
-    if (rotated && !interleaved) {
+    const int turned = interleaved ? 0 : rot / (2 * V), from = interleaved ? 0 : rot;
+    if (lane < turned) {
       at[0] = lane * V;
       at[1] = rot / 2 + lane * V;
-    } else {  // neighbours: 2 V elements in a row, also where nothing is rotated
-      at[0] = 2 * lane * V;
-      at[1] = at[0] + V;
+      pair[0] = pair[1] = lane * V;
+      rotated[0] = rotated[1] = true;
+    } else {
+      at[0] = from + (lane - turned) * V;
+      at[1] = at[0] + (D - from) / 2;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        pair[i] = at[i] / 2;
+        rotated[i] = interleaved && at[i] < rot;
+      }
     }
   }
 };
+
+// A 16-byte piece of a result, stored past the caches: nothing of a large call is read again before it
+// would have left them (training batch: 52 us, 67 through the caches; append of chunks: 56 and 73).
+__device__ __forceinline__ void put(char* to, const uint4& v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(to));
+}
 
 // cos and sin of the angles of tokens t0 .. t0 + count, [count][rot / 2] pairs in LDS.
 __device__ __forceinline__ void angles(const Rotation& r, long long t0, int count, float2* cs) {
@@ -55,20 +70,30 @@ __device__ __forceinline__ void angles(const Rotation& r, long long t0, int coun
   }
 }
 
-// x: V elements of piece 0, then V of piece 1. dir = 1 turns by the angles, -1 turns back.
-template <int V>
-__device__ __forceinline__ void rotate(float* x, const float2* cs, bool interleaved, float dir) {
+// x: V elements of piece 0, then V of piece 1; cs: the token's pairs. dir = 1 turns by the angles, -1
+// turns back.
+template <int DT, int D>
+__device__ __forceinline__ void rotate(float* x, const float2* cs, const Split<DT, D>& split, bool interleaved,
+                                       float dir) {
+  constexpr int V = Split<DT, D>::V;
   if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float c = cs[i].x, s = dir * cs[i].y, a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = a * c - b * s;
-      x[2 * i + 1] = a * s + b * c;
+    for (int p = 0; p < 2; ++p) {
+      if (!split.rotated[p]) continue;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        float* y = x + p * V + 2 * i;
+        const float2 w = cs[split.pair[p] + i];
+        const float c = w.x, s = dir * w.y, a = y[0], b = y[1];
+        y[0] = a * c - b * s;
+        y[1] = a * s + b * c;
+      }
     }
-  } else {
+  } else if (split.rotated[0]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float c = cs[i].x, s = dir * cs[i].y, a = x[i], b = x[V + i];
+      const float2 w = cs[split.pair[0] + i];
+      const float c = w.x, s = dir * w.y, a = x[i], b = x[V + i];
       x[i] = a * c - b * s;
       x[V + i] = a * s + b * c;
     }
@@ -157,7 +182,7 @@ struct Walk {
 #pragma unroll
           for (int i = 0; i < 2 * V; ++i) y[i] = y[i] * r * wv[i];
         }
-        if (split.rotated) rotate<V>(y, cs + t * pairs + lane * V, a.rope.interleaved, 1.f);
+        rotate<DT, D>(y, cs + t * pairs, split, a.rope.interleaved, 1.f);
         now[0] = narrow<DT>(y);
         now[1] = narrow<DT>(y + V);
       }
@@ -170,12 +195,12 @@ struct Walk {
         to = static_cast<char*>(out) + ((t0 + t) * heads + h) * D * Storage<DT>::bytes;
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(to + split.at[i] * Storage<DT>::bytes) = now[i];
+      for (int i = 0; i < 2; ++i) put(to + split.at[i] * Storage<DT>::bytes, now[i]);
     }
   }
 };
 
-constexpr int kMaxTokens = 8;  // tokens of a workgroup
+constexpr int kMaxTokens = 4;  // tokens of a workgroup
 
 // Cache slots of tokens t0 .. t0 + count, one wave each, the last wave first: the first ones have the
 // angles to form.
@@ -240,6 +265,9 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(NormRopeArgs a, int
 constexpr int kBwdGroups = 1024;  // workgroups that share the tokens; one row of partial weight gradients each
 constexpr int kBwdTokens = 4;     // tokens whose angles are held at once
 
+// One kind of head of the workgroup's tokens. (With loads an item ahead, or the next tokens' angles formed
+// beside, the kernel takes 166 registers and more, three waves to a SIMD instead of four: 104 .. 114 us for
+// the training batch against 100.)
 template <int DT, int D>
 __device__ __forceinline__ void walk_bwd(const NormRopeBwdArgs& a, const Heads& dy, const Heads& x, int heads,
                                          const float* w, long long t0, int count, const float2* cs, void* out,
@@ -261,7 +289,7 @@ __device__ __forceinline__ void walk_bwd(const NormRopeBwdArgs& a, const Heads& 
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       widen<DT>(*reinterpret_cast<const uint4*>(from + split.at[i] * Storage<DT>::bytes), g + i * V);
-    if (split.rotated) rotate<V>(g, cs + t * pairs + lane * V, a.rope.interleaved, -1.f);
+    rotate<DT, D>(g, cs + t * pairs, split, a.rope.interleaved, -1.f);
     if (w) {
       const char* in = head_at<DT>(x, t0 + t, h);
       float u[2 * V];
@@ -287,8 +315,7 @@ __device__ __forceinline__ void walk_bwd(const NormRopeBwdArgs& a, const Heads& 
     }
     char* to = static_cast<char*>(out) + ((t0 + t) * heads + h) * D * Storage<DT>::bytes;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<uint4*>(to + split.at[i] * Storage<DT>::bytes) = narrow<DT>(g + i * V);
+    for (int i = 0; i < 2; ++i) put(to + split.at[i] * Storage<DT>::bytes, narrow<DT>(g + i * V));
   }
 }
 
@@ -356,7 +383,7 @@ __global__ __launch_bounds__(kDwThreads) void norm_rope_dw_kernel(const float* _
 // Tokens of a workgroup: as many as leave four workgroups to each CU, so that the angles of a
 // token are shared by all its heads and small calls still spread over the chip.
 int tokens_per_group(long long n) {
-  long long t = n / 1024;
+    long long t = n / 1024;
   return static_cast<int>(t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t);
 }
 
