@@ -655,6 +655,11 @@ def _turn_args(dev, positions, inv_freq, w_q, w_k, eps, sections, interleaved, t
                  _plain(w_k, "w_k", torch.float32, dim, dev), eps, 1 if interleaved else 0)
 
 
+# The handle of a device's current stream without the Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 class _Here:
     """The calling thread's current stream on a device that is already the current one."""
 
@@ -693,7 +698,7 @@ def _on(dev: int, where: torch.device, stream):
         return _There(torch.cuda.stream(stream), lambda: stream.cuda_stream)
     if torch.cuda.current_device() != dev:
         return _There(torch.cuda.device(where), lambda: torch.cuda.current_stream(where).cuda_stream)
-    return _Here(torch._C._cuda_getCurrentRawStream(dev))
+    return _Here(_raw_stream(dev))
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor],

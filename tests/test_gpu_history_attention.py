@@ -235,3 +235,50 @@ def test_graph_replays():
         torch.cuda.synchronize()
         for a, b in zip(got, eager):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("D,Hq,Hk", [(32, 2, 1), (64, 2, 2), (128, 4, 2), (256, 2, 1)])
+def test_one_workgroup_over_a_long_history(D, Hq, Hk, t):
+    """With a hint of one entry nothing is split: a workgroup takes 9001 entries, past the pages it holds at
+    a time, one of them bad."""
+    h = History([1, 20], [9001, 4300], Hq, Hk, D, 16, t, seed=D)
+    h.page_table[0, 530] = 10 ** 6
+    h.page_table[1, 201] = -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = ops.paged_attn(*h.args(), max_q=1, max_kv=1, want_lse=True, status=status)
+    assert status.item() == ops.STATUS_BAD_PAGE
+    check(h, got=got)
+    got = ops.paged_attn(*h.args(), max_q=20 * 16, max_kv=1, want_lse=True, status=status)
+    check(h, got=got)
+
+
+def test_more_sequences_than_a_grid_dimension():
+    """70,001 sequences of one entry: the result is the entry's value; and 5,003 with gaps in the append."""
+    S, D = 70_001, 32
+    k, v = (torch.randn((S, 1, 16, D), device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((S, 1, D), device="cuda").to(torch.bfloat16)
+    i32 = lambda x: x.to(device="cuda", dtype=torch.int32)
+    table = i32(torch.randperm(S))[:, None]
+    out, lse = ops.paged_attn(q, k, v, i32(torch.arange(S + 1)), i32(torch.ones(S)), table.contiguous(), want_lse=True,
+                              max_q=1, max_kv=1)
+    assert torch.equal(out[:, 0], v[table[:, 0].long(), 0, 0])
+    want = (q[:, 0].double() * k[table[:, 0].long(), 0, 0].double()).sum(1) * D ** -0.5
+    size = (q[:, 0].double() * k[table[:, 0].long(), 0, 0].double()).abs().sum(1) * D ** -0.5
+    assert ((lse[:, 0].double() - want).abs() <= (D + 16) * 2.0 ** -24 * (size + 1)).all()
+
+    S, rng = 5003, np.random.default_rng(0)
+    lens = torch.from_numpy(rng.integers(0, 3, S))
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    N = int(off[-1])
+    kn, vn = rand((N, 1, D), "bf16", 1).cuda(), rand((N, 1, D), "bf16", 2).cuda()
+    k[:], v[:] = 0, 0
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ops.kv_append(kn, vn, k, v, i32(off), i32(lens + 5), table[:S], status=status)
+    seq = torch.repeat_interleave(torch.arange(S), lens)
+    slot = 5 + torch.arange(N) - off[seq]
+    at = table[:S, 0].long().cpu()[seq].cuda()
+    assert status.item() == 0
+    assert torch.equal(k[at, :, slot.cuda()], kn) and torch.equal(v[at, :, slot.cuda()], vn)
+    k[at, :, slot.cuda()] = 0
+    assert not k.any()
