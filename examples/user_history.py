@@ -49,19 +49,21 @@ class HistoryCache:
             table[i, :len(self.pages[u])] = torch.tensor(self.pages[u], dtype=torch.int32)
         offsets = torch.tensor([0] + list(rows)).cumsum(0).to(torch.int32)
         lens = torch.tensor([self.held[u] for u in users], dtype=torch.int32)
-        return (offsets.to(dev), lens.to(dev), table.to(dev)), dict(max_q=max(rows), max_kv=max(self.held[u] for u in users))
+        most = dict(max_q=max(rows), max_kv=max(self.held[u] for u in users))
+        return (offsets.to(dev), lens.to(dev), table.to(dev)), most
 
 
 class HistoryEncoder:
     """One attention layer over item embeddings: a joint projection, per-head norms, and a rotation whose first
     pairs turn by the event's place in the history and whose last ones by its hour."""
 
-    def __init__(self, items: int, width: int, q_heads: int, kv_heads: int, dim: int, dtype=torch.bfloat16, device="cuda",
-                 seed: int = 0):
+    def __init__(self, items: int, width: int, q_heads: int, kv_heads: int, dim: int, dtype=torch.bfloat16,
+                 device="cuda", seed: int = 0):
         g = torch.Generator().manual_seed(seed)
         self.q_heads, self.kv_heads, self.dim = q_heads, kv_heads, dim
         self.items = torch.randn((items, width), generator=g).to(device, dtype)
-        self.proj = (torch.randn((width, (q_heads + 2 * kv_heads) * dim), generator=g) * width ** -0.5).to(device, dtype)
+        proj = torch.randn((width, (q_heads + 2 * kv_heads) * dim), generator=g) * width ** -0.5
+        self.proj = proj.to(device, dtype)
         self.w_q = torch.ones(dim, device=device)
         self.w_k = torch.ones(dim, device=device)
         pairs = dim // 2
@@ -114,7 +116,8 @@ def main() -> None:
     dev = "cuda"
     enc = HistoryEncoder(items=10_000, width=128, q_heads=8, kv_heads=2, dim=64)
     users = 6
-    cache = HistoryCache(users, pages=256, kv_heads=2, page=16, dim=64, max_events=512, dtype=torch.bfloat16, device=dev)
+    cache = HistoryCache(users, pages=256, kv_heads=2, page=16, dim=64, max_events=512, dtype=torch.bfloat16,
+                         device=dev)
     g = torch.Generator().manual_seed(1)
     past = [200, 3, 77, 120, 1, 64]
     ids = torch.randint(0, 10_000, (sum(past),), generator=g, dtype=torch.int32).to(dev)

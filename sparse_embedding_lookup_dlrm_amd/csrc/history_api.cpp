@@ -73,7 +73,8 @@ int check_paged(int64_t n, int32_t seqs, int32_t kv_heads, int32_t dim, int dtyp
                 int32_t page, int64_t num_pages, int64_t page_stride, int64_t head_stride, const void* k_cache,
                 const void* v_cache, int32_t* status, Paged* p) {
   if (seqs < 0 || (n > 0 && (!q_offsets || (seqs > 0 && !kv_lens)))) return DLRM_E_INVAL;
-  if (seqs >= kI32Max || table_width < 0 || table_stride < 0 || num_pages < 0 || num_pages > kI32Max) return DLRM_E_INVAL;
+  if (seqs >= kI32Max || table_width < 0 || table_stride < 0 || num_pages < 0 || num_pages > kI32Max)
+    return DLRM_E_INVAL;
   if (n > 0 && seqs > 0 && table_width > 0 && !page_table) return DLRM_E_INVAL;
   if (n > 0 && num_pages > 0 && (!k_cache || !v_cache)) return DLRM_E_INVAL;
   if (page < 16 || page > 65536 || (page & (page - 1))) return DLRM_E_UNSUPPORTED;

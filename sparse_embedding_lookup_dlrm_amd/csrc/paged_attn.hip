@@ -47,10 +47,11 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 template <int DT>
 __device__ __forceinline__ f32x4 mfma16_half(const uint2& a, const uint2& b, const f32x4& c) {
   if constexpr (DT == DLRM_BF16)
-    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0, 0,
-                                                     0);
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0,
+                                                     0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, a), __builtin_bit_cast(f16x4, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, a), __builtin_bit_cast(f16x4, b), c, 0, 0,
+                                                 0);
 }
 
 // All bits of those of the two 16-bit values of a dword that are infinite or NaN.
@@ -363,7 +364,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Cut 
               if constexpr (TT == 1)
                 sum = mfma16_half<DT>(make_uint2(vt[0], vt[1]), make_uint2(pw[0][0], pw[0][1]), sum);
               else
-                sum = mfma16<DT>(vt, u32x4{pw[t][0], pw[t][1], pw[t + 1 < TT ? t + 1 : t][0], pw[t + 1 < TT ? t + 1 : t][1]}, sum);
+                sum = mfma16<DT>(vt, u32x4{pw[t][0], pw[t][1], pw[t + 1][0], pw[t + 1][1]}, sum);
             }
             if (mine) o[e] = sum;
           }
@@ -465,6 +466,13 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Cut 
 // A row of D elements is D / 8 pieces of 16 bytes; piece c of entry r lies at place c ^ swizzle(r),
 // so that the lanes that LDS serves together fall on different banks. The copy to LDS writes places
 // in order and picks the piece for each.
+//
+// Bound by LDS: a piece of keys or values feeds one matrix instruction of 32 clocks and is 1 KB, so four
+// SIMDs ask for 128 bytes a clock where LDS gives 64 (147 bytes/ns a CU measured): the matrix units are at
+// 45 %. Four chunks of up to 2048 new tokens over up to 8192 entries, 32 heads of 128: 280 us, 957 TFLOP/s.
+// Two blocks of 32 rows to a wave halve the reads, but leave one wave to a SIMD, whose exponentials then
+// stand beside idle matrix units: 357 .. 550 us. Scores of the next tile formed beside this one's
+// exponentials: 307 .. 335 us, for the registers. Priorities around the matrix instructions: no difference.
 // ---------------------------------------------------------------------------
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -571,8 +579,8 @@ __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs 
     const int32_t* table = pg.page_table + seq * pg.table_stride;
 
     // the last rows of a causal chunk see the most: they start first
-    for (long long first_row = static_cast<long long>(cut.q_tiles - 1 - blockIdx.y / cut.splits) * Rows; first_row < rows;
-         first_row += static_cast<long long>(cut.q_tiles) * Rows) {
+    for (long long first_row = static_cast<long long>(cut.q_tiles - 1 - blockIdx.y / cut.splits) * Rows;
+         first_row < rows; first_row += static_cast<long long>(cut.q_tiles) * Rows) {
       const int row0 = static_cast<int>(first_row), row_end = rows - row0 > Rows ? row0 + Rows : rows;
       const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut);
       if (split >= rc.parts) continue;
@@ -689,98 +697,100 @@ __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs 
           special = __syncthreads_or(found) != 0;
         }
 
+        // pieces of keys and values are read KW and VW ahead of the matrix unit
         constexpr int KW = Q < 8 ? Q : 8, VW = 2 * T * C < 8 ? 2 * T * C : 8;
 #pragma unroll 1
         for (int p0 = 0; p0 < K; p0 += Part) {
-        if (k0 + p0 >= w_hi || k0 + p0 + Part <= w_lo) continue;  // this wave's rows see none of these entries
-        const auto key_frag = [&](int t, int i) {
-          const int r = p0 + 32 * t + c32, place = (2 * i + h) ^ key_swizzle<D>(r);
-          return *reinterpret_cast<const u32x4*>(lds_k[buf] + r * D + place * 8);
-        };
-        f32x16 s[T];
-        // pieces of keys and values are read KW and VW ahead of the matrix unit
-        u32x4 kf[KW];
+          if (k0 + p0 >= w_hi || k0 + p0 + Part <= w_lo) continue;  // this wave's rows see none of these entries
+          const auto key_frag = [&](int t, int i) {
+            const int r = p0 + 32 * t + c32, place = (2 * i + h) ^ key_swizzle<D>(r);
+            return *reinterpret_cast<const u32x4*>(lds_k[buf] + r * D + place * 8);
+          };
+          f32x16 s[T];
+          u32x4 kf[KW];
 #pragma unroll
-        for (int i = 0; i < KW; ++i) kf[i] = key_frag(i / Q, i % Q);
+          for (int i = 0; i < KW; ++i) kf[i] = key_frag(i / Q, i % Q);
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
+          for (int t = 0; t < T; ++t) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) s[t][r] = 0.f;
+            for (int r = 0; r < 16; ++r) s[t][r] = 0.f;
 #pragma unroll
-          for (int i = 0; i < Q; ++i) {
-            const int n = t * Q + i, ahead = n + KW;
-            s[t] = mfma32<DT>(kf[n % KW], qf[i], s[t]);
-            if (ahead < T * Q) kf[n % KW] = key_frag(ahead / Q, ahead % Q);
+            for (int i = 0; i < Q; ++i) {
+              const int n = t * Q + i, ahead = n + KW;
+              s[t] = mfma32<DT>(kf[n % KW], qf[i], s[t]);
+              if (ahead < T * Q) kf[n % KW] = key_frag(ahead / Q, ahead % Q);
+            }
           }
-        }
-        if (k0 + p0 < w_all_lo || k0 + p0 + Part > w_all_hi || k0 + p0 + Part > hi || good != kAllGood) {
+          const int part0 = k0 + p0, part1 = part0 + Part;
+          if (part0 < w_all_lo || part1 > w_all_hi || part1 > hi || good != kAllGood) {
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) {
+                const int e = p0 + 32 * t + 8 * (r / 4) + 4 * h + r % 4, key = k0 + e;
+                if (key < row_lo || key >= row_hi || key >= hi || !(good >> (e / 16) & 1)) s[t][r] = -INFINITY;
+              }
+          }
+
+          // V^T of 16 entries (step) and 32 elements (piece): entries 4 h .. and 8 + 4 h .. of the step
+          const auto value_frag = [&](int step, int piece) {
+            u32x4 w;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const int r = p0 + 16 * step + 8 * n + 4 * h + (lane & 15) / 4;
+              const int place =
+                  ((half * C + piece) * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1)) ^ value_swizzle<D>(r);
+              const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                  (__attribute__((address_space(3))) s16x4*)(lds_v[buf] + r * D + place * 8 + (lane & 1) * 4));
+              const uint2 u = __builtin_bit_cast(uint2, x);
+              w[2 * n] = u.x;
+              w[2 * n + 1] = u.y;
+            }
+            return w;
+          };
+          u32x4 vf[VW];
+#pragma unroll
+          for (int i = 0; i < VW; ++i) vf[i] = value_frag(i / C, i % C);
+
+          float top = s[0][0];
 #pragma unroll
           for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const int e = p0 + 32 * t + 8 * (r / 4) + 4 * h + r % 4, key = k0 + e;
-              if (key < row_lo || key >= row_hi || key >= hi || !(good >> (e / 16) & 1)) s[t][r] = -INFINITY;
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
+          top = max_halves(top);
+          const float next = fmaxf(m, top);
+          // O and l stay relative to an older maximum until a row's grows by 2^8: weights are then at most
+          // 2^8 (fp16: 2^15 with its lift)
+          if (__any((next - m) * c > (DT == DLRM_F16 ? 7.f : 8.f))) {
+            const float keep = m == -INFINITY ? 0.f : exp2f((m - next) * c);
+            m = next;
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) o[i][r] *= keep;
+          }
+          const float base = m == -INFINITY ? 0.f : m * c - kLift<DT>;
+          u32x4 pw[2 * T];
+          float sum[4] = {};
+#pragma unroll
+          for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+              const float p_0 = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -base));
+              const float p_1 = __builtin_amdgcn_exp2f(fmaf(s[t][r + 1], c, -base));
+              sum[r % 4] += p_0;
+              sum[r % 4 + 1] += p_1;
+              pw[2 * t + r / 8][r % 8 / 2] = pack2<DT>(p_0, p_1);
             }
-        }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 
-        // V^T of 16 entries (step) and 32 elements (piece): entries 4 h .. and 8 + 4 h .. of the step
-        const auto value_frag = [&](int step, int piece) {
-          u32x4 w;
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int r = p0 + 16 * step + 8 * n + 4 * h + (lane & 15) / 4;
-            const int place = ((half * C + piece) * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1)) ^ value_swizzle<D>(r);
-            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)(lds_v[buf] + r * D + place * 8 + (lane & 1) * 4));
-            const uint2 u = __builtin_bit_cast(uint2, x);
-            w[2 * n] = u.x;
-            w[2 * n + 1] = u.y;
+          for (int n = 0; n < 2 * T * C; ++n) {
+            o[n % C] = mfma32<DT>(vf[n % VW], pw[n / C], o[n % C]);
+            if (n + VW < 2 * T * C) vf[n % VW] = value_frag((n + VW) / C, (n + VW) % C);
           }
-          return w;
-        };
-        u32x4 vf[VW];
-#pragma unroll
-        for (int i = 0; i < VW; ++i) vf[i] = value_frag(i / C, i % C);
-
-        float top = s[0][0];
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
-        top = max_halves(top);
-        const float next = fmaxf(m, top);
-        // O and l stay relative to an older maximum until a row's grows by 2^8: weights are then at most
-        // 2^8 (fp16: 2^15 with its lift)
-        if (__any((next - m) * c > (DT == DLRM_F16 ? 7.f : 8.f))) {
-          const float keep = m == -INFINITY ? 0.f : exp2f((m - next) * c);
-          m = next;
-          l *= keep;
-#pragma unroll
-          for (int i = 0; i < C; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) o[i][r] *= keep;
         }
-        const float base = m == -INFINITY ? 0.f : m * c - kLift<DT>;
-        u32x4 pw[2 * T];
-        float sum[4] = {};
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; r += 2) {
-            const float p0 = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -base));
-            const float p1 = __builtin_amdgcn_exp2f(fmaf(s[t][r + 1], c, -base));
-            sum[r % 4] += p0;
-            sum[r % 4 + 1] += p1;
-            pw[2 * t + r / 8][r % 8 / 2] = pack2<DT>(p0, p1);
-          }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-
-#pragma unroll
-        for (int n = 0; n < 2 * T * C; ++n) {
-          o[n % C] = mfma32<DT>(vf[n % VW], pw[n / C], o[n % C]);
-          if (n + VW < 2 * T * C) vf[n % VW] = value_frag((n + VW) / C, (n + VW) % C);
-        }
-        }  // parts
 
         if (special) {
 #pragma unroll 1
@@ -788,7 +798,8 @@ __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs 
             const int key = k0 + e;
             const int page = key < hi ? scalar_load(table, key >> pg.page_shift) : -1;
             if (page < 0 || page >= pg.num_pages) continue;
-            const uint16_t* v = vh + page * pg.page_stride + static_cast<long long>(key & page_mask) * D + half * 32 * C + 4 * h;
+            const uint16_t* v =
+                vh + page * pg.page_stride + static_cast<long long>(key & page_mask) * D + half * 32 * C + 4 * h;
             const bool mine = key >= row_lo && key < row_hi;
 #pragma unroll
             for (int i = 0; i < 4 * C; ++i) {
@@ -916,10 +927,10 @@ int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
 
 // Where the workgroups of a call would not fill the chip, or histories may be of unequal length, every
 // history is split into parts.
-// Rows kernel: parts of 128 KB of keys and as much of values (64 histories of up to 16k entries of 128:
+// Rows kernel: parts of 256 KB of keys and as much of values (64 histories of up to 16k entries of 128:
 // 224 us; with half as much 231 us, with twice 242 us), smaller ones of at least 512 entries where that
-// leaves fewer than 512 workgroups, and at most 16k workgroups. One history of 131k: 33 us; with parts of
-// 256 entries 40 us.
+// leaves fewer than 256 workgroups, and at most 16k workgroups. One history of 131k and two heads: 30.7 us in
+// parts of 1024, 32.8 in 512, 40 in 256.
 // Tile kernel: twice as many workgroups as there are places, in parts of at least 512 entries. 24 sequences
 // of up to 257 x 1500, 288 workgroups: 22.9 us against 29 unsplit; 8 sequences of 32 tokens over up to 32k:
 // 56 us, 71 with as many as places; but 432 workgroups of 256-wide heads, one to a CU: 81 us unsplit against
@@ -935,11 +946,12 @@ Cut cut_call(long long max_rows, int seqs, int kv_heads, int dim, int causal, in
   c.q_tiles = static_cast<int>(tiles);
   const long long whole = tiles * seqs * kv_heads;
   long long span = max_kv > 0 ? max_kv : 1;
-  if (causal && window && span > static_cast<long long>(window) + max_q + 32) span = static_cast<long long>(window) + max_q + 32;
+  const long long seen = static_cast<long long>(window) + max_q + 32;
+  if (causal && window && span > seen) span = seen;
   long long splits;
   const long long units = whole > 0 ? whole : 1;
   if (rows == 16) {
-    const long long least = 131072 / dim, fill = 512 / units, finest = (span + 511) / 512, most = 16384 / units;
+    const long long least = 131072 / dim, fill = 256 / units, finest = (span + 511) / 512, most = 16384 / units;
     splits = (span + least - 1) / least;
     if (splits < fill) splits = fill < finest ? fill : finest;
     if (splits > most) splits = most;
@@ -981,7 +993,7 @@ hipError_t run(const AttnArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((attn_rows_kernel<DT, D>), grid, dim3(kThreads), 0, s, a, cut);
   else
     hipLaunchKernelGGL((attn_tile_kernel<DT, D>), grid, dim3(kTileThreads<D>), 0, s, a, cut);
-  if (cut.splits > 16)
+  if (cut.splits > 32)
     join<DT, D, kThreads / (D / 8)>(a, cut, tile, s);
   else if (cut.splits > 1)
     join<DT, D, 1>(a, cut, tile, s);
@@ -1003,9 +1015,8 @@ hipError_t run_dim(const AttnArgs& a, hipStream_t s) {
 size_t attn_workspace(int64_t n, int seqs, int q_heads, int kv_heads, int dim, int causal, int window, int max_q,
                       int max_kv) {
   if (n == 0 || seqs == 0) return 0;
-  return cut_bytes(cut_call(static_cast<long long>(max_q) * (q_heads / kv_heads), seqs, kv_heads, dim, causal, window, max_q,
-                            max_kv),
-                   n, q_heads, dim);
+  const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
+  return cut_bytes(cut_call(rows, seqs, kv_heads, dim, causal, window, max_q, max_kv), n, q_heads, dim);
 }
 
 hipError_t launch_paged_attn(const AttnArgs& a, hipStream_t s) {
