@@ -608,7 +608,8 @@ def _heads_of(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None, s
     a, b, c = strides
     if c != 1 and width != 1:
         raise ValueError(f"the elements of a head of {name} must be contiguous")
-    return (n, many, width), (t.data_ptr(), a, b)
+    # a stride over one token or head is never taken, and may be any number
+    return (n, many, width), (t.data_ptr(), a if n > 1 else 0, b if many > 1 else 0)
 
 
 def _plain(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: int, dev: int, at_least: bool = False):

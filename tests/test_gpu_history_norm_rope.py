@@ -134,6 +134,18 @@ def test_far_and_negative_positions():
     close(qo, ref, norm_rope_tol("f32", ref, mag) + 2.0 ** -21 * mag, "q")
 
 
+def test_strides_of_single_tokens_and_heads_are_not_looked_at():
+    base = rand((5 * 64,), "bf16", 1).cuda()
+    a = base.as_strided((5, 1, 64), (64, 3, 1))
+    b = base.as_strided((1, 5, 64), (7, 64, 1))
+    pos, freq = torch.arange(5, dtype=torch.int32, device="cuda"), torch.rand(32, device="cuda")
+    qa, ka = ops.qk_norm_rope(a, a, pos, freq)
+    qc, _ = ops.qk_norm_rope(a.contiguous(), a.contiguous(), pos, freq)
+    assert torch.equal(qa, qc) and torch.equal(ka, qc)
+    qb, _ = ops.qk_norm_rope(b, b, pos[:1], freq)
+    assert torch.equal(qb, ops.qk_norm_rope(b.contiguous(), b.contiguous(), pos[:1], freq)[0])
+
+
 def test_nan_and_infinity_stay_in_their_head():
     q, k = rand((4, 4, 64), "bf16", 1), rand((4, 2, 64), "bf16", 2)
     q[1, 2, 5], q[3, 0, 0] = float("nan"), float("inf")
