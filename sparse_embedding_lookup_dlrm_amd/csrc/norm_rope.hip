@@ -54,6 +54,15 @@ __device__ __forceinline__ void put(char* to, const uint4& v) {
   __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(to));
 }
 
+// A 16-byte piece of an input; Far: past the caches.
+template <bool Far>
+__device__ __forceinline__ uint4 get(const char* from) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  if constexpr (!Far) return *reinterpret_cast<const uint4*>(from);
+  const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // cos and sin of the angles of tokens t0 .. t0 + count, [count][rot / 2] pairs in LDS.
 __device__ __forceinline__ void angles(const Rotation& r, long long t0, int count, float2* cs) {
   const int pairs = r.rot / 2;
@@ -268,7 +277,7 @@ constexpr int kBwdTokens = 4;     // tokens whose angles are held at once
 // One kind of head of the workgroup's tokens. (With loads an item ahead, or the next tokens' angles formed
 // beside, the kernel takes 166 registers and more, three waves to a SIMD instead of four: 104 .. 114 us for
 // the training batch against 100.)
-template <int DT, int D>
+template <int DT, int D, bool Far>
 __device__ __forceinline__ void walk_bwd(const NormRopeBwdArgs& a, const Heads& dy, const Heads& x, int heads,
                                          const float* w, long long t0, int count, const float2* cs, void* out,
                                          float* dw) {
@@ -288,14 +297,14 @@ __device__ __forceinline__ void walk_bwd(const NormRopeBwdArgs& a, const Heads& 
     float g[2 * V];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      widen<DT>(*reinterpret_cast<const uint4*>(from + split.at[i] * Storage<DT>::bytes), g + i * V);
+      widen<DT>(get<Far>(from + split.at[i] * Storage<DT>::bytes), g + i * V);
     rotate<DT, D>(g, cs + t * pairs, split, a.rope.interleaved, -1.f);
     if (w) {
       const char* in = head_at<DT>(x, t0 + t, h);
       float u[2 * V];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        widen<DT>(*reinterpret_cast<const uint4*>(in + split.at[i] * Storage<DT>::bytes), u + i * V);
+        widen<DT>(get<Far>(in + split.at[i] * Storage<DT>::bytes), u + i * V);
       float sq = 0.f, dot = 0.f;
 #pragma unroll
       for (int i = 0; i < 2 * V; ++i) {
@@ -338,7 +347,7 @@ __device__ __forceinline__ void join(const Rotation& rope, const float* dw, floa
   for (int d = threadIdx.x; d < D; d += kThreads) row[d] = lds[d] + lds[D + d] + lds[2 * D + d] + lds[3 * D + d];
 }
 
-template <int DT, int D>
+template <int DT, int D, bool Far>
 __global__ __launch_bounds__(kThreads) void norm_rope_bwd_kernel(NormRopeBwdArgs a) {
   constexpr int V = Storage<DT>::per16;
   __shared__ float2 cs[kBwdTokens * D / 2];
@@ -350,8 +359,8 @@ __global__ __launch_bounds__(kThreads) void norm_rope_bwd_kernel(NormRopeBwdArgs
     __syncthreads();  // the angles of the tokens before are no longer read
     angles(a.rope, t0, count, cs);
     __syncthreads();
-    walk_bwd<DT, D>(a, a.dq_out, a.q, a.q_heads, a.w_q, t0, count, cs, a.d_q, dq);
-    walk_bwd<DT, D>(a, a.dk_out, a.k, a.kv_heads, a.w_k, t0, count, cs, a.d_k, dk);
+    walk_bwd<DT, D, Far>(a, a.dq_out, a.q, a.q_heads, a.w_q, t0, count, cs, a.d_q, dq);
+    walk_bwd<DT, D, Far>(a, a.dk_out, a.k, a.kv_heads, a.w_k, t0, count, cs, a.d_k, dk);
   }
   if (a.w_q) {
     float* row = a.partials + static_cast<long long>(blockIdx.x) * 2 * D;
@@ -413,7 +422,13 @@ int bwd_groups(long long n) {
 template <int DT, int D>
 hipError_t run_bwd(const NormRopeBwdArgs& a, hipStream_t s) {
   const int groups = bwd_groups(a.n);
-  if (groups > 0) hipLaunchKernelGGL((norm_rope_bwd_kernel<DT, D>), dim3(groups), dim3(kThreads), 0, s, a);
+  // Inputs of more than the 256 MB of the last cache are read past the caches (500 MB in all: 94 us against
+  // 100); smaller ones may still lie there from the kernels that made them (250 MB: 50 us against 54).
+  const double read = static_cast<double>(a.n) * (a.q_heads + a.kv_heads) * D * Storage<DT>::bytes * (a.w_q ? 2 : 1);
+  if (groups > 0 && read > 256e6)
+    hipLaunchKernelGGL((norm_rope_bwd_kernel<DT, D, true>), dim3(groups), dim3(kThreads), 0, s, a);
+  else if (groups > 0)
+    hipLaunchKernelGGL((norm_rope_bwd_kernel<DT, D, false>), dim3(groups), dim3(kThreads), 0, s, a);
   if (a.w_q)
     hipLaunchKernelGGL(norm_rope_dw_kernel, dim3(2 * D / 32), dim3(kDwThreads), 0, s, a.partials, groups, D, a.d_w_q,
                        a.d_w_k);

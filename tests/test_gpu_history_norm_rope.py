@@ -234,3 +234,22 @@ def test_append_into_a_layer_of_a_larger_cache_and_padded_tokens():
         assert torch.equal(big_k[at], k[n]) and torch.equal(big_v[at], v[n])
         big_k[at], big_v[at] = 0, 0
     assert not big_k.any() and not big_v.any()
+
+
+def test_backward_of_more_than_the_caches_hold():
+    """Inputs past 256 MB are read another way: the same bits as the same tokens in two smaller calls, the
+    weight gradients the sum of theirs."""
+    N, Hq, Hk, D = 16384, 32, 8, 128
+    g = torch.Generator("cuda").manual_seed(0)
+    q, dq = (torch.randn((N, Hq, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    k, dk = (torch.randn((N, Hk, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    r = Rope(N, D, 128, 1, True, seed=0)
+    pos, freq, w_q, w_k = r.dev()
+    whole = ops.qk_norm_rope_bwd(dq, dk, q, k, pos, freq, w_q, w_k)
+    a, b = (ops.qk_norm_rope_bwd(dq[c], dk[c], q[c], k[c], pos[:, c], freq, w_q, w_k)
+            for c in (slice(0, N // 2), slice(N // 2, N)))
+    for i in (0, 1):
+        assert torch.equal(whole[i], torch.cat([a[i], b[i]]))
+    for i, many in ((2, N * Hq), (3, N * Hk)):
+        # each side is off by a few u of the sum of sizes, about many; lanes add at most 64 terms in a row
+        assert ((whole[i] - a[i] - b[i]).abs() <= 2 * 80 * U * many).all()
