@@ -616,8 +616,7 @@ def _plain(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: int,
     """Checks a contiguous tensor's dtype, size and device; returns its address, None for None."""
     if t is None:
         return None
-    n = t.numel()
-    if t.dtype != dtype or ((n < numel) if at_least else (n != numel)):
+    if t.dtype is not dtype or t.numel() != numel:
         _expect(t, name, dtype, numel, at_least)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -659,6 +658,7 @@ def _turn_args(dev, positions, inv_freq, w_q, w_k, eps, sections, interleaved, t
 # The handle of a device's current stream without the Stream object around it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 class _Here:
@@ -695,11 +695,11 @@ def _on(dev: int, where: torch.device, stream):
     """The device and stream a call works on, as a context that gives the stream's handle."""
     if dev < 0:
         raise ValueError("device tensors must be CUDA (HIP) tensors")
-    if stream is not None:
-        return _There(torch.cuda.stream(stream), lambda: stream.cuda_stream)
-    if torch.cuda.current_device() != dev:
+    if stream is None:
+        if _current_device() == dev:
+            return _Here(_raw_stream(dev))
         return _There(torch.cuda.device(where), lambda: torch.cuda.current_stream(where).cuda_stream)
-    return _Here(_raw_stream(dev))
+    return _There(torch.cuda.stream(stream), lambda: stream.cuda_stream)
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor],
@@ -715,13 +715,15 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
     N, Hq, D = shape
     dt, dev, where = q.dtype, q.get_device(), q.device
     rot, turn = _turn_args(dev, positions, inv_freq, w_q, w_k, eps, sections, interleaved, N, D)
-    _plain(q_out, "q_out", dt, N * Hq * D, dev)
-    _plain(k_out, "k_out", dt, N * Hk * D, dev)
+    if q_out is not None:
+        _plain(q_out, "q_out", dt, N * Hq * D, dev)
+    if k_out is not None:
+        _plain(k_out, "k_out", dt, N * Hk * D, dev)
     with _on(dev, where, stream) as s:
         if q_out is None:
-            q_out = q.new_empty(shape)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if k_out is None:
-            k_out = q.new_empty((N, Hk, D))
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         _check(lib().dlrm_qk_norm_rope(N, Hq, Hk, D, rot, _TORCH_DT[dt], *qa, *ka, *turn, q_out.data_ptr(),
                                        k_out.data_ptr(), s), "dlrm_qk_norm_rope")
     return q_out, k_out
@@ -751,10 +753,11 @@ def qk_norm_rope_bwd(d_q_out: torch.Tensor, d_k_out: torch.Tensor, q: torch.Tens
     dt, dev, where = q.dtype, q.get_device(), q.device
     rot, turn = _turn_args(dev, positions, inv_freq, w_q, w_k, eps, sections, interleaved, N, D)
     need = qk_norm_rope_bwd_workspace_bytes(N, D, w_q is not None)
-    _plain(workspace, "workspace", torch.uint8, need, dev, at_least=True)
+    if workspace is not None:
+        _plain(workspace, "workspace", torch.uint8, need, dev, at_least=True)
     with _on(dev, where, stream) as s:
-        d_q = q.new_empty(shape)
-        d_k = q.new_empty((N, Hk, D))
+        d_q = torch.empty_like(q, memory_format=torch.contiguous_format)
+        d_k = torch.empty_like(k, memory_format=torch.contiguous_format)
         d_w_q = d_w_k = None
         if w_q is not None:
             d_w_q = torch.empty(D, dtype=torch.float32, device=where)
@@ -786,10 +789,11 @@ def _paged_args(dtype, dev: int, k_cache, v_cache, q_offsets, kv_lens, page_tabl
     if width > 1 and by_entry != 1:
         raise ValueError("the entries of a row of page_table must be contiguous")
     where = (_plain(q_offsets, "q_offsets", torch.int32, S + 1, dev), _plain(kv_lens, "kv_lens", torch.int32, S, dev),
-             page_table.data_ptr(), _plain(status, "status", torch.int32, 1, dev, at_least=True))
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("page_table", page_table)):
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, not on device {dev}")
+             page_table.data_ptr(),
+             None if status is None else _plain(status, "status", torch.int32, 1, dev, at_least=True))
+    if k_cache.get_device() != dev or v_cache.get_device() != dev or page_table.get_device() != dev:
+        raise ValueError(f"the caches and page_table must be on device {dev}, are on {k_cache.device}, "
+                         f"{v_cache.device} and {page_table.device}")
     if shape[0] > 0 and (strides[2] != D or strides[3] != 1):
         raise ValueError("a page's entries of a head must be contiguous in the caches")
     return (S, shape[2], shape[0], strides[0], strides[1], by_seq, width), where
@@ -822,10 +826,11 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         turn = turn[:5] + (None,) + turn[6:]
     (S, page, pages, by_page, by_head, by_seq, width), (offsets_at, lens_at, table_at, status_at) = _paged_args(
         dt, dev, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk, D)
-    _plain(q_out, "q_out", dt, N * Hq * D, dev)
+    if q_out is not None:
+        _plain(q_out, "q_out", dt, N * Hq * D, dev)
     with _on(dev, where, stream) as s:
         if q is not None and q_out is None:
-            q_out = k.new_empty((N, Hq, D))
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         _check(lib().dlrm_kv_append(N, S, Hq, Hk, D, rot, _TORCH_DT[dt], *qa, *ka, *va, *turn, offsets_at, lens_at,
                                     table_at, by_seq, width, page, pages, by_page, by_head, k_cache.data_ptr(),
                                     v_cache.data_ptr(), _ptr(q_out), status_at, s), "dlrm_kv_append")
@@ -864,12 +869,15 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, q_
     if scale is None:
         scale = D ** -0.5 if D > 0 else 1.0
     need = paged_attn_workspace_bytes(N, S, Hq, Hk, D, causal, window, max_q, max_kv)
-    _plain(out, "out", dt, N * Hq * D, dev)
-    _plain(lse, "lse", torch.float32, N * Hq, dev)
-    _plain(workspace, "workspace", torch.uint8, need, dev, at_least=True)
+    if out is not None:
+        _plain(out, "out", dt, N * Hq * D, dev)
+    if lse is not None:
+        _plain(lse, "lse", torch.float32, N * Hq, dev)
+    if workspace is not None:
+        _plain(workspace, "workspace", torch.uint8, need, dev, at_least=True)
     with _on(dev, where, stream) as s:
         if out is None:
-            out = q.new_empty(shape)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if lse is None and want_lse:
             lse = q.new_empty((N, Hq), dtype=torch.float32)
         if workspace is None and need > 0:
