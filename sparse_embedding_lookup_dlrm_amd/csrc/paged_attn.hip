@@ -931,7 +931,10 @@ int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
 // 224 us; with half as much 231 us, with twice 242 us), smaller ones of at least 512 entries where that
 // leaves fewer than 256 workgroups, and at most 16k workgroups. One history of 131k and two heads: 30.7 us in
 // parts of 1024, 32.8 in 512, 40 in 256.
-// Tile kernel: twice as many workgroups as there are places, in parts of at least 512 entries. 24 sequences
+// Tile kernel: twice as many workgroups as there are places, in parts of at least 512 entries, and of heads
+// below 256 up to four times as many in parts of at least 1024 (13 sequences of up to 83 tokens over up to 24k:
+// 58 us against 78), of which more than 20 cost more than they give (3 sequences of up to 352 tokens over up to
+// 37k: 75 us in 19 parts, 93 in 37). 24 sequences
 // of up to 257 x 1500, 288 workgroups: 22.9 us against 29 unsplit; 8 sequences of 32 tokens over up to 32k:
 // 56 us, 71 with as many as places; but 432 workgroups of 256-wide heads, one to a CU: 81 us unsplit against
 // 118 in two parts, since the parts wait for a place and their sums are written and read.
@@ -956,9 +959,11 @@ Cut cut_call(long long max_rows, int seqs, int kv_heads, int dim, int causal, in
     if (splits < fill) splits = fill < finest ? fill : finest;
     if (splits > most) splits = most;
   } else {
-    const long long places = dim == 256 ? 256 : dim == 128 ? 512 : 768, most = (span + 511) / 512;
+    const long long places = dim == 256 ? 256 : dim == 128 ? 512 : 768, finest = (span + 511) / 512;
     splits = 2 * places / units;
-    if (splits > most) splits = most;
+    if (splits > finest) splits = finest;
+    const long long coarse = 4 * places / units < span / 1024 ? 4 * places / units : span / 1024;
+    if (dim < 256 && splits < coarse) splits = coarse < 20 ? coarse : splits < 20 ? 20 : splits;
   }
   if (splits < 1) splits = 1;
   if (splits > 1) splits |= 1;
@@ -993,7 +998,8 @@ hipError_t run(const AttnArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((attn_rows_kernel<DT, D>), grid, dim3(kThreads), 0, s, a, cut);
   else
     hipLaunchKernelGGL((attn_tile_kernel<DT, D>), grid, dim3(kTileThreads<D>), 0, s, a, cut);
-  if (cut.splits > 32)
+  const long long all_rows = rows * a.kv_heads * a.paged.seqs;
+  if (cut.splits > 16 && all_rows <= 512)
     join<DT, D, kThreads / (D / 8)>(a, cut, tile, s);
   else if (cut.splits > 1)
     join<DT, D, 1>(a, cut, tile, s);
