@@ -41,19 +41,6 @@ __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f3
                                                   0);
 }
 
-// The same with 16 steps instead of 32: four elements a lane.
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-template <int DT>
-__device__ __forceinline__ f32x4 mfma16_half(const uint2& a, const uint2& b, const f32x4& c) {
-  if constexpr (DT == DLRM_BF16)
-    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0,
-                                                     0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, a), __builtin_bit_cast(f16x4, b), c, 0, 0,
-                                                 0);
-}
-
 // All bits of those of the two 16-bit values of a dword that are infinite or NaN.
 template <int DT>
 __device__ __forceinline__ uint32_t not_finite_halves(uint32_t w) {
@@ -168,21 +155,19 @@ __device__ __forceinline__ void finish(const AttnArgs& a, long long to, int at, 
 }
 
 // ---------------------------------------------------------------------------
-// Rows kernel: 16 rows of one head to a workgroup, the four waves take the tiles of 16 TT entries of the
+// Rows kernel: 16 rows of one head to a workgroup, the four waves take the tiles of 32 entries of the
 // history in turn and join their (m, l, O) through LDS at the end. Bound by memory: keys and values go from
 // global memory to registers, each is used once. A lane takes D / 16 neighbouring elements of four values'
 // rows of each 16, so that a load instruction covers whole rows, and the transposition that the second
 // product needs is 16-bit permutations in registers.
 // A wave has a tile of loads on the way all the time: the next tile's keys are asked for as soon as this
-// one's are used, its values likewise, without a second set of registers. TT is what the registers hold at
-// two waves to a SIMD (256-wide heads: 16 entries a tile, with the 16x16x16 product for the values).
+// one's are used, its values likewise, without a second set of registers. Tiles of 32 entries: 64 of heads of
+// 64 and 32 leave fewer waves (63 us against 61 for 64 histories of up to 16k), 16 of heads of 256 keep two
+// waves to a SIMD but half the loads on the way (151 us against 135 for 64 of up to 8k).
 // ---------------------------------------------------------------------------
-template <int D>
-constexpr int kRowsBlocks = D == 256 ? 1 : D == 128 ? 2 : 4;
-
 template <int DT, int D>
-__global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Cut cut) {
-  constexpr int TT = kRowsBlocks<D>;  // blocks of 16 entries to a tile
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(AttnArgs a, Cut cut) {
+  constexpr int TT = 2;          // blocks of 16 entries to a tile
   constexpr int K = 16 * TT;
   constexpr int F = D / 32;      // k steps of the first product
   constexpr int E = D / 16;      // elements of a value row that a lane takes, and 16-wide pieces of O
@@ -355,16 +340,13 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Cut 
             f32x4 sum = o[e];
 #pragma unroll
             for (int t = 0; t < TT; t += 2) {
-              u32x4 vt = {0, 0, 0, 0};
+              u32x4 vt;
 #pragma unroll
-              for (int i = 0; i < (TT == 1 ? 2 : 4); ++i) {
+              for (int i = 0; i < 4; ++i) {
                 const int j = 4 * t + 2 * i;
                 vt[i] = __builtin_amdgcn_perm(v[j + 1][e / 2] & seen(j + 1), v[j][e / 2] & seen(j), pick);
               }
-              if constexpr (TT == 1)
-                sum = mfma16_half<DT>(make_uint2(vt[0], vt[1]), make_uint2(pw[0][0], pw[0][1]), sum);
-              else
-                sum = mfma16<DT>(vt, u32x4{pw[t][0], pw[t][1], pw[t + 1][0], pw[t + 1][1]}, sum);
+              sum = mfma16<DT>(vt, u32x4{pw[t][0], pw[t][1], pw[t + 1][0], pw[t + 1][1]}, sum);
             }
             if (mine) o[e] = sum;
           }
@@ -475,6 +457,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Cut 
 // exponentials: 307 .. 335 us, for the registers. Priorities around the matrix instructions: no difference.
 // ---------------------------------------------------------------------------
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 template <int DT>
 __device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f32x16& c) {
@@ -503,7 +486,8 @@ constexpr int kTileKeys = 64;
 // `to` + 1024 i + 16 j; from and to are the same in every lane. Written out because after the builtin
 // the compiler holds every LDS read back until the copy has landed, also reads of the other tile. No
 // register receives anything; the kernel itself waits (wait_copies) before the barrier that publishes
-// the tile. The offset of the instruction counts on both sides.
+// the tile. The offset of the instruction counts on both sides. m0 holds the LDS address; nothing else in
+// these kernels uses it (the compiler warns that it is reserved).
 template <int N>
 __device__ __forceinline__ void copy16(const char* from, const uint32_t (&off)[N], const uint16_t* to) {
   const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
@@ -940,7 +924,8 @@ int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
 // 118 in two parts, since the parts wait for a place and their sums are written and read.
 // The number of workgroups of a sequence is made odd where heads allow: workgroups go to the XCDs in turn,
 // and with 16 parts of 4 heads the first parts of all sequences, the ones that short histories fill, would
-// meet on the same four of eight (64 histories of up to 8k, 256-wide heads: 184 us, with 17 parts 151 us).
+// meet on the same four of eight (64 histories of up to 8k, 256-wide heads and tiles of 16: 184 us, with
+// 17 parts 151 us).
 Cut cut_call(long long max_rows, int seqs, int kv_heads, int dim, int causal, int window, int max_q, int max_kv) {
   Cut c;
   const int rows = tile_rows(max_rows);
