@@ -114,7 +114,8 @@ int check_attn(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32
   TRY(check_heads(n, q_heads, kv_heads, dim, DLRM_BF16, true));
   if (q_heads < 1 || q_heads % kv_heads != 0) return DLRM_E_INVAL;
   if (seqs < 0 || window < 0 || (window > 0 && !causal) || max_q < 0 || max_kv < 0) return DLRM_E_INVAL;
-  if (q_heads / kv_heads > 1024 || n * q_heads > kI32Max) return DLRM_E_UNSUPPORTED;  // rows are counted in int32
+  // rows are counted in int32, with room for a tile past the last one
+  if (q_heads / kv_heads > 1024 || n * q_heads > kI32Max - (1 << 17)) return DLRM_E_UNSUPPORTED;
   return DLRM_OK;
 }
 

@@ -197,7 +197,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
       const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut);
       if (split >= rc.parts) continue;
       const int k_first = rc.first + split * rc.part;
-      const int hi = rc.hi < k_first + rc.part ? rc.hi : k_first + rc.part;
+      const int hi = rc.hi - k_first < rc.part ? rc.hi : k_first + rc.part;
       const int k_begin = k_first + K * wave;
 
       // Pages of the blocks of this wave's next Ahead tiles, one to a lane; past the end: of the last entry.
@@ -569,7 +569,7 @@ __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs 
       const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut);
       if (split >= rc.parts) continue;
       const int k_first = rc.first + split * rc.part;
-      const int hi = rc.hi < k_first + rc.part ? rc.hi : k_first + rc.part;
+      const int hi = rc.hi - k_first < rc.part ? rc.hi : k_first + rc.part;
       // what this wave's rows see: some of them [w_lo, w_hi), all of them [w_all_lo, w_all_hi)
       const int w0 = row0 + 32 * wave, w1 = w0 + 32 < row_end ? w0 + 32 : row_end;
       int tok0 = 0, tok1 = -1, w_lo = 0, w_hi = 0, w_all_lo = 0, w_all_hi = 0;
@@ -934,6 +934,7 @@ Cut cut_call(long long max_rows, int seqs, int kv_heads, int dim, int causal, in
   c.q_tiles = static_cast<int>(tiles);
   const long long whole = tiles * seqs * kv_heads;
   long long span = max_kv > 0 ? max_kv : 1;
+  if (span > 0x7fffffffLL - (1 << 17)) span = 0x7fffffffLL - (1 << 17);  // no history is longer
   const long long seen = static_cast<long long>(window) + max_q + 32;
   if (causal && window && span > seen) span = seen;
   long long splits;

@@ -282,3 +282,20 @@ def test_more_sequences_than_a_grid_dimension():
     assert torch.equal(k[at, :, slot.cuda()], kn) and torch.equal(v[at, :, slot.cuda()], vn)
     k[at, :, slot.cuda()] = 0
     assert not k.any()
+
+
+@pytest.mark.parametrize("max_q", [3, 1 << 24])
+def test_entries_counted_up_to_31_bits(max_q):
+    """The window lies in the last two of 32765 pages of 65536 entries; a hint of many new tokens makes
+    parts that would end past 31 bits."""
+    page, width = 65536, 32765
+    h = History([3], [2 * page - 5], 2, 1, 32, page, "bf16", seed=51)
+    q, k, v, offsets, _, _ = h.args()
+    table = torch.full((1, width), -1, dtype=torch.int32)
+    table[0, -2:] = h.page_table[0, :2]
+    lens = torch.tensor([width * page - 5], dtype=torch.int32).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = ops.paged_attn(q, k, v, offsets, lens, table.cuda(), causal=True, window=70000, want_lse=True, status=status,
+                         max_q=max_q)
+    assert status.item() == 0
+    check(h, window=70000, got=got)
