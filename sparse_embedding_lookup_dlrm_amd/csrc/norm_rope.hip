@@ -392,7 +392,7 @@ __global__ __launch_bounds__(kDwThreads) void norm_rope_dw_kernel(const float* _
 // Tokens of a workgroup: as many as leave four workgroups to each CU, so that the angles of a
 // token are shared by all its heads and small calls still spread over the chip.
 int tokens_per_group(long long n) {
-    long long t = n / 1024;
+  const long long t = n / 1024;
   return static_cast<int>(t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t);
 }
 

@@ -918,10 +918,10 @@ int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
 // Tile kernel: twice as many workgroups as there are places, in parts of at least 512 entries, and of heads
 // below 256 up to four times as many in parts of at least 1024 (13 sequences of up to 83 tokens over up to 24k:
 // 58 us against 78), of which more than 20 cost more than they give (3 sequences of up to 352 tokens over up to
-// 37k: 75 us in 19 parts, 93 in 37). 24 sequences
-// of up to 257 x 1500, 288 workgroups: 22.9 us against 29 unsplit; 8 sequences of 32 tokens over up to 32k:
-// 56 us, 71 with as many as places; but 432 workgroups of 256-wide heads, one to a CU: 81 us unsplit against
-// 118 in two parts, since the parts wait for a place and their sums are written and read.
+// 37k: 75 us in 19 parts, 93 in 37). 24 sequences of up to 257 x 1500, 288 workgroups: 22.9 us against 29
+// unsplit; 8 sequences of 32 tokens over up to 32k: 56 us, 71 with as many as places; but 432 workgroups of
+// 256-wide heads, one to a CU: 81 us unsplit against 118 in two parts, since the parts wait for a place and
+// their sums are written and read.
 // The number of workgroups of a sequence is made odd where heads allow: workgroups go to the XCDs in turn,
 // and with 16 parts of 4 heads the first parts of all sequences, the ones that short histories fill, would
 // meet on the same four of eight (64 histories of up to 8k, 256-wide heads and tiles of 16: 184 us, with
