@@ -497,12 +497,12 @@ __device__ __forceinline__ void copy16(const char* from, const uint32_t (&off)[N
                  :: "s"(lds), "v"(off[0]), "s"(from) : "memory", "m0");
   else if constexpr (N == 2)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
-                 "global_load_lds_dwordx4 %2, %3 offset:1024"
+                 "global_load_lds_dwordx4 %2, %3 offset:0x400"
                  :: "s"(lds), "v"(off[0]), "v"(off[1]), "s"(from) : "memory", "m0");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
-                 "global_load_lds_dwordx4 %2, %5 offset:1024\n\tglobal_load_lds_dwordx4 %3, %5 offset:2048\n\t"
-                 "global_load_lds_dwordx4 %4, %5 offset:3072"
+                 "global_load_lds_dwordx4 %2, %5 offset:0x400\n\tglobal_load_lds_dwordx4 %3, %5 offset:0x800\n\t"
+                 "global_load_lds_dwordx4 %4, %5 offset:0xc00"
                  :: "s"(lds), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(from) : "memory", "m0");
 }
 
