@@ -49,8 +49,12 @@
  * before anything is enqueued. Data errors never make a kernel read or write out
  * of bounds; they OR a bit into *status (device int32, may be NULL):
  *   DLRM_STATUS_BAD_OFFSETS  q_offsets decrease or leave [0, n], or kv_lens is
- *                            negative or passes the page table's width: a sequence
- *                            with bad offsets counts as having no tokens. The
+ *                            negative or passes the page table's width. A sequence
+ *                            whose own two offsets decrease, or leave [0, n] or
+ *                            [q_offsets[0], q_offsets[seqs]], counts as having no
+ *                            tokens; the others keep theirs. Where some of those
+ *                            overlap, a token they share is stored for one of them,
+ *                            and its attention output is that of one of them. The
  *                            attention clamps a length to [0, table_width * page];
  *                            the append stores no token of a sequence whose length is
  *                            bad, and none that would fall before the first entry (a

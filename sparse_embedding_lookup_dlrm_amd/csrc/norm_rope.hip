@@ -211,22 +211,51 @@ struct Walk {
 
 constexpr int kMaxTokens = 4;  // tokens of a workgroup
 
+// The first sequence with good offsets that holds a token, by the whole wave, or -1. For offsets that do not
+// ascend, where the search of find_slots can end elsewhere.
+__device__ __forceinline__ int scan_sequences(const Paged& p, int lo, int hi, int token) {
+  const int lane = threadIdx.x & (kWave - 1);
+  for (long long s0 = 0; s0 < p.seqs; s0 += kWave) {
+    const long long s = s0 + lane;
+    bool holds = false;
+    if (s < p.seqs) {
+      const int a = p.q_offsets[s], b = p.q_offsets[s + 1];
+      holds = a >= lo && b <= hi && a <= token && token < b;
+    }
+    const unsigned long long found = __ballot(holds);
+    if (found) return static_cast<int>(s0) + __builtin_ctzll(found);
+  }
+  return -1;
+}
+
 // Cache slots of tokens t0 .. t0 + count, one wave each, the last wave first: the first ones have the
-// angles to form.
+// angles to form. A sequence's offsets are good if they ascend between the first and the last one of all.
 template <int D>
 __device__ __forceinline__ void find_slots(const Paged& p, long long n, long long t0, int count, long long* slots) {
   const int lane = threadIdx.x & (kWave - 1);
   for (int t = kThreads / kWave - 1 - threadIdx.x / kWave; t < count; t += kThreads / kWave) {
     const int token = static_cast<int>(t0) + t;
-    const int seq = wave_upper_bound(p.q_offsets, p.seqs + 1, token) - 1;
+    const int first_of_all = p.q_offsets[0], last_of_all = p.q_offsets[p.seqs];
+    int seq = wave_upper_bound(p.q_offsets, p.seqs + 1, token) - 1;
     long long slot = -1;
-    if (seq >= 0 && seq < p.seqs) {  // else the token is past the last sequence
-      const int first = p.q_offsets[seq], last = p.q_offsets[seq + 1];
-      const int held = p.kv_lens[seq];
+    if (token >= first_of_all && token < last_of_all) {  // else the token is in no sequence
+      const int lo = first_of_all > 0 ? first_of_all : 0, hi = last_of_all < n ? last_of_all : static_cast<int>(n);
+      bool bad = seq < 0 || seq >= p.seqs;
+      int last = 0;
+      if (!bad) {
+        const int first = p.q_offsets[seq];
+        last = p.q_offsets[seq + 1];
+        bad = first < lo || last > hi || token < first || token >= last;
+      }
+      if (bad) {
+        if (lane == 0) flag(p.status, DLRM_STATUS_BAD_OFFSETS);
+        seq = scan_sequences(p, lo, hi, token);
+        if (seq >= 0) last = p.q_offsets[seq + 1];
+      }
+      const int held = seq < 0 ? -1 : p.kv_lens[seq];
       const long long room = static_cast<long long>(p.table_width) << p.page_shift;
-      bool bad = first < 0 || last > n || token < first || token >= last;
       const long long at = static_cast<long long>(held) - last + token;
-      bad |= at < 0 || at >= room || held < 0 || held > room;
+      bad = at < 0 || at >= room || held < 0 || held > room;
       if (bad) {
         if (lane == 0) flag(p.status, DLRM_STATUS_BAD_OFFSETS);
       } else {

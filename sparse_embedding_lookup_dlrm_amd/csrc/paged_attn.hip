@@ -62,8 +62,9 @@ struct Seq {
 __device__ __forceinline__ Seq load_seq(const Paged& p, long long n, int seq) {
   Seq s;
   const int a = scalar_load(p.q_offsets, seq), b = scalar_load(p.q_offsets, seq + 1LL);
+  const int first = scalar_load(p.q_offsets, 0), last = scalar_load(p.q_offsets, p.seqs);
   const int held = scalar_load(p.kv_lens, seq), room = p.table_width << p.page_shift;
-  const bool bad = a < 0 || b < a || b > n;
+  const bool bad = a < 0 || a < first || b < a || b > last || b > n;
   s.first = bad ? 0 : a;
   s.tokens = bad ? 0 : b - a;
   s.held = held < 0 ? 0 : held > room ? room : held;
