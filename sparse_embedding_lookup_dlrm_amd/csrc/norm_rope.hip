@@ -272,10 +272,10 @@ __device__ __forceinline__ void find_slots(const Paged& p, long long n, long lon
 }
 
 template <int DT, int D, bool APPEND>
-__global__ __launch_bounds__(kThreads) void norm_rope_kernel(NormRopeArgs a, int per_group) {
+__global__ __launch_bounds__(kThreads) void norm_rope_kernel(NormRopeArgs a, long long from, int per_group) {
   __shared__ float2 cs[kMaxTokens * D / 2];
   __shared__ long long slots[APPEND ? kMaxTokens : 1];
-  const long long t0 = static_cast<long long>(blockIdx.x) * per_group;
+  const long long t0 = from + static_cast<long long>(blockIdx.x) * per_group;
   const int count = static_cast<int>(a.n - t0 < per_group ? a.n - t0 : per_group);
   constexpr int G = Split<DT, D>::groups;
   const int after_q = G - count * a.q_heads % G, after_k = after_q + G - count * a.kv_heads % G;
@@ -428,8 +428,14 @@ int tokens_per_group(long long n) {
 template <int DT, int D, bool APPEND>
 hipError_t run(const NormRopeArgs& a, hipStream_t s) {
   const int per = tokens_per_group(a.n);
-  hipLaunchKernelGGL((norm_rope_kernel<DT, D, APPEND>), dim3(static_cast<unsigned>((a.n + per - 1) / per)),
-                     dim3(kThreads), 0, s, a, per);
+  // a grid has fewer than 2^32 threads: 2^23 workgroups to a launch
+  constexpr long long kMostGroups = 1 << 23;
+  for (long long from = 0; from < a.n; from += kMostGroups * per) {
+    const long long left = (a.n - from + per - 1) / per;
+    hipLaunchKernelGGL((norm_rope_kernel<DT, D, APPEND>),
+                       dim3(static_cast<unsigned>(left < kMostGroups ? left : kMostGroups)), dim3(kThreads), 0, s, a,
+                       from, per);
+  }
   return hipGetLastError();
 }
 
