@@ -68,12 +68,11 @@ __device__ __forceinline__ Seq load_seq(const Paged& p, long long n, int seq) {
   s.first = bad ? 0 : a;
   s.tokens = bad ? 0 : b - a;
   s.held = held < 0 ? 0 : held > room ? room : held;
-  if (s.held > 0 && p.num_pages == 0) {  // nothing to read
-    s.held = 0;
-    if (threadIdx.x == 0) flag(p.status, DLRM_STATUS_BAD_PAGE);
-    return s;
-  }
   if ((bad || s.held != held) && threadIdx.x == 0) flag(p.status, DLRM_STATUS_BAD_OFFSETS);
+  if (p.num_pages == 0) {  // nothing to read; the last token would see the last entry
+    if (s.held > 0 && s.tokens > 0 && threadIdx.x == 0) flag(p.status, DLRM_STATUS_BAD_PAGE);
+    s.held = 0;
+  }
   return s;
 }
 

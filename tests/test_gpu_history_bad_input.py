@@ -82,3 +82,27 @@ def test_append_and_attention_take_the_same_sequences(case):
         want[a:b] = ops.paged_attn(q[a:b].cuda(), kc, vc, i32([0, b - a]), i32(lens[s:s + 1]), table[s:s + 1].cuda(), **how)
     once = torch.tensor([len(slots[t]) <= 1 for t in range(n)], device="cuda")
     assert torch.equal(out[once], want[once])
+
+
+@pytest.mark.parametrize("max_q", [1, 40])
+def test_attention_over_a_cache_without_pages(max_q):
+    """Bad offsets and lengths are reported as with pages, bad pages only where a token would see an entry; the
+    tokens see nothing."""
+    S, B, P = 2, ops.STATUS_BAD_OFFSETS, ops.STATUS_BAD_PAGE
+    q = rand((6, 4, 64), "bf16", 1).cuda()
+    table = torch.full((S, 3), -1, dtype=torch.int32, device="cuda")
+    for offsets, lens, want in (([0, 2, 6], [9, 8], P), ([0, 2, 6], [0, 0], 0), ([0, 0, 0], [9, 8], 0),
+                                ([0, 6, 6], [0, 8], 0), ([0, 9, 6], [5, 5], B), ([0, 2, 6], [0, -1], B),
+                                ([0, 2, 6], [0, 10 ** 6], B | P), ([0, 2, 6], [1, -3], B | P)):
+        for pages in (0, 1):  # no page at all, and one that no table names
+            cache = torch.zeros((pages, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+            status = i32([0])
+            out, lse = torch.full_like(q, 3.0), torch.full((6, 4), 3.0, device="cuda")
+            ops.paged_attn(q, cache, cache, i32(offsets), i32(lens), table, out=out, lse=lse, want_lse=True,
+                           status=status, max_q=max_q)
+            assert status.item() == want, (offsets, lens, pages)
+            taken = torch.zeros(6, dtype=torch.bool)
+            for a, b in sequences_of(offsets, 6).values():
+                taken[a:b] = True
+            assert (out[taken.cuda()] == 0).all() and (lse[taken.cuda()] == -float("inf")).all()
+            assert (out[~taken.cuda()] == 3).all() and (lse[~taken.cuda()] == 3).all()
