@@ -44,6 +44,10 @@
  *   kv_lens    device int32 [seqs]: entries of the history of each sequence, its
  *              new tokens included; token i of m new ones is entry kv_lens[s] - m + i.
  *
+ * Limits (DLRM_E_UNSUPPORTED past them): 65535 heads of queries and keys together; at
+ * most 2^31 - 2^17 - 1 sequences, entries of a page table's row (table_width * page)
+ * and, in the attention, rows (n * q_heads), with 1024 query heads to a cache head.
+ *
  * Pointers, ordering and errors are as in dlrm_embbag.h: the caller owns every
  * buffer, the call only enqueues work on `stream`, argument errors are returned
  * before anything is enqueued. Data errors never make a kernel read or write out

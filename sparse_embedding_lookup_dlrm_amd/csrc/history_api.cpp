@@ -12,6 +12,8 @@ namespace {
 using namespace dlrm;
 
 constexpr int64_t kI32Max = 0x7fffffffLL;
+// What kernels count in int32, with room for a tile or a grid's step past the last one.
+constexpr int64_t kMostCounted = kI32Max - (1 << 17);
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -73,13 +75,13 @@ int check_paged(int64_t n, int32_t seqs, int32_t kv_heads, int32_t dim, int dtyp
                 int32_t page, int64_t num_pages, int64_t page_stride, int64_t head_stride, const void* k_cache,
                 const void* v_cache, int32_t* status, Paged* p) {
   if (seqs < 0 || (n > 0 && (!q_offsets || (seqs > 0 && !kv_lens)))) return DLRM_E_INVAL;
-  if (seqs >= kI32Max || table_width < 0 || table_stride < 0 || num_pages < 0 || num_pages > kI32Max)
+  if (table_width < 0 || table_stride < 0 || num_pages < 0 || num_pages > kI32Max)
     return DLRM_E_INVAL;
   if (n > 0 && seqs > 0 && table_width > 0 && !page_table) return DLRM_E_INVAL;
   if (n > 0 && num_pages > 0 && (!k_cache || !v_cache)) return DLRM_E_INVAL;
   if (page < 16 || page > 65536 || (page & (page - 1))) return DLRM_E_UNSUPPORTED;
-  // entries are counted in int32, with room for a tile past the last one
-  if (static_cast<int64_t>(table_width) * page > kI32Max - (1 << 17)) return DLRM_E_UNSUPPORTED;
+  // entries and sequences
+  if (static_cast<int64_t>(table_width) * page > kMostCounted || seqs > kMostCounted) return DLRM_E_UNSUPPORTED;
   const int64_t per16 = 16 / bytes_of(dtype);
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || page_stride % per16 || head_stride % per16) return DLRM_E_ALIGN;
   if (!aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(page_table, 4) || !aligned(status, 4))
@@ -114,8 +116,8 @@ int check_attn(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32
   TRY(check_heads(n, q_heads, kv_heads, dim, DLRM_BF16, true));
   if (q_heads < 1 || q_heads % kv_heads != 0) return DLRM_E_INVAL;
   if (seqs < 0 || window < 0 || (window > 0 && !causal) || max_q < 0 || max_kv < 0) return DLRM_E_INVAL;
-  // rows are counted in int32, with room for a tile past the last one
-  if (q_heads / kv_heads > 1024 || n * q_heads > kI32Max - (1 << 17)) return DLRM_E_UNSUPPORTED;
+  // rows and sequences
+  if (q_heads / kv_heads > 1024 || n * q_heads > kMostCounted || seqs > kMostCounted) return DLRM_E_UNSUPPORTED;
   return DLRM_OK;
 }
 
