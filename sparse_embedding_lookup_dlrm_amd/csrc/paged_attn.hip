@@ -926,7 +926,12 @@ int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
 // and with 16 parts of 4 heads the first parts of all sequences, the ones that short histories fill, would
 // meet on the same four of eight (64 histories of up to 8k, 256-wide heads and tiles of 16: 184 us, with
 // 17 parts 151 us).
-Cut cut_call(long long max_rows, int seqs, int kv_heads, int dim, int causal, int window, int max_q, int max_kv) {
+//
+// The parts' sums take n x q_heads rows each. Where these rows are more than the hints and the sequences have tiles
+// for (max_q too small, or tokens past the last sequence), the number of parts is bounded so that the sums take at
+// most four times what they can with right hints: 1.6 GB for heads of 256, half of it for half of the width.
+Cut cut_call(long long all_rows, long long max_rows, int seqs, int kv_heads, int dim, int causal, int window, int max_q,
+             int max_kv) {
   Cut c;
   const int rows = tile_rows(max_rows);
   long long tiles = max_rows > rows ? (max_rows + rows - 1) / rows : 1;
@@ -939,17 +944,20 @@ Cut cut_call(long long max_rows, int seqs, int kv_heads, int dim, int causal, in
   if (causal && window && span > seen) span = seen;
   long long splits;
   const long long units = whole > 0 ? whole : 1;
+  const long long held = (all_rows + rows - 1) / rows, busy = held > units ? held : units;  // tiles of all rows
   if (rows == 16) {
     const long long least = 131072 / dim, fill = 256 / units, finest = (span + 511) / 512, most = 16384 / units;
     splits = (span + least - 1) / least;
     if (splits < fill) splits = fill < finest ? fill : finest;
     if (splits > most) splits = most;
+    if (splits > 4 * 16384 / busy) splits = 4 * 16384 / busy;
   } else {
     const long long places = dim == 256 ? 256 : dim == 128 ? 512 : 768, finest = (span + 511) / 512;
     splits = 2 * places / units;
     if (splits > finest) splits = finest;
     const long long coarse = 4 * places / units < span / 1024 ? 4 * places / units : span / 1024;
     if (dim < 256 && splits < coarse) splits = coarse < 20 ? coarse : splits < 20 ? 20 : splits;
+    if (splits > 4 * 4 * places / busy) splits = 4 * 4 * places / busy;
   }
   if (splits < 1) splits = 1;
   if (splits > 1) splits |= 1;
@@ -974,7 +982,7 @@ size_t cut_bytes(const Cut& c, int64_t n, int q_heads, int dim) {
 template <int DT, int D>
 hipError_t run(const AttnArgs& a, hipStream_t s) {
   const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
-  Cut cut = cut_call(rows, a.paged.seqs, a.kv_heads, D, a.causal, a.window, a.max_q, a.max_kv);
+  Cut cut = cut_call(a.n * a.q_heads, rows, a.paged.seqs, a.kv_heads, D, a.causal, a.window, a.max_q, a.max_kv);
   cut.o = static_cast<float*>(a.workspace);
   cut.ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) +
                                      round256(static_cast<size_t>(a.n) * a.q_heads * cut.splits * D * sizeof(float)));
@@ -1008,7 +1016,7 @@ size_t attn_workspace(int64_t n, int seqs, int q_heads, int kv_heads, int dim, i
                       int max_kv) {
   if (n == 0 || seqs == 0) return 0;
   const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
-  return cut_bytes(cut_call(rows, seqs, kv_heads, dim, causal, window, max_q, max_kv), n, q_heads, dim);
+  return cut_bytes(cut_call(n * q_heads, rows, seqs, kv_heads, dim, causal, window, max_q, max_kv), n, q_heads, dim);
 }
 
 hipError_t launch_paged_attn(const AttnArgs& a, hipStream_t s) {

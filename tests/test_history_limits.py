@@ -18,3 +18,31 @@ def test_more_sequences_than_a_counter_holds_are_refused(lib):
         assert _attn(lib, S=S) == E_UNSUPPORTED and _append(lib, S=S) == E_UNSUPPORTED, S
         need = ctypes.c_size_t(0)
         assert lib.dlrm_paged_attn_workspace_bytes(4, S, 4, 2, 64, 1, 0, 2, 128, ctypes.byref(need)) == E_UNSUPPORTED
+
+
+def _workspace(lib, n, S, Hq, Hk, D, max_q, max_kv, window=0):
+    need = ctypes.c_size_t(0)
+    assert lib.dlrm_paged_attn_workspace_bytes(n, S, Hq, Hk, D, 1, window, max_q, max_kv, ctypes.byref(need)) == 0
+    return need.value
+
+
+def test_workspace_of_hints_that_are_too_small(lib):
+    """max_q below the real number of new tokens, or many tokens past the last sequence: slower, but no workspace
+    of many GB."""
+    for n in (4096, 65536, 1 << 20, 1 << 24):
+        for S in (1, 8, 300):
+            for Hq, Hk in ((32, 8), (16, 1), (4, 4), (64, 64)):
+                if n * Hq >= 1 << 31:
+                    continue
+                for D in (32, 64, 128, 256):
+                    for max_q in (0, 1, 5, 17, 129):
+                        for max_kv in (4096, 131072, 1 << 30):
+                            need = _workspace(lib, n, S, Hq, Hk, D, max_q, max_kv)
+                            assert need < 8 * D * 1_000_000, (n, S, Hq, Hk, D, max_q, max_kv, need)
+
+
+def test_workspace_of_right_hints(lib):
+    """17 parts of 64 histories of up to 16384 entries, 129 of one of 131009; none with one entry."""
+    for n, Hq, Hk, D, max_kv, parts in ((64, 32, 8, 128, 16384, 17), (1, 16, 2, 128, 131009, 129), (64, 32, 8, 128, 1, 0)):
+        rows = n * Hq * parts
+        assert _workspace(lib, n, n, Hq, Hk, D, 1, max_kv) == -(-rows * D * 4 // 256) * 256 + rows * 8
