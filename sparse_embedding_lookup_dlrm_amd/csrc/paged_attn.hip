@@ -486,24 +486,26 @@ constexpr int kTileKeys = 64;
 // `to` + 1024 i + 16 j; from and to are the same in every lane. Written out because after the builtin
 // the compiler holds every LDS read back until the copy has landed, also reads of the other tile. No
 // register receives anything; the kernel itself waits (wait_copies) before the barrier that publishes
-// the tile. The offset of the instruction counts on both sides. m0 holds the LDS address; nothing else in
-// these kernels uses it (the compiler warns that it is reserved).
+// the tile. The offset of the instruction counts on both sides. m0, which holds the LDS address, is the compiler's:
+// each block puts back what it found there.
 template <int N>
 __device__ __forceinline__ void copy16(const char* from, const uint32_t (&off)[N], const uint16_t* to) {
   const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
       (const __attribute__((address_space(3))) uint16_t*)to));
+  uint32_t m0;
   if constexpr (N == 1)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(lds), "v"(off[0]), "s"(from) : "memory", "m0");
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\t"
+                 "s_mov_b32 m0, %0"
+                 : "=&s"(m0) : "s"(lds), "v"(off[0]), "s"(from) : "memory");
   else if constexpr (N == 2)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
-                 "global_load_lds_dwordx4 %2, %3 offset:0x400"
-                 :: "s"(lds), "v"(off[0]), "v"(off[1]), "s"(from) : "memory", "m0");
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %4\n\t"
+                 "global_load_lds_dwordx4 %3, %4 offset:0x400\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0) : "s"(lds), "v"(off[0]), "v"(off[1]), "s"(from) : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
-                 "global_load_lds_dwordx4 %2, %5 offset:0x400\n\tglobal_load_lds_dwordx4 %3, %5 offset:0x800\n\t"
-                 "global_load_lds_dwordx4 %4, %5 offset:0xc00"
-                 :: "s"(lds), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(from) : "memory", "m0");
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %6\n\t"
+                 "global_load_lds_dwordx4 %3, %6 offset:0x400\n\tglobal_load_lds_dwordx4 %4, %6 offset:0x800\n\t"
+                 "global_load_lds_dwordx4 %5, %6 offset:0xc00\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0) : "s"(lds), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(from) : "memory");
 }
 
 // Waits for this wave's copies to LDS (vmcnt 0, the other counts open); a barrier makes those of the
