@@ -581,6 +581,8 @@ class BwdPlan:
 
 # The checks of these calls cost more host time than a small launch takes on the GPU, so they read each
 # property of a tensor once and compare devices by number (-1: a host tensor).
+# ctypes cuts a number that is too long for its type.
+_I32_MAX = 0x7FFFFFFF
 _I32_ARRAY = [_i32 * n for n in range(MAX_AXES + 1)]
 
 
@@ -648,6 +650,8 @@ def _turn_args(dev, positions, inv_freq, w_q, w_k, eps, sections, interleaved, t
         if len(sections) != axes:
             raise ValueError(f"{len(sections)} sections for {axes} axes of positions")
         secs = (_I32_ARRAY[axes] if axes <= MAX_AXES else _i32 * axes)(*sections)
+        if secs[:] != list(sections):
+            raise ValueError(f"sections {tuple(sections)} do not fit 32 bits")
         pos = positions.data_ptr()
     if (w_q is None) != (w_k is None):
         raise ValueError("w_q and w_k come together")
@@ -865,9 +869,11 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, q_
     if max_q is None:
         max_q = N
     if max_kv is None:
-        max_kv = width * page
+        max_kv = min(width * page, _I32_MAX)
     if scale is None:
         scale = D ** -0.5 if D > 0 else 1.0
+    if window > _I32_MAX or max_q > _I32_MAX or max_kv > _I32_MAX or window < 0 or max_q < 0 or max_kv < 0:
+        raise ValueError(f"window {window}, max_q {max_q} and max_kv {max_kv} must lie between 0 and {_I32_MAX}")
     need = paged_attn_workspace_bytes(N, S, Hq, Hk, D, causal, window, max_q, max_kv)
     if out is not None:
         _plain(out, "out", dt, N * Hq * D, dev)

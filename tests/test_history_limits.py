@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from sparse_embedding_lookup_dlrm_amd import ops
 from test_history_abi import E_UNSUPPORTED, _append, _attn
@@ -46,3 +47,16 @@ def test_workspace_of_right_hints(lib):
     for n, Hq, Hk, D, max_kv, parts in ((64, 32, 8, 128, 16384, 17), (1, 16, 2, 128, 131009, 129), (64, 32, 8, 128, 1, 0)):
         rows = n * Hq * parts
         assert _workspace(lib, n, n, Hq, Hk, D, 1, max_kv) == -(-rows * D * 4 // 256) * 256 + rows * 8
+
+
+def test_numbers_past_32_bits_are_refused_by_the_binding():
+    """A window of 2^32 + 5 is not one of 5, nor a section of 2^32 + 16 one of 16."""
+    q, cache = torch.zeros(4, 4, 64), torch.zeros(6, 2, 16, 64)
+    off, lens, table = (torch.zeros(s, dtype=torch.int32) for s in ((3,), (2,), (2, 4)))
+    for kw in (dict(window=2 ** 32 + 5), dict(window=-1), dict(max_q=2 ** 32 + 1), dict(max_kv=2 ** 31), dict(max_q=-2)):
+        with pytest.raises(ValueError, match="must lie between"):
+            ops.paged_attn(q, cache, cache, off, lens, table, **kw)
+    pos, freq = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(32)
+    for sections in ([2 ** 32 + 16, 16], [2 ** 32 + 16, 16 - 2 ** 32]):
+        with pytest.raises(ValueError, match="32 bits"):
+            ops.qk_norm_rope(q, cache[:4, :, 0], pos, freq, sections=sections)
