@@ -703,6 +703,8 @@ def _on(dev: int, where: torch.device, stream):
         if _current_device() == dev:
             return _Here(_raw_stream(dev))
         return _There(torch.cuda.device(where), lambda: torch.cuda.current_stream(where).cuda_stream)
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {where}")
     return _There(torch.cuda.stream(stream), lambda: stream.cuda_stream)
 
 

@@ -1,5 +1,6 @@
 """Limits of the user-history operators' sizes, which need no GPU: refused before any HIP call."""
 import ctypes
+import types
 
 import pytest
 import torch
@@ -60,3 +61,10 @@ def test_numbers_past_32_bits_are_refused_by_the_binding():
     for sections in ([2 ** 32 + 16, 16], [2 ** 32 + 16, 16 - 2 ** 32]):
         with pytest.raises(ValueError, match="32 bits"):
             ops.qk_norm_rope(q, cache[:4, :, 0], pos, freq, sections=sections)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The kernels would run there on this device's addresses."""
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    with pytest.raises(ValueError, match="stream is on"):
+        ops._on(0, torch.device("cuda", 0), stream)
