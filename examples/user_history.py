@@ -35,7 +35,15 @@ class HistoryCache:
 
     def grow(self, users: Sequence[int], new: Sequence[int]):
         """Room for new[i] events of users[i]; returns q_offsets, kv_lens and page table of the call and its
-        largest numbers of new and of held events."""
+        largest numbers of new and of held events. Without room nothing changes."""
+        if len(set(users)) != len(users):
+            raise ValueError("a user's new events go in one sequence")
+        for u, n in zip(users, new):
+            if self.held[u] + n > self.width * self.page:
+                raise ValueError(f"user {u} would hold {self.held[u] + n} events, there is room for {self.width * self.page}")
+        pages = sum(-(-(self.held[u] + n) // self.page) - len(self.pages[u]) for u, n in zip(users, new))
+        if pages > len(self.free):
+            raise ValueError(f"{pages} more pages are needed, {len(self.free)} are free")
         for u, n in zip(users, new):
             self.held[u] += n
             while len(self.pages[u]) * self.page < self.held[u]:
