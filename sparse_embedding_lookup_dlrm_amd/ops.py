@@ -783,7 +783,8 @@ def _paged_args(dtype, dev: int, k_cache, v_cache, q_offsets, kv_lens, page_tabl
     shape, strides = k_cache.shape, k_cache.stride()
     if len(shape) != 4 or shape[1] != Hk or shape[3] != D:
         raise ValueError(f"k_cache must be [pages, {Hk}, page, {D}], got {tuple(shape)}")
-    if v_cache.shape != shape or v_cache.stride() != strides:
+    if v_cache.shape != shape or (v_cache.stride() != strides and any(
+            a != b and n > 1 for a, b, n in zip(v_cache.stride(), strides, shape))):
         raise ValueError("v_cache must have k_cache's shape and strides")
     if k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise ValueError(f"the caches must be {dtype}, got {k_cache.dtype} and {v_cache.dtype}")
@@ -802,7 +803,9 @@ def _paged_args(dtype, dev: int, k_cache, v_cache, q_offsets, kv_lens, page_tabl
                          f"{v_cache.device} and {page_table.device}")
     if shape[0] > 0 and (strides[2] != D or strides[3] != 1):
         raise ValueError("a page's entries of a head must be contiguous in the caches")
-    return (S, shape[2], shape[0], strides[0], strides[1], by_seq, width), where
+    # a stride over one page or head is never taken, and may be any number
+    by_page, by_head = strides[0] if shape[0] > 1 else 0, strides[1] if Hk > 1 else 0
+    return (S, shape[2], shape[0], by_page, by_head, by_seq, width), where
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,

@@ -1,5 +1,5 @@
 """Bad offsets of sequences in the user-history operators: which tokens the append stores, and that the
-attention takes the same sequences."""
+attention takes the same sequences. Caches without pages, and strides that are never taken."""
 import pytest
 import torch
 
@@ -106,3 +106,16 @@ def test_attention_over_a_cache_without_pages(max_q):
                 taken[a:b] = True
             assert (out[taken.cuda()] == 0).all() and (lse[taken.cuda()] == -float("inf")).all()
             assert (out[~taken.cuda()] == 3).all() and (lse[~taken.cuda()] == 3).all()
+
+
+def test_strides_of_single_pages_and_heads_are_not_looked_at():
+    """One head, or one page, with any stride over it, another one in each cache."""
+    q, k, v = (rand((3, h, 64), "bf16", i).cuda() for i, h in enumerate((2, 1, 1)))
+    for pages, odd_k, odd_v in ((4, (1024, 7, 64, 1), (1024, 13, 64, 1)), (1, (3, 1024, 64, 1), (1024, 5, 64, 1))):
+        kc, vc, want_k, want_v = (torch.zeros((pages, 1, 16, 64), dtype=torch.bfloat16, device="cuda") for _ in range(4))
+        args = i32([0, 3]), i32([9]), i32([[pages - 1]])
+        ops.kv_append(k, v, want_k, want_v, *args)
+        ops.kv_append(k, v, kc.as_strided(kc.shape, odd_k), vc.as_strided(vc.shape, odd_v), *args)
+        assert torch.equal(kc, want_k) and torch.equal(vc, want_v) and kc.any()
+        out = ops.paged_attn(q, kc.as_strided(kc.shape, odd_k), vc.as_strided(vc.shape, odd_v), *args)
+        assert torch.equal(out, ops.paged_attn(q, want_k, want_v, *args))
