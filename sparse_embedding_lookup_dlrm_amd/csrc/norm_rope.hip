@@ -47,8 +47,10 @@ struct Split {
   }
 };
 
-// A 16-byte piece of a result, stored past the caches: nothing of a large call is read again before it
-// would have left them (training batch: 52 us, 67 through the caches; append of chunks: 56 and 73).
+// A 16-byte piece of a result, stored past the caches. Other inputs each time, past and through them: training
+// batch 60 us and 64, half of it 29 and 32, append of chunks 67 and 72. Calls of fewer tokens take as long either
+// way, also with the attention that reads the results next: append and attention of 96 tokens 104 us and 105, of
+// 4 x 1024 205 and 202, of 8 x 2048 760 and 767. (The backward alone would be faster through them: 94 us and 89.)
 __device__ __forceinline__ void put(char* to, const uint4& v) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(to));
@@ -457,8 +459,9 @@ int bwd_groups(long long n) {
 template <int DT, int D>
 hipError_t run_bwd(const NormRopeBwdArgs& a, hipStream_t s) {
   const int groups = bwd_groups(a.n);
-  // Inputs of more than the 256 MB of the last cache are read past the caches (500 MB in all: 94 us against
-  // 100); smaller ones may still lie there from the kernels that made them (250 MB: 50 us against 54).
+  // Inputs of more than the 256 MB of the last cache are read past the caches (16384 tokens of 40 heads of 128,
+  // 335 MB: 94 us against 100); smaller ones may still lie there from the kernels that made them (8192 tokens,
+  // 168 MB: 48 us against 52 if they do, 56 against 53 if not).
   const double read = static_cast<double>(a.n) * (a.q_heads + a.kv_heads) * D * Storage<DT>::bytes * (a.w_q ? 2 : 1);
   if (groups > 0 && read > 256e6)
     hipLaunchKernelGGL((norm_rope_bwd_kernel<DT, D, true>), dim3(groups), dim3(kThreads), 0, s, a);

@@ -163,7 +163,7 @@ __device__ __forceinline__ void finish(const AttnArgs& a, long long to, int at, 
 // A wave has a tile of loads on the way all the time: the next tile's keys are asked for as soon as this
 // one's are used, its values likewise, without a second set of registers. Tiles of 32 entries: 64 of heads of
 // 64 and 32 leave fewer waves (63 us against 61 for 64 histories of up to 16k), 16 of heads of 256 keep two
-// waves to a SIMD but half the loads on the way (151 us against 135 for 64 of up to 8k).
+// waves to a SIMD but half the loads on the way (151 us against 134 for 64 of up to 8k).
 // ---------------------------------------------------------------------------
 template <int DT, int D>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(AttnArgs a, Cut cut) {
@@ -449,12 +449,15 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
 // so that the lanes that LDS serves together fall on different banks. The copy to LDS writes places
 // in order and picks the piece for each.
 //
-// Bound by LDS: a piece of keys or values feeds one matrix instruction of 32 clocks and is 1 KB, so four
-// SIMDs ask for 128 bytes a clock where LDS gives 64 (147 bytes/ns a CU measured): the matrix units are at
-// 45 %. Four chunks of up to 2048 new tokens over up to 8192 entries, 32 heads of 128: 280 us, 957 TFLOP/s.
-// Two blocks of 32 rows to a wave halve the reads, but leave one wave to a SIMD, whose exponentials then
-// stand beside idle matrix units: 357 .. 550 us. Scores of the next tile formed beside this one's
-// exponentials: 307 .. 335 us, for the registers. Priorities around the matrix instructions: no difference.
+// Long chunks are bound by the matrix and the vector units, which are rarely at work at once. A tile takes a wave 32
+// matrix instructions of 32 clocks (D = 128) and 188 vector ones, about 890 clocks of the softmax, of the 2280 clocks
+// that its SIMD has for it: the matrix units are at 45 %. Four chunks of up to 2048 new tokens over up to 8192
+// entries, 32 heads of 128: 278 us, 963 TFLOP/s; the matrix instructions alone take 198 us, everything else 181. LDS
+// is at 23 %: its reads left out save 14 us, the copies to it 29. Short histories and windows wait for a workgroup's
+// tiles in a row (24 sequences of up to 257 x 1500: 17 us, 208 workgroups of heads of 256 with a window of 1024: 80).
+// Two blocks of 32 rows to a wave halve the LDS reads, but leave one wave to a SIMD, whose exponentials then stand
+// beside idle matrix units: 357 .. 550 us. Scores of the next tile formed beside this one's exponentials: 307 .. 335
+// us, for the registers. Priorities around the matrix instructions: no difference.
 // ---------------------------------------------------------------------------
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -913,21 +916,20 @@ int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
 
 // Where the workgroups of a call would not fill the chip, or histories may be of unequal length, every
 // history is split into parts.
-// Rows kernel: parts of 256 KB of keys and as much of values (64 histories of up to 16k entries of 128:
-// 224 us; with half as much 231 us, with twice 242 us), smaller ones of at least 512 entries where that
-// leaves fewer than 256 workgroups, and at most 16k workgroups. One history of 131k and two heads: 30.7 us in
-// parts of 1024, 32.8 in 512, 40 in 256.
-// Tile kernel: twice as many workgroups as there are places, in parts of at least 512 entries, and of heads
-// below 256 up to four times as many in parts of at least 1024 (13 sequences of up to 83 tokens over up to 24k:
-// 58 us against 78), of which more than 20 cost more than they give (3 sequences of up to 352 tokens over up to
-// 37k: 75 us in 19 parts, 93 in 37). 24 sequences of up to 257 x 1500, 288 workgroups: 22.9 us against 29
-// unsplit; 8 sequences of 32 tokens over up to 32k: 56 us, 71 with as many as places; but 432 workgroups of
-// 256-wide heads, one to a CU: 81 us unsplit against 118 in two parts, since the parts wait for a place and
-// their sums are written and read.
-// The number of workgroups of a sequence is made odd where heads allow: workgroups go to the XCDs in turn,
-// and with 16 parts of 4 heads the first parts of all sequences, the ones that short histories fill, would
-// meet on the same four of eight (64 histories of up to 8k, 256-wide heads and tiles of 16: 184 us, with
-// 17 parts 151 us).
+// Rows kernel: parts of 256 KB of keys and as much of values (64 histories of up to 16k entries of 128: 220 us in 17
+// parts, 222 in 9, 231 in 33), smaller ones of 512 entries where that leaves fewer than 256 workgroups, and 16k
+// workgroups. One history of 131k and two heads: 30 us in 129 parts, 29 in 65, 32 in 257, 36 in 511.
+// Tile kernel: twice as many workgroups as there are places, in parts of 512 entries, and of heads below 256 up to
+// four times as many in parts of 1024 (13 sequences of up to 83 tokens over up to 24k: 57 us in 19 parts, 69 in 11,
+// 63 in 31), of which more than 20 cost more than they give (3 sequences of up to 352 tokens over up to 37k: 76 us
+// in 19 parts, 81 in 21, 92 in 37). 24 sequences of up to 257 x 1500: 21 us in 3 parts, 27 in one; 8 sequences of
+// 32 tokens over up to 32k: 49 us in 33 parts, 61 in 15, as many as places; but 208 working workgroups of 256-wide
+// heads, one to a CU: 80 us unsplit, 120 in two parts and 94 in three, since the parts wait for a place and their
+// sums are written and read.
+// The number of parts, and of tiles of a sequence, is made odd last: workgroups go to the XCDs in turn, and with 16
+// parts of 4 heads the first parts of all sequences, the ones that short histories fill, would meet on the same four
+// of eight (64 histories of up to 8k, 256-wide heads: 180 us, with 17 parts 134 us). There may so be one part more
+// than the limits above say, and parts may be shorter: 513 entries make three of 192.
 //
 // The parts' sums take n x q_heads rows each. Where these rows are more than the hints and the sequences have tiles
 // for (max_q too small, or tokens past the last sequence), the number of parts is bounded so that the sums take at

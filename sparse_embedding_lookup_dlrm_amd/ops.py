@@ -576,7 +576,8 @@ class BwdPlan:
         _check(self._fn(*self._args), self._name)
 
 
-# Attention over user histories (include/dlrm_history.h).
+# Attention over user histories (include/dlrm_history.h). As the rest of this module, these calls are not recorded
+# for autograd: a gradient of qk_norm_rope is taken with qk_norm_rope_bwd, the attention has none.
 
 
 # The checks of these calls cost more host time than a small launch takes on the GPU, so they read each
@@ -863,7 +864,8 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, q_
     """Attention of the new tokens q [N, Hq, D] over the paged caches [pages, Hk, page, D]
     (dlrm_paged_attn); the sequences as in kv_append. window > 0 (with causal): a token sees the last
     `window` entries up to its own. max_q, max_kv: the most new tokens and the longest history of a
-    sequence, for how the work is cut; without them N and the page table's width are taken. Returns
+    sequence, for how the work is cut; without them N and the page table's width are taken, which is
+    right for one sequence and slow for many of one token each. Returns
     out [N, Hq, D], or (out, lse [N, Hq] fp32) with want_lse."""
     shape, qa = _heads_of(q, "q")
     N, Hq, D = shape

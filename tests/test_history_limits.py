@@ -68,3 +68,19 @@ def test_a_stream_of_another_device_is_refused():
     stream = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
     with pytest.raises(ValueError, match="stream is on"):
         ops._on(0, torch.device("cuda", 0), stream)
+
+
+def test_parts_of_histories(lib):
+    """The number of parts is odd, at most 511, and passes its limits by one part at most."""
+    for S in (1, 5, 64, 3000, 8192):
+        for Hq, Hk in ((1, 1), (32, 8), (16, 2)):
+            for D in (32, 64, 128, 256):
+                for max_q in (1, 40):
+                    for span in (1, 512, 513, 1024, 2048, 16384, 131009, 1 << 22):
+                        parts = _workspace(lib, S, S, Hq, Hk, D, max_q, span) // (S * Hq * (4 * D + 8))
+                        if parts == 0:
+                            continue
+                        assert parts % 2 == 1 and parts <= 511
+                        shortest = 512 if max_q * (Hq // Hk) > 16 else min(512, 131072 // D)
+                        assert parts - 1 <= -(-span // shortest), (S, Hq, Hk, D, max_q, span, parts)
+                        assert max_q > 1 or (parts - 1) * S * Hk <= 16384
