@@ -22,36 +22,36 @@ BLOCK = 16  # entries that share a scale
 def listed():
     return [
         # pages for one new event of each of 64 users out of 10,000, histories of up to 16k
-        dict(name="assign, serving batch", op="assign", seqs=64, users=10000, q_max=1, held_max=16383, page=16, width=1024, lens=1),
+        dict(name="assign: serving batch", op="assign", seqs=64, users=10000, q_max=1, held_max=16383, page=16, width=1024, lens=1),
         # pages for chunks of up to 2048 events of 300 users, most of whom are new
-        dict(name="assign, chunks", op="assign", seqs=300, users=4000, q_max=2048, held_max=600, page=32, width=128, lens=2),
+        dict(name="assign: chunks", op="assign", seqs=300, users=4000, q_max=2048, held_max=600, page=32, width=128, lens=2),
         # drafted events that were not taken are cut off again
-        dict(name="release, cut", op="release", seqs=96, users=10000, held_max=4096, page=16, width=512, cut=True, lens=3),
+        dict(name="release: cut", op="release", seqs=96, users=10000, held_max=4096, page=16, width=512, cut=True, lens=3),
         # life-long histories of 256 users are dropped
-        dict(name="release, long histories", op="release", seqs=256, users=1000, held_max=65536, page=16, width=4096, cut=False, lens=4),
+        dict(name="release: long histories", op="release", seqs=256, users=1000, held_max=65536, page=16, width=4096, cut=False, lens=4),
         # one new event for each of 96 users
-        dict(name="append, one token each", op="append", seqs=96, q_max=1, kv_max=4096, page=16, q_heads=16, kv_heads=4,
+        dict(name="append: one token each", op="append", seqs=96, q_max=1, kv_max=4096, page=16, q_heads=16, kv_heads=4,
              dim=128, rot=128, axes=1, inter=False, norm=True, type="bf16", lens=5),
         # histories filled in chunks of up to 2048 events
-        dict(name="append, chunks", op="append", seqs=12, q_max=2048, kv_max=8192, page=64, q_heads=32, kv_heads=8,
+        dict(name="append: chunks", op="append", seqs=12, q_max=2048, kv_max=8192, page=64, q_heads=32, kv_heads=8,
              dim=128, rot=64, axes=1, inter=True, norm=False, type="f16", lens=6),
         # one new event over a short history: latency
-        dict(name="attention, one short", op="attention", seqs=1, q_max=1, kv_max=301, page=16, q_heads=8, kv_heads=2,
+        dict(name="attention: one short", op="attention", seqs=1, q_max=1, kv_max=301, page=16, q_heads=8, kv_heads=2,
              dim=64, causal=True, window=0, type="f16", lens=7),
         # a serving batch: one new event each, histories from one event to 16k
-        dict(name="attention, serving batch", op="attention", seqs=64, q_max=1, kv_max=16384, page=64, q_heads=32,
+        dict(name="attention: serving batch", op="attention", seqs=64, q_max=1, kv_max=16384, page=64, q_heads=32,
              kv_heads=8, dim=128, causal=True, window=0, type="bf16", lens=8),
         # one life-long history
-        dict(name="attention, one long", op="attention", seqs=1, q_max=1, kv_max=131009, page=16, q_heads=16, kv_heads=2,
+        dict(name="attention: one long", op="attention", seqs=1, q_max=1, kv_max=131009, page=16, q_heads=16, kv_heads=2,
              dim=128, causal=True, window=0, type="bf16", lens=9),
         # ranking: up to 257 candidates per user, each over the user's whole history
-        dict(name="attention, candidates", op="attention", seqs=24, q_max=257, kv_max=1500, page=32, q_heads=4,
+        dict(name="attention: candidates", op="attention", seqs=24, q_max=257, kv_max=1500, page=32, q_heads=4,
              kv_heads=4, dim=64, causal=False, window=0, type="bf16", lens=10),
         # ragged chunks that see the last 1024 events, wide heads
-        dict(name="attention, ragged window", op="attention", seqs=12, q_max=513, kv_max=6000, page=16, q_heads=8,
+        dict(name="attention: ragged window", op="attention", seqs=12, q_max=513, kv_max=6000, page=16, q_heads=8,
              kv_heads=4, dim=256, causal=True, window=1024, type="f16", lens=11),
         # long chunks over long histories
-        dict(name="attention, long chunks", op="attention", seqs=4, q_max=2048, kv_max=8192, page=64, q_heads=32,
+        dict(name="attention: long chunks", op="attention", seqs=4, q_max=2048, kv_max=8192, page=64, q_heads=32,
              kv_heads=8, dim=128, causal=True, window=0, type="bf16", lens=12),
     ]
 
