@@ -1,13 +1,14 @@
 /*
  * dlrm_history.h -- C ABI of libdlrm_embbag.so, the encoder of a user's event
  * history: instead of summing the rows of a history bag (dlrm_embbag.h), the
- * events are attended to as a sequence. Four operations:
+ * events are attended to as a sequence. The operations:
  *   - norms of queries and keys per head with the position rotation in the same
  *     pass, and its backward (training);
  *   - appending keys and values to a paged cache, the norm and rotation applied
  *     on the way (serving);
  *   - attention of the new tokens of many users over that cache (serving: one new
- *     event, a chunk of a history, or candidates to rank).
+ *     event, a chunk of a history, or candidates to rank);
+ *   - pages of the cache handed out to growing histories and taken back, on the device.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -78,6 +79,8 @@ extern "C" {
 
 #define DLRM_MAX_AXES 8
 #define DLRM_STATUS_BAD_PAGE 4
+#define DLRM_STATUS_NO_ROOM 8   /* pages: a history longer than its page table, or too few free pages */
+#define DLRM_STATUS_BAD_USER 16 /* pages: a user that does not exist, or is in the call twice */
 
 /*
  * Norm and rotation of queries and keys, one pass.
@@ -166,6 +169,64 @@ int dlrm_paged_attn(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, 
                     const int32_t* q_offsets, const int32_t* kv_lens, const int32_t* page_table, int64_t table_stride,
                     int32_t table_width, int32_t causal, int32_t window, float scale, int32_t max_q, int32_t max_kv,
                     void* out, float* lse, void* workspace, size_t ws_bytes, int32_t* status, void* stream);
+
+/*
+ * Pages of the cache for many users, kept on the device. The caller owns the state:
+ *   held        int32 [users]: entries of each user's history
+ *   tables      int32 [users][table_width], rows table_stride elements apart: their pages.
+ *               Only the first ceil(held / page) of a row mean anything
+ *   free_pages  int32 [num_pages], free_count int32 [1]: the free pages are the first
+ *               *free_count of them; num_pages is the number of pages of the cache
+ * Calls that share a state are ordered by the caller. who is int32 [seqs], the user of each
+ * sequence, or NULL: sequence s is user s. held_out and count_out take the lengths of the call's
+ * users and the count after the call; with held and free_count themselves the state is updated in
+ * place. In other buffers they leave the state as it was, but for places in tables and free_pages
+ * that mean nothing then, so that a step may be planned and dropped.
+ */
+
+/* Workspace of dlrm_pages_assign and dlrm_pages_release. */
+int dlrm_pages_workspace_bytes(int32_t seqs, size_t* bytes);
+
+/*
+ * Pages for new entries: sequence s grows by new_lens[s] >= 0 entries. It needs
+ * ceil((held + new) / page) - ceil(held / page) pages, taken from the end of the free list,
+ * sequence by sequence: the first page of the first one is free_pages[*free_count - 1]. All outputs of
+ * dlrm_kv_append and dlrm_paged_attn's description of the call are written:
+ *   n           tokens that slots and positions have room for, 0 <= n < 2^31
+ *   q_offsets   out, int32 [seqs + 1]: sums of new_lens, from 0
+ *   kv_lens     out, int32 [seqs]: held + new
+ *   page_table  out, int32 [seqs][out_width], contiguous: the pages of each sequence, then -1
+ *   slots       out, int64 [n] or NULL: page * (entries of a page) + place of each new entry, for data
+ *               of the caller's own that lies beside the cache; -1 past the last token
+ *   positions   out, int32 [n] or NULL: place of each new entry in its history; -1 past the last token
+ * The call does all of it or nothing: if a user is outside [0, users) or has new entries in two
+ * sequences (DLRM_STATUS_BAD_USER), a length is negative or held longer than table_width pages, or
+ * there are more than n tokens (DLRM_STATUS_BAD_OFFSETS), a history would not fit out_width pages or
+ * too few pages are free (DLRM_STATUS_NO_ROOM), or *free_count is outside [0, num_pages]
+ * (DLRM_STATUS_BAD_PAGE), then no sequence grows: q_offsets are all 0, kv_lens and page_table are the
+ * histories as they are (a length that is not valid: none), slots and positions -1. A page outside
+ * [0, num_pages) in a user's row is copied as it is; its slots are -1 and flagged (DLRM_STATUS_BAD_PAGE).
+ * A user whose sequences have no new entries but one may be in the call more than once; those see the
+ * history as it was.
+ */
+int dlrm_pages_assign(int64_t n, int32_t seqs, int32_t users, const int32_t* new_lens, const int32_t* who,
+                      const int32_t* held, int32_t* held_out, int32_t* tables, int64_t table_stride,
+                      int32_t table_width, int32_t page, const int32_t* free_pages, int64_t num_pages,
+                      const int32_t* free_count, int32_t* count_out, int32_t* q_offsets, int32_t* kv_lens,
+                      int32_t* page_table, int32_t out_width, int64_t* slots, int32_t* positions, void* workspace,
+                      size_t ws_bytes, int32_t* status, void* stream);
+
+/*
+ * The way back: the history of sequence s keeps its first min(keep[s], held) entries (keep NULL: none),
+ * and the pages past them go to the end of the free list, sequence by sequence, in order. All of it or
+ * nothing: a user outside [0, users) or in the call twice (DLRM_STATUS_BAD_USER), a negative length or
+ * one past table_width pages (DLRM_STATUS_BAD_OFFSETS), or more free pages than num_pages
+ * (DLRM_STATUS_BAD_PAGE).
+ */
+int dlrm_pages_release(int32_t seqs, int32_t users, const int32_t* keep, const int32_t* who, const int32_t* held,
+                       int32_t* held_out, const int32_t* tables, int64_t table_stride, int32_t table_width,
+                       int32_t page, int32_t* free_pages, int64_t num_pages, const int32_t* free_count,
+                       int32_t* count_out, void* workspace, size_t ws_bytes, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -116,3 +116,74 @@ def attention(q, k_cache, v_cache, q_offsets, kv_lens, page_table, causal, windo
                 size[n, h] = scale * (np.abs(kk) @ np.abs(q[n, h].astype(np.float64))).max()
                 count[n, h] = use.sum()
     return out, lse, mag, size, count
+
+
+def pages_assign(new, users, held, tables, free, count, page, n, out_width):
+    """Pages handed out one by one. Returns (refusal bits, outputs, state): q_offsets, kv_lens, page_table, slots and
+    positions, and held, tables and count after the call, all as lists; refused calls change nothing."""
+    U, width = len(held), len(tables[0]) if len(tables) else 0
+    held, tables = list(held), [list(r) for r in tables]
+    valid = [0 <= u < U for u in users]
+    fits = [v and 0 <= held[u] <= width * page for u, v in zip(users, valid)]
+    before = [held[u] if f else 0 for u, f in zip(users, fits)]
+    grown = [max(m, 0) for m in new]
+    pages = lambda e: -(-e // page)
+    bits = 0
+    if not all(valid):
+        bits |= 16
+    if any(v and not f for v, f in zip(valid, fits)) or any(m < 0 for m in new) or sum(grown) > n:
+        bits |= 2
+    if not 0 <= count <= len(free):
+        bits |= 4
+    need = sum(pages(h + m) - pages(h) if v else pages(m) for h, m, v in zip(before, grown, valid))
+    if any(h + m > out_width * page for h, m in zip(before, grown)) or need > count:
+        bits |= 8
+    if not bits and len({u for u, m in zip(users, new) if m > 0}) < sum(m > 0 for m in new):
+        bits |= 16
+    slots, positions, offsets, lens, rows = [], [], [0], [], []
+    stack, refused = list(free[:max(count, 0)]), bits != 0
+    for u, h, m in zip(users, before, grown):
+        if refused:
+            m = 0
+        for i in range(pages(h), pages(h + m)):
+            tables[u][i] = stack.pop()
+        row = list(tables[u][:min(pages(h + m), out_width)]) if h + m else []
+        rows.append(row + [-1] * (out_width - len(row)))
+        for e in range(h, h + m):
+            p = tables[u][e // page]
+            good = 0 <= p < len(free)
+            bits |= 0 if good else 4
+            slots.append(p * page + e % page if good else -1)
+            positions.append(e)
+        offsets.append(offsets[-1] + m)
+        lens.append(h + m)
+        if m:
+            held[u] = h + m
+    rest = [-1] * (n - len(slots))
+    return bits, (offsets, lens, rows, slots + rest, positions + rest), (held, tables, len(stack) if count >= 0 else count)
+
+
+def pages_release(users, keep, held, tables, free, count, page):
+    """(refusal bits, held, free list, count) after the release."""
+    U, width = len(held), len(tables[0]) if len(tables) else 0
+    held, free = list(held), list(free)
+    valid = [0 <= u < U for u in users]
+    bits = 0 if all(valid) else 16
+    if any(v and not 0 <= held[u] <= width * page for u, v in zip(users, valid)) or any(k < 0 for k in keep):
+        bits |= 2
+    pages = lambda e: -(-e // page)
+    moved = []
+    for u, k, v in zip(users, keep, valid):
+        h = held[u] if v and 0 <= held[u] <= width * page else 0
+        moved.append((u, pages(min(max(k, 0), h)), pages(h), min(max(k, 0), h)))
+    if not 0 <= count <= len(free) or count + sum(b - a for _, a, b, _ in moved) > len(free):
+        bits |= 4
+    if not bits and len(set(users)) < len(users):
+        bits |= 16
+    if bits:
+        return bits, held, free, count
+    for u, a, b, k in moved:
+        free[count:count + b - a] = tables[u][a:b]
+        count += b - a
+        held[u] = k
+    return 0, held, free, count

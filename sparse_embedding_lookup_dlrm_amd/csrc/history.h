@@ -1,5 +1,5 @@
 // Host-side interface between the C ABI of dlrm_history.h (history_api.cpp) and its kernel
-// launchers (norm_rope.hip, paged_attn.hip). Plain C++: no device code.
+// launchers (norm_rope.hip, paged_attn.hip, pages.hip). Plain C++: no device code.
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -82,5 +82,22 @@ struct AttnArgs {
 size_t attn_workspace(int64_t n, int seqs, int q_heads, int kv_heads, int dim, int causal, int window, int max_q,
                       int max_kv);
 hipError_t launch_paged_attn(const AttnArgs& a, hipStream_t s);
+
+// Pages handed out and taken back.
+struct PagesArgs {
+  int64_t n, num_pages, table_stride;
+  int32_t seqs, users, page_shift, table_width, out_width;
+  const int32_t *lens, *who, *held;  // lens: new entries, or those to keep
+  const int32_t* count;
+  int32_t *tables, *free_pages, *held_out, *count_out;
+  int32_t *q_offsets, *kv_lens, *page_table, *positions;
+  int64_t* slots;
+  void* workspace;
+  int32_t* status;
+};
+
+size_t pages_workspace(int seqs);
+hipError_t launch_pages_assign(const PagesArgs& a, hipStream_t s);
+hipError_t launch_pages_release(const PagesArgs& a, hipStream_t s);
 
 }  // namespace dlrm

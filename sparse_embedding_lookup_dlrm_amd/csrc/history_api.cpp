@@ -121,6 +121,27 @@ int check_attn(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32
   return DLRM_OK;
 }
 
+// What assignment and release of pages share.
+int check_pages(int32_t seqs, int32_t users, const int32_t* who, const int32_t* held, const int32_t* held_out,
+                const int32_t* tables, int64_t table_stride, int32_t table_width, int32_t page,
+                const int32_t* free_pages, int64_t num_pages, const int32_t* count, const int32_t* count_out,
+                const void* workspace, size_t ws_bytes, const int32_t* status) {
+  if (seqs < 0 || users < 0 || table_width < 0 || num_pages < 0 || num_pages > kI32Max) return DLRM_E_INVAL;
+  if (page < 16 || page > 65536 || (page & (page - 1))) return DLRM_E_UNSUPPORTED;
+  if (static_cast<int64_t>(table_width) * page > kMostCounted || seqs > kMostCounted) return DLRM_E_UNSUPPORTED;
+  if (!who && seqs > users) return DLRM_E_INVAL;
+  if (table_stride < 0 || (users > 1 && table_stride < table_width)) return DLRM_E_INVAL;
+  if (!count || !count_out || (num_pages > 0 && !free_pages)) return DLRM_E_INVAL;
+  if (seqs > 0 && users > 0 && (!held || !held_out || (table_width > 0 && !tables))) return DLRM_E_INVAL;
+  if (!aligned(who, 4) || !aligned(held, 4) || !aligned(held_out, 4) || !aligned(tables, 4) ||
+      !aligned(free_pages, 4) || !aligned(count, 4) || !aligned(count_out, 4) || !aligned(status, 4) ||
+      !aligned(workspace, 256))
+    return DLRM_E_ALIGN;
+  if (ws_bytes < pages_workspace(seqs)) return DLRM_E_WORKSPACE;
+  if (!workspace) return DLRM_E_INVAL;
+  return DLRM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -253,6 +274,55 @@ int dlrm_paged_attn(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, 
   a.causal = causal != 0; a.window = window; a.max_q = max_q; a.max_kv = max_kv; a.scale = scale;
   a.out = out; a.lse = lse; a.workspace = workspace;
   return from_hip(launch_paged_attn(a, static_cast<hipStream_t>(stream)));
+}
+
+int dlrm_pages_workspace_bytes(int32_t seqs, size_t* bytes) {
+  if (!bytes || seqs < 0) return DLRM_E_INVAL;
+  if (seqs > kMostCounted) return DLRM_E_UNSUPPORTED;
+  *bytes = pages_workspace(seqs);
+  return DLRM_OK;
+}
+
+int dlrm_pages_assign(int64_t n, int32_t seqs, int32_t users, const int32_t* new_lens, const int32_t* who,
+                      const int32_t* held, int32_t* held_out, int32_t* tables, int64_t table_stride,
+                      int32_t table_width, int32_t page, const int32_t* free_pages, int64_t num_pages,
+                      const int32_t* free_count, int32_t* count_out, int32_t* q_offsets, int32_t* kv_lens,
+                      int32_t* page_table, int32_t out_width, int64_t* slots, int32_t* positions, void* workspace,
+                      size_t ws_bytes, int32_t* status, void* stream) {
+  PagesArgs a;
+  memset(&a, 0, sizeof(a));
+  if (n < 0 || n >= kI32Max || out_width < 0 || out_width > table_width) return DLRM_E_INVAL;
+  TRY(check_pages(seqs, users, who, held, held_out, tables, table_stride, table_width, page, free_pages, num_pages,
+                  free_count, count_out, workspace, ws_bytes, status));
+  if (!q_offsets || (seqs > 0 && (!new_lens || !kv_lens || (out_width > 0 && !page_table)))) return DLRM_E_INVAL;
+  if (!aligned(new_lens, 4) || !aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(page_table, 4) ||
+      !aligned(slots, 8) || !aligned(positions, 4))
+    return DLRM_E_ALIGN;
+  a.n = n; a.num_pages = num_pages; a.table_stride = table_stride;
+  a.seqs = seqs; a.users = users; a.page_shift = __builtin_ctz(page);
+  a.table_width = table_width; a.out_width = out_width;
+  a.lens = new_lens; a.who = who; a.held = held; a.count = free_count;
+  a.tables = tables; a.free_pages = const_cast<int32_t*>(free_pages); a.held_out = held_out; a.count_out = count_out;
+  a.q_offsets = q_offsets; a.kv_lens = kv_lens; a.page_table = page_table; a.positions = positions; a.slots = slots;
+  a.workspace = workspace; a.status = status;
+  return from_hip(launch_pages_assign(a, static_cast<hipStream_t>(stream)));
+}
+
+int dlrm_pages_release(int32_t seqs, int32_t users, const int32_t* keep, const int32_t* who, const int32_t* held,
+                       int32_t* held_out, const int32_t* tables, int64_t table_stride, int32_t table_width,
+                       int32_t page, int32_t* free_pages, int64_t num_pages, const int32_t* free_count,
+                       int32_t* count_out, void* workspace, size_t ws_bytes, int32_t* status, void* stream) {
+  PagesArgs a;
+  memset(&a, 0, sizeof(a));
+  TRY(check_pages(seqs, users, who, held, held_out, tables, table_stride, table_width, page, free_pages, num_pages,
+                  free_count, count_out, workspace, ws_bytes, status));
+  if (!aligned(keep, 4)) return DLRM_E_ALIGN;
+  a.num_pages = num_pages; a.table_stride = table_stride;
+  a.seqs = seqs; a.users = users; a.page_shift = __builtin_ctz(page); a.table_width = table_width;
+  a.lens = keep; a.who = who; a.held = held; a.count = free_count;
+  a.tables = const_cast<int32_t*>(tables); a.free_pages = free_pages; a.held_out = held_out; a.count_out = count_out;
+  a.workspace = workspace; a.status = status;
+  return from_hip(launch_pages_release(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -26,6 +26,8 @@ PAIRS_SELF, WITH_EMBEDDINGS = 1, 2  # interaction layout bits
 STATUS_BAD_INDEX = 1
 STATUS_BAD_OFFSETS = 2
 STATUS_BAD_PAGE = 4
+STATUS_NO_ROOM = 8
+STATUS_BAD_USER = 16
 MAX_TABLES = 128
 MAX_AXES = 8
 
@@ -92,6 +94,11 @@ _SIGNATURES = {
     "dlrm_paged_attn": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, *_HEADS, _c_void_p, _c_void_p, _i32, _i64,
                                        _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _i64, _i32, _i32, _i32, _f32, _i32,
                                        _i32, _c_void_p, _c_void_p, _c_void_p, _size_t, _c_void_p, _c_void_p]),
+    "dlrm_pages_workspace_bytes": (ctypes.c_int, [_i32, _P(_size_t)]),
+    "dlrm_pages_assign": (ctypes.c_int, [_i64, _i32, _i32, *[_c_void_p] * 5, _i64, _i32, _i32, _c_void_p, _i64,
+                                         *[_c_void_p] * 5, _i32, *[_c_void_p] * 3, _size_t, _c_void_p, _c_void_p]),
+    "dlrm_pages_release": (ctypes.c_int, [_i32, _i32, *[_c_void_p] * 5, _i64, _i32, _i32, _c_void_p, _i64,
+                                          *[_c_void_p] * 3, _size_t, _c_void_p, _c_void_p]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -901,3 +908,105 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, q_
                                      _ptr(workspace), 0 if workspace is None else workspace.numel(), status_at, s),
                "dlrm_paged_attn")
     return (out, lse) if want_lse else out
+
+
+@functools.lru_cache(maxsize=1024)
+def pages_workspace_bytes(S: int) -> int:
+    out = _size_t(0)
+    _check(lib().dlrm_pages_workspace_bytes(S, ctypes.byref(out)), "dlrm_pages_workspace_bytes")
+    return out.value
+
+
+def _pages_args(held, tables, free_pages, free_count, lens, name, users, S, held_out, count_out, status, workspace):
+    """Checks the state of pages and the sequences of a call. Returns (users, row stride, width, pages) and the
+    addresses (lens, users, held, held_out, tables, free_pages, free_count, count_out, workspace, status)."""
+    dev = held.get_device()
+    shape = tables.shape
+    if len(shape) != 2 or tables.dtype != torch.int32:
+        raise ValueError("tables must be torch.int32 [users, pages]")
+    U, width = shape
+    by_user, by_page = tables.stride()
+    if width > 1 and by_page != 1:
+        raise ValueError("the pages of a user in tables must be contiguous")
+    if tables.get_device() != dev:
+        raise ValueError(f"tables is on {tables.device}, not on {held.device}")
+    if users is None and S > U:
+        raise ValueError(f"{S} sequences of {U} users")
+    need = pages_workspace_bytes(S)
+    if workspace is not None:
+        _plain(workspace, "workspace", torch.uint8, need, dev, at_least=True)
+    # a stride over a single user is never taken, and may be any number
+    return (U, by_user if U > 1 else width, width, free_pages.numel(), need), (
+        _plain(lens, name, torch.int32, S, dev), _plain(users, "users", torch.int32, S, dev),
+        _plain(held, "held", torch.int32, U, dev), _plain(held_out, "held_out", torch.int32, U, dev), tables.data_ptr(),
+        _plain(free_pages, "free_pages", torch.int32, free_pages.numel(), dev),
+        _plain(free_count, "free_count", torch.int32, 1, dev), _plain(count_out, "count_out", torch.int32, 1, dev),
+        None if workspace is None else workspace.data_ptr(),
+        None if status is None else _plain(status, "status", torch.int32, 1, dev, at_least=True))
+
+
+def pages_assign(new_lens: torch.Tensor, held: torch.Tensor, tables: torch.Tensor, free_pages: torch.Tensor,
+                 free_count: torch.Tensor, page: int, N: int, *, users: Optional[torch.Tensor] = None,
+                 table_width: Optional[int] = None, held_out: Optional[torch.Tensor] = None,
+                 count_out: Optional[torch.Tensor] = None, want_slots: bool = True,
+                 workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Pages for new_lens[s] new entries of users[s] (None: user s), N tokens in all or fewer (dlrm_pages_assign).
+    The state: held [users], tables [users, width], free_pages [pages] of which the first free_count [1] are free;
+    updated in place, or with held_out and count_out the lengths and the count go there. Returns q_offsets
+    [S + 1], kv_lens [S], page_table [S, table_width] (None: the width of tables), slots [N] int64 and positions [N] (both
+    None without want_slots). If anything does not fit nothing is handed out, and status says why."""
+    S = new_lens.numel()
+    where = held.device
+    if held_out is None:
+        held_out = held
+    if count_out is None:
+        count_out = free_count
+    (U, by_user, width, pages, need), (lens_at, users_at, held_at, held_out_at, tables_at, free_at, count_at, count_out_at,
+                                       workspace_at, status_at) = _pages_args(
+        held, tables, free_pages, free_count, new_lens, "new_lens", users, S, held_out, count_out, status, workspace)
+    if table_width is None:
+        table_width = width
+    if not 0 <= N < _I32_MAX or not 0 <= table_width <= width or not 0 < page <= _I32_MAX:
+        raise ValueError(f"N {N}, table_width {table_width} or page {page} out of range")
+    with _on(held.get_device(), where, stream) as s:
+        # one allocation: slots, then the 32-bit outputs
+        wide = N if want_slots else 0
+        sizes = [2 * wide, S + 1, S, S * table_width, wide]
+        if workspace is None:
+            sizes.insert(0, need // 4)
+        parts = torch.empty(sum(sizes), dtype=torch.int32, device=where).split(sizes)
+        if workspace is None:
+            workspace_at, parts = parts[0].data_ptr(), parts[1:]
+        slots, q_offsets, kv_lens, page_table, positions = parts
+        _check(lib().dlrm_pages_assign(N, S, U, lens_at, users_at, held_at, held_out_at, tables_at, by_user, width, page,
+                                       free_at, pages, count_at, count_out_at, q_offsets.data_ptr(), kv_lens.data_ptr(),
+                                       page_table.data_ptr(), table_width, slots.data_ptr() if want_slots else None,
+                                       positions.data_ptr() if want_slots else None, workspace_at,
+                                       need if workspace is None else workspace.numel(), status_at, s),
+               "dlrm_pages_assign")
+    page_table = page_table.view(S, table_width)
+    if not want_slots:
+        return q_offsets, kv_lens, page_table, None, None
+    return q_offsets, kv_lens, page_table, slots.view(torch.int64), positions
+
+
+def pages_release(held: torch.Tensor, tables: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
+                  page: int, *, users: Optional[torch.Tensor] = None, keep: Optional[torch.Tensor] = None,
+                  held_out: Optional[torch.Tensor] = None, count_out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Histories of users (None: of all) cut to their first keep entries (None: dropped), their other pages back in
+    the free list (dlrm_pages_release). The state as in pages_assign."""
+    S = held.numel() if users is None else users.numel()
+    where = held.device
+    (U, by_user, width, pages, need), at = _pages_args(held, tables, free_pages, free_count, keep, "keep", users, S,
+                                                       held if held_out is None else held_out,
+                                                       free_count if count_out is None else count_out, status, workspace)
+    lens_at, users_at, held_at, held_out_at, tables_at, free_at, count_at, count_out_at, workspace_at, status_at = at
+    if not 0 < page <= _I32_MAX:
+        raise ValueError(f"page {page} out of range")
+    with _on(held.get_device(), where, stream) as s:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=where)
+        _check(lib().dlrm_pages_release(S, U, lens_at, users_at, held_at, held_out_at, tables_at, by_user, width, page,
+                                        free_at, pages, count_at, count_out_at, workspace.data_ptr(), workspace.numel(),
+                                        status_at, s), "dlrm_pages_release")
