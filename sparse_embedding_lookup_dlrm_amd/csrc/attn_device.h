@@ -1,0 +1,245 @@
+// What the attention kernels of the 16-bit and the 8-bit cache share: sequences and what their tokens see,
+// how a call is cut, matrix instructions, and the join of split histories.
+//
+// For one head of the cache, the `group` query heads that read it and the new tokens of a
+// sequence form rows, row = token * group + head in group. With c = scale log2(e), scores
+// s = q . k and a running maximum m and sum l per row:
+//     m' = max(m, max s),  p = 2^(c (s - m')),  l' = l 2^(c (m - m')) + sum p,
+//     O' = O 2^(c (m - m')) + sum p v,          out = O / l,   lse = scale m + ln l.
+#pragma once
+
+#include <type_traits>
+
+#include "history_device.h"
+
+namespace dlrm {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// fp16 weights are held times 2^8: a weight below 2^-14 of the largest would otherwise be
+// subnormal and lose bits. bf16 has the exponent range of fp32.
+template <int DT>
+constexpr float kLift = DT == DLRM_F16 ? 8.f : 0.f;
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
+  if constexpr (DT == DLRM_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+
+// All bits of those of the two 16-bit values of a dword that are infinite or NaN.
+template <int DT>
+__device__ __forceinline__ uint32_t not_finite_halves(uint32_t w) {
+  constexpr uint32_t e = DT == DLRM_BF16 ? 0x7f80u : 0x7c00u;
+  return ((w & e) == e ? 0xffffu : 0u) | ((w >> 16 & e) == e ? 0xffff0000u : 0u);
+}
+
+// A word that is the same for the whole wave, read by the scalar unit: no wait for it holds up vector
+// loads on the way. Nothing writes the arrays read so while a kernel runs.
+__device__ __forceinline__ int scalar_load(const int32_t* p, long long i) {
+  return ((const __attribute__((address_space(4))) int32_t*)p)[i];
+}
+
+// A sequence of the call: its tokens and its history, checked.
+struct Seq {
+  int first, tokens, held;  // first token of the call, new tokens, entries (0 .. page table's room)
+};
+
+__device__ __forceinline__ Seq load_seq(const Paged& p, long long n, int seq) {
+  Seq s;
+  const int a = scalar_load(p.q_offsets, seq), b = scalar_load(p.q_offsets, seq + 1LL);
+  const int first = scalar_load(p.q_offsets, 0), last = scalar_load(p.q_offsets, p.seqs);
+  const int held = scalar_load(p.kv_lens, seq), room = p.table_width << p.page_shift;
+  const bool bad = a < 0 || a < first || b < a || b > last || b > n;
+  s.first = bad ? 0 : a;
+  s.tokens = bad ? 0 : b - a;
+  s.held = held < 0 ? 0 : held > room ? room : held;
+  if ((bad || s.held != held) && threadIdx.x == 0) flag(p.status, DLRM_STATUS_BAD_OFFSETS);
+  if (p.num_pages == 0) {  // nothing to read; the last token would see the last entry
+    if (s.held > 0 && s.tokens > 0 && threadIdx.x == 0) flag(p.status, DLRM_STATUS_BAD_PAGE);
+    s.held = 0;
+  }
+  return s;
+}
+
+// Entries [lo, hi) that a token sees.
+struct Span {
+  int lo, hi;
+};
+
+__device__ __forceinline__ Span seen_by(const Seq& s, int token, int causal, int window) {
+  if (!causal) return {0, s.held};
+  const long long at = static_cast<long long>(s.held) - s.tokens + token;
+  const long long hi = at + 1, lo = window ? at - window + 1 : 0;
+  return {static_cast<int>(lo > 0 ? lo : 0), static_cast<int>(hi > 0 ? hi : 0)};
+}
+
+constexpr int kWaves = 4;
+constexpr int kThreads = kWaves * kWave;
+
+// The larger of a lane and the one 32 away.
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The same within pairs of sixteen lanes.
+__device__ __forceinline__ float max_quarters(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_quarters(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// How a call is cut: q_tiles tiles of rows per sequence and head, splits parts of a tile's entries. The
+// grid is heads x (tiles x parts) x sequences.
+struct Cut {
+  int q_tiles, splits, part;  // part: entries of a part, unless the history is longer than announced
+  float* o;                   // [splits][n][q_heads][dim], not yet divided by the sums
+  float2* ml;                 // [n][q_heads][splits]: maximum and sum
+};
+
+// Entries that the rows [row0, row_end) of a sequence see between them, and their parts.
+struct Reach {
+  int tok0, tok1;
+  int lo, hi;          // some row sees these
+  int all_lo, all_hi;  // every row sees these
+  int first, part, parts;
+  __device__ __forceinline__ Reach(const Seq& s, int row0, int row_end, int group, int causal, int window,
+                                   const Cut& cut) {
+    tok0 = row0 / group;
+    tok1 = (row_end - 1) / group;
+    const Span s0 = seen_by(s, tok0, causal, window), s1 = seen_by(s, tok1, causal, window);
+    lo = s0.lo;
+    hi = s1.hi;
+    all_lo = s1.lo;
+    all_hi = s0.hi;
+    first = lo & ~31;
+    const int span = hi > first ? hi - first : 0;
+    part = cut.part;
+    // spans stay below 2^31 - 2^17, so the sums below fit 32 bits
+    if (span > static_cast<long long>(part) * cut.splits)
+      part = ((static_cast<uint32_t>(span) + cut.splits - 1) / static_cast<uint32_t>(cut.splits) + 63) & ~63u;
+    parts = span > part ? (static_cast<uint32_t>(span) + part - 1) / static_cast<uint32_t>(part) : 1;
+  }
+};
+
+// Eight elements of a row's result, x still to be divided by the sum; a row that saw nothing is zero.
+template <int DT>
+__device__ __forceinline__ void finish(const AttnArgs& a, long long to, int at, float* x, float m, float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int d = 0; d < 8; ++d) x[d] *= inv;
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + to * a.dim + at) = narrow<DT>(x);
+  if (at == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : fmaf(m, a.scale, logf(l) - kLift<DT> * kLn2);
+}
+
+// ---------------------------------------------------------------------------
+// Joins the parts of split histories: D / 8 lanes to a row, eight elements each. Slots > 1: the parts of
+// a row are shared between that many groups of lanes (a workgroup to a row), which is quicker where
+// there are many parts and so few rows.
+// ---------------------------------------------------------------------------
+constexpr int kMaxSplits = 512;
+
+template <int DT, int D, int Slots>
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, Cut cut, int tile_rows) {
+  constexpr int Lanes = D / 8, Rows = kThreads / (Lanes * Slots);
+  __shared__ float lds_x[Slots > 1 ? Slots : 1][D];
+  __shared__ float2 lds_ml[Slots];
+  const int group = a.q_heads / a.kv_heads;
+  const float c = a.scale * kLog2e;
+  const int at = threadIdx.x % Lanes * 8, slot = threadIdx.x / Lanes % Slots;
+  for (int seq = blockIdx.y; seq < a.paged.seqs; seq += gridDim.y) {
+    const Seq sq = load_seq(a.paged, a.n, seq);
+    const int rows = sq.tokens * a.q_heads;
+    for (long long first = static_cast<long long>(blockIdx.x) * Rows; first < rows;
+         first += static_cast<long long>(gridDim.x) * Rows) {
+      const int row = static_cast<int>(first) + threadIdx.x / (Lanes * Slots);
+      if (row >= rows) continue;  // with Slots > 1 there is one row, and no thread leaves it
+      const int tok = row / a.q_heads, in_head = tok * group + (row - tok * a.q_heads) % group;
+      const int row0 = in_head / tile_rows * tile_rows, in_all = sq.tokens * group;
+      const Reach rc(sq, row0, in_all - row0 > tile_rows ? row0 + tile_rows : in_all, group, a.causal, a.window, cut);
+      if (rc.parts == 1) continue;
+      const long long to = static_cast<long long>(sq.first) * a.q_heads + row;
+      const float2* ml = cut.ml + to * cut.splits;
+      const float* o = cut.o + to * D + at;
+      const long long step = a.n * a.q_heads * D;
+      float m = -INFINITY, l = 0.f, x[8] = {};
+#pragma unroll 4
+      for (int i = slot; i < rc.parts; i += Slots) m = fmaxf(m, ml[i].x);
+#pragma unroll 4
+      for (int i = slot; i < rc.parts; i += Slots) {
+        const float4 u = *reinterpret_cast<const float4*>(o + i * step);
+        const float4 v = *reinterpret_cast<const float4*>(o + i * step + 4);
+        const float2 p = ml[i];
+        const float w = p.x == -INFINITY ? 0.f : exp2f((p.x - m) * c);
+        l = fmaf(p.y, w, l);
+        x[0] = fmaf(u.x, w, x[0]); x[1] = fmaf(u.y, w, x[1]); x[2] = fmaf(u.z, w, x[2]); x[3] = fmaf(u.w, w, x[3]);
+        x[4] = fmaf(v.x, w, x[4]); x[5] = fmaf(v.y, w, x[5]); x[6] = fmaf(v.z, w, x[6]); x[7] = fmaf(v.w, w, x[7]);
+      }
+      if constexpr (Slots == 1) {
+        finish<DT>(a, to, at, x, m, l);
+      } else {
+        __syncthreads();  // the row before was read
+#pragma unroll
+        for (int d = 0; d < 8; ++d) lds_x[slot][at + d] = x[d];
+        if (at == 0) lds_ml[slot] = make_float2(m, l);
+        __syncthreads();
+        if (slot == 0) {
+          for (int i = 1; i < Slots; ++i) m = fmaxf(m, lds_ml[i].x);
+          l = 0.f;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) x[d] = 0.f;
+          for (int i = 0; i < Slots; ++i) {
+            const float2 p = lds_ml[i];
+            const float w = p.x == -INFINITY ? 0.f : exp2f((p.x - m) * c);
+            l = fmaf(p.y, w, l);
+#pragma unroll
+            for (int d = 0; d < 8; ++d) x[d] = fmaf(lds_x[i][at + d], w, x[d]);
+          }
+          finish<DT>(a, to, at, x, m, l);
+        }
+      }
+    }
+  }
+}
+
+template <int DT, int D, int Slots>
+void join(const AttnArgs& a, const Cut& cut, int tile_rows, hipStream_t s) {
+  constexpr int Rows = kThreads / (D / 8 * Slots);
+  const long long rows = static_cast<long long>(a.max_q) * a.q_heads, groups = (rows + Rows - 1) / Rows;
+  const unsigned x = static_cast<unsigned>(groups < 1 ? 1 : groups < 65535 ? groups : 65535);
+  const unsigned y = static_cast<unsigned>(a.paged.seqs < 65535 / 8 ? a.paged.seqs : 65535 / 8);
+  hipLaunchKernelGGL((attn_join_kernel<DT, D, Slots>), dim3(x, y), dim3(kThreads), 0, s, a, cut, tile_rows);
+}
+
+// Rows of a tile: 16 for the rows kernel (one wave's matrix instruction), 128 for the tile kernel.
+int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
+
+constexpr size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+size_t cut_bytes(const Cut& c, int64_t n, int q_heads, int dim) {
+  if (c.splits == 1) return 0;
+  const size_t rows = static_cast<size_t>(n) * q_heads * c.splits;
+  return round256(rows * dim * sizeof(float)) + rows * sizeof(float2);
+}
+
+}  // namespace
+}  // namespace dlrm
