@@ -8,6 +8,7 @@
  *     on the way (serving);
  *   - attention of the new tokens of many users over that cache (serving: one new
  *     event, a chunk of a history, or candidates to rank);
+ *   - append and attention with the cache in 8 bits;
  *   - pages of the cache handed out to growing histories and taken back, on the device.
  *
  * Conventions shared by every entry point
@@ -169,6 +170,35 @@ int dlrm_paged_attn(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, 
                     const int32_t* q_offsets, const int32_t* kv_lens, const int32_t* page_table, int64_t table_stride,
                     int32_t table_width, int32_t causal, int32_t window, float scale, int32_t max_q, int32_t max_kv,
                     void* out, float* lse, void* workspace, size_t ws_bytes, int32_t* status, void* stream);
+
+/*
+ * The 8-bit cache: half the bytes of a 16-bit one. k_cache and v_cache hold e4m3 codes (sign, 4 bits of
+ * exponent with bias 7, 3 bits of significand; at most 448, no infinities, 0x7f and 0xff are NaN), in the
+ * layout of the paged cache above with one byte an element (strides in bytes, multiples of 16). kv_scales
+ * holds two bytes for each block of DLRM_KV_BLOCK entries of a head, the first for the keys and the second
+ * for the values: [page / DLRM_KV_BLOCK][2] contiguous for a page and head, heads scale_head_stride and
+ * pages scale_page_stride bytes apart (even). A code c under byte b stands for c * 2^(b - 127), and for NaN
+ * under b = 255 (the types e4m3fn and e8m0fnu of the OCP 8-bit formats).
+ */
+#define DLRM_KV_BLOCK 16
+
+/* Workspace of dlrm_paged_attn_q8 for these sizes (0 where no history is split). */
+int dlrm_paged_attn_q8_workspace_bytes(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                                       int32_t causal, int32_t window, int32_t max_q, int32_t max_kv, size_t* bytes);
+
+/*
+ * dlrm_paged_attn over the 8-bit cache: the same attention over the values that the codes stand for. In the
+ * products these are of dtype, which holds them exactly within its range: of DLRM_F16 one past 65504 is
+ * infinite and one below 2^-14 is a multiple of 2^-24, of DLRM_BF16 one below 2^-126 may count as zero.
+ */
+int dlrm_paged_attn_q8(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t dtype,
+                       const void* q, int64_t q_stride, int64_t q_head_stride, const void* k_cache,
+                       const void* v_cache, int32_t page, int64_t num_pages, int64_t cache_page_stride,
+                       int64_t cache_head_stride, const uint8_t* kv_scales, int64_t scale_page_stride,
+                       int64_t scale_head_stride, const int32_t* q_offsets, const int32_t* kv_lens,
+                       const int32_t* page_table, int64_t table_stride, int32_t table_width, int32_t causal,
+                       int32_t window, float scale, int32_t max_q, int32_t max_kv, void* out, float* lse,
+                       void* workspace, size_t ws_bytes, int32_t* status, void* stream);
 
 /*
  * Pages of the cache for many users, kept on the device. The caller owns the state:

@@ -23,7 +23,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdlrm_embbag.so")
 
 SOURCES = ["embbag_fwd.hip", "embbag_bwd.hip", "offsets.hip", "noalloc.hip", "probe.hip", "api.cpp",
-           "norm_rope.hip", "paged_attn.hip", "pages.hip", "history_api.cpp"]
+           "norm_rope.hip", "paged_attn.hip", "paged_attn_q8.hip", "pages.hip",
+           "history_api.cpp"]
 ARCH = "gfx950"
 
 # Packed fp32 instructions are switched off for all device code.
@@ -64,7 +65,7 @@ def _compile(src: str, asm: bool) -> str:
 
 def build(asm: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(4, os.cpu_count() or 1)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         objs = list(ex.map(lambda s: _compile(s, asm), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]

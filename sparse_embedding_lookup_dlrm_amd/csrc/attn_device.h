@@ -38,6 +38,24 @@ __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f3
                                                   0);
 }
 
+// The 8-bit cache: e4m3 codes, and for each block of 16 entries of a head a byte b for the keys and one for the
+// values, whose codes stand for code x 2^(b - 127).
+constexpr int kScaleBlock = 16;
+
+// Two values of a dword of codes (the low or the high half) in the 16-bit type; exact within its range. The
+// instruction takes the power of two from the exponent of its scale.
+template <int DT, bool HIGH>
+__device__ __forceinline__ uint32_t widen_codes(uint32_t codes, float scale) {
+  if constexpr (DT == DLRM_BF16)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, HIGH));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, HIGH));
+}
+
+// The scales of keys and of values from the two bytes of a block.
+__device__ __forceinline__ float key_scale(int bytes) { return __uint_as_float((bytes & 0xff) << 23); }
+__device__ __forceinline__ float value_scale(int bytes) { return __uint_as_float((bytes >> 8 & 0xff) << 23); }
+
 // All bits of those of the two 16-bit values of a dword that are infinite or NaN.
 template <int DT>
 __device__ __forceinline__ uint32_t not_finite_halves(uint32_t w) {
@@ -151,6 +169,65 @@ __device__ __forceinline__ void finish(const AttnArgs& a, long long to, int at, 
   if (at == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : fmaf(m, a.scale, logf(l) - kLift<DT> * kLn2);
 }
 
+template <int D>
+constexpr int kPitch = D + 4;  // floats; a row of O in LDS
+
+// The end of a workgroup of the rows kernels: joins its four waves' maxima, sums and O of 16 rows, lane (g, c16) with
+// elements 4 E g .. 4 E (g + 1) of row c16, E = D / 16 at a time, and writes the rows' results or their part.
+template <int DT, int D>
+__device__ __forceinline__ void join_waves(const AttnArgs& a, const Cut& cut, const Reach& rc, const Seq& sq, int row0,
+                                           int row_end, int group, int head, int split, float m, float l,
+                                           const f32x4 (&o)[D / 16], float (*lds_o)[16 * kPitch<D>],
+                                           float2 (*lds_ml)[16]) {
+  constexpr int E = D / 16, Rows = 16, Pitch = kPitch<D>;
+  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, c16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const float c = a.scale * kLog2e;
+  l = add_halves(add_quarters(l));
+  if (g == 0) lds_ml[wave][c16] = make_float2(m, l);
+  __syncthreads();
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_ml[w][c16].x);
+  const float keep = m == -INFINITY ? 0.f : exp2f((m - top) * c);
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int e = 0; e < E; ++e) lds_o[wave][c16 * Pitch + (4 * g + r) * E + e] = o[e][r] * keep;
+  __syncthreads();
+  constexpr int Pieces = D / 8;
+  for (int i = threadIdx.x; i < Rows * Pieces; i += kThreads) {
+    const int r16 = i / Pieces, at = i % Pieces * 8;
+    const int out_row = row0 + r16;
+    if (out_row >= row_end) continue;
+    float mt = -INFINITY, lt = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) mt = fmaxf(mt, lds_ml[w][r16].x);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float2 ml = lds_ml[w][r16];
+      lt += ml.y * (ml.x == -INFINITY ? 0.f : exp2f((ml.x - mt) * c));
+    }
+    float x[8];
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      x[d] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) x[d] += lds_o[w][r16 * Pitch + at + d];
+    }
+    const int tok = out_row / group, gi = out_row - tok * group;
+    const long long to = static_cast<long long>(sq.first + tok) * a.q_heads + head * group + gi;
+    if (rc.parts == 1) {
+      finish<DT>(a, to, at, x, mt, lt);
+    } else {
+      float* p = cut.o + (split * a.n * a.q_heads + to) * D + at;
+      *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+      if (at == 0) cut.ml[to * cut.splits + split] = make_float2(mt, lt);
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Joins the parts of split histories: D / 8 lanes to a row, eight elements each. Slots > 1: the parts of
 // a row are shared between that many groups of lanes (a workgroup to a row), which is quicker where
@@ -239,6 +316,28 @@ size_t cut_bytes(const Cut& c, int64_t n, int q_heads, int dim) {
   if (c.splits == 1) return 0;
   const size_t rows = static_cast<size_t>(n) * q_heads * c.splits;
   return round256(rows * dim * sizeof(float)) + rows * sizeof(float2);
+}
+
+// The kernel of a call that is cut into parts, and their join.
+template <int DT, int D>
+hipError_t launch_cut(const AttnArgs& a, Cut cut, void (*rows_kernel)(AttnArgs, Cut), void (*tile_kernel)(AttnArgs, Cut),
+                      int tile_threads, hipStream_t s) {
+  const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
+  cut.o = static_cast<float*>(a.workspace);
+  cut.ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) +
+                                     round256(static_cast<size_t>(a.n) * a.q_heads * cut.splits * D * sizeof(float)));
+  const dim3 grid(a.kv_heads, cut.q_tiles * cut.splits, a.paged.seqs < 65535 ? a.paged.seqs : 65535);
+  const int tile = tile_rows(rows);
+  if (tile == 16)
+    hipLaunchKernelGGL(rows_kernel, grid, dim3(kThreads), 0, s, a, cut);
+  else
+    hipLaunchKernelGGL(tile_kernel, grid, dim3(tile_threads), 0, s, a, cut);
+  const long long all_rows = rows * a.kv_heads * a.paged.seqs;
+  if (cut.splits > 16 && all_rows <= 512)
+    join<DT, D, kThreads / (D / 8)>(a, cut, tile, s);
+  else if (cut.splits > 1)
+    join<DT, D, 1>(a, cut, tile, s);
+  return hipGetLastError();
 }
 
 }  // namespace

@@ -95,7 +95,10 @@ constexpr int kHalves = D == 256 ? 2 : 1;
 template <int D>
 constexpr int kTileThreads = kThreads * kHalves<D>;
 
-template <int DT, int D>
+// Q8: the cache holds 8-bit codes. A wave then takes its 16 entries of a tile through registers, loaded while the
+// tile two before is worked on, and widens them on their way to LDS: once for the workgroup, not once for each of its
+// waves.
+template <int DT, int D, bool Q8>
 __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs a, Cut cut) {
   constexpr int K = kTileKeys;
   constexpr int T = D == 256 ? 1 : K / 32;  // 32-entry blocks of scores held at once
@@ -132,8 +135,10 @@ __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs 
   for (int seq = blockIdx.z; seq < pg.seqs; seq += gridDim.z) {
     const Seq sq = load_seq(pg, a.n, seq);
     const int rows = sq.tokens * group;
-    const uint16_t* kh = static_cast<const uint16_t*>(a.k_cache) + head * pg.head_stride;
-    const uint16_t* vh = static_cast<const uint16_t*>(a.v_cache) + head * pg.head_stride;
+    using Stored = std::conditional_t<Q8, uint8_t, uint16_t>;
+    const Stored* kh = static_cast<const Stored*>(a.k_cache) + head * pg.head_stride;
+    const Stored* vh = static_cast<const Stored*>(a.v_cache) + head * pg.head_stride;
+    const uint8_t* sh = Q8 ? a.kv_scales + head * a.scale_head_stride : nullptr;
     const int32_t* table = pg.page_table + seq * pg.table_stride;
 
     // the last rows of a causal chunk see the most: they start first
@@ -211,10 +216,75 @@ __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs 
       };
       constexpr int kAllGood = (1 << (K / 16)) - 1;
 
+      // 8-bit codes: this wave's 16 entries of a tile, a contiguous piece of the cache, in registers. Chunk bytes a
+      // lane and load, which are one or two pieces of 16 bytes in LDS.
+      constexpr int Chunk = D == 32 ? 8 : 16, Loads = 16 * D / (kWave * Chunk);
+      uint32_t raw[3 - H][Q8 ? Loads : 1][4];  // keys and values, or this half's
+      int scales = 0;  // of the blocks whose pages are at hand, one to a lane
+      const auto look_up_scales = [&](int k0, int page, uint64_t good) {
+        const int key = k0 + 16 * lane, known = (key < hi ? key : hi - 1) & page_mask;
+        const int from = good >> lane & 1 ? page : 0;
+        return static_cast<int>(
+            *reinterpret_cast<const uint16_t*>(sh + from * a.scale_page_stride + known / kScaleBlock * 2));
+      };
+      const auto fetch_tile = [&](int k0, int pages, uint64_t good, int at) {
+        const int key = k0 + 16 * wave, known = key < hi ? key : hi - 1;
+        const int block = 4 * at + wave;
+        const int page = good >> block & 1 ? __builtin_amdgcn_readlane(pages, block) : 0;
+        const long long from = page * pg.page_stride + (known & page_mask & ~15) * D + lane * Chunk;
+#pragma unroll
+        for (int i = 0; i < Loads; ++i) {
+          const uint8_t* first = reinterpret_cast<const uint8_t*>(H == 1 || half == 0 ? kh : vh);
+          __builtin_memcpy(raw[0][i], __builtin_assume_aligned(first + from + i * kWave * Chunk, Chunk), Chunk);
+          if constexpr (H == 1)
+            __builtin_memcpy(raw[1][i], __builtin_assume_aligned(
+                reinterpret_cast<const uint8_t*>(vh) + from + i * kWave * Chunk, Chunk), Chunk);
+        }
+      };
+      const auto put_piece = [&](uint16_t* to, const uint32_t* codes, float scale) {
+        *reinterpret_cast<uint4*>(to) =
+            make_uint4(widen_codes<DT, false>(codes[0], scale), widen_codes<DT, true>(codes[0], scale),
+                       widen_codes<DT, false>(codes[1], scale), widen_codes<DT, true>(codes[1], scale));
+      };
+      const auto put_tile = [&](int at, int buf) {
+        const int two = __builtin_amdgcn_readlane(scales, 4 * at + wave);
+        const float ks = key_scale(two), vs = value_scale(two);
+#pragma unroll
+        for (int i = 0; i < Loads; ++i) {
+          const int r = (i * kWave + lane) * Chunk / D, piece = (i * kWave + lane) * Chunk % D / 8;
+#pragma unroll
+          for (int j = 0; j < Chunk / 8; ++j) {
+            const int to = (16 * wave + r) * D;
+            if (H == 1 || half == 0)
+              put_piece(lds_k[buf] + to + ((piece + j) ^ key_swizzle<D>(r)) * 8, raw[0][i] + 2 * j, ks);
+            if (H == 1 || half == 1)
+              put_piece(lds_v[buf] + to + ((piece + j) ^ value_swizzle<D>(r)) * 8, raw[2 - H][i] + 2 * j, vs);
+          }
+        }
+      };
+
       __syncthreads();  // the tiles of the rows before are no longer read
       int pages = 0, pages_next = 0, at = 0, good_next = 0;
       uint64_t good64 = 0;
-      if (k_first < hi) {
+      const auto next_pages = [&](int k0) {  // the tile at k0 is the first of the next 16
+        pages = pages_next;
+        good64 = good_pages(k0, pages);
+        pages_next = look_up(k0 + 16 * K < hi ? k0 + 16 * K : k0);
+        if constexpr (Q8) scales = look_up_scales(k0, pages, good64);
+      };
+      if constexpr (Q8) {
+        if (k_first < hi) {
+          pages_next = look_up(k_first);
+          next_pages(k_first);
+          fetch_tile(k_first, pages, good64, 0);
+          put_tile(0, 0);
+          good_next = static_cast<int>(good64) & kAllGood;
+          if (k_first + K < hi) {
+            at = 1;
+            fetch_tile(k_first + K, pages, good64, 1);
+          }
+        }
+      } else if (k_first < hi) {
         pages = look_up(k_first);
         pages_next = look_up(k_first + 16 * K < hi ? k_first + 16 * K : k_first);
         good64 = good_pages(k_first, pages);
@@ -222,16 +292,22 @@ __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs 
         good_next = static_cast<int>(good64) & kAllGood;
       }
       for (int k0 = k_first, buf = 0; k0 < hi; k0 += K, buf ^= 1) {
-        wait_copies();
+        if constexpr (!Q8) wait_copies();
         __syncthreads();  // this tile is in LDS, and the other one is no longer read
         const int good = good_next;
-        if (k0 + K < hi) {
-          at = (at + 1) & 15;
-          if (at == 0) {
-            pages = pages_next;
-            good64 = good_pages(k0 + K, pages);
-            pages_next = look_up(k0 + 17 * K < hi ? k0 + 17 * K : k0);
+        if constexpr (Q8) {
+          if (k0 + K < hi) {
+            put_tile(at, buf ^ 1);
+            good_next = static_cast<int>(good64 >> (4 * at)) & kAllGood;
+            if (k0 + 2 * K < hi) {
+              at = (at + 1) & 15;
+              if (at == 0) next_pages(k0 + 2 * K);
+              fetch_tile(k0 + 2 * K, pages, good64, at);
+            }
           }
+        } else if (k0 + K < hi) {
+          at = (at + 1) & 15;
+          if (at == 0) next_pages(k0 + K);
           copy_tile(k0 + K, pages, good64, at, buf ^ 1);
           good_next = static_cast<int>(good64 >> (4 * at)) & kAllGood;
         }
@@ -356,12 +432,21 @@ __global__ __launch_bounds__(kTileThreads<D>, 2) void attn_tile_kernel(AttnArgs 
             const int key = k0 + e;
             const int page = key < hi ? scalar_load(table, key >> pg.page_shift) : -1;
             if (page < 0 || page >= pg.num_pages) continue;
-            const uint16_t* v =
+            const Stored* v =
                 vh + page * pg.page_stride + static_cast<long long>(key & page_mask) * D + half * 32 * C + 4 * h;
             const bool mine = key >= row_lo && key < row_hi;
+            float vs = 0.f;
+            if constexpr (Q8)
+              vs = value_scale(sh[page * a.scale_page_stride + (key & page_mask) / kScaleBlock * 2 + 1] << 8);
 #pragma unroll
             for (int i = 0; i < 4 * C; ++i) {
-              const uint2 w = *reinterpret_cast<const uint2*>(v + 8 * i);
+              uint2 w;
+              if constexpr (Q8) {
+                const uint32_t codes = *reinterpret_cast<const uint32_t*>(v + 8 * i);
+                w = make_uint2(widen_codes<DT, false>(codes, vs), widen_codes<DT, true>(codes, vs));
+              } else {
+                w = *reinterpret_cast<const uint2*>(v + 8 * i);
+              }
               const uint32_t u[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {

@@ -77,11 +77,17 @@ struct AttnArgs {
   void* out;
   float* lse;
   void* workspace;
+  // the 8-bit cache: two bytes a block of 16 entries
+  const uint8_t* kv_scales;
+  int64_t scale_page_stride, scale_head_stride;
 };
 
 size_t attn_workspace(int64_t n, int seqs, int q_heads, int kv_heads, int dim, int causal, int window, int max_q,
                       int max_kv);
 hipError_t launch_paged_attn(const AttnArgs& a, hipStream_t s);
+size_t attn_q8_workspace(int64_t n, int seqs, int q_heads, int kv_heads, int dim, int causal, int window, int max_q,
+                         int max_kv);
+hipError_t launch_paged_attn_q8(const AttnArgs& a, hipStream_t s);
 
 // Pages handed out and taken back.
 struct PagesArgs {

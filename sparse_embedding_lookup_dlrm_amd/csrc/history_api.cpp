@@ -70,10 +70,11 @@ int check_norm(const float* w_q, const float* w_k, float eps) {
   return DLRM_OK;
 }
 
-int check_paged(int64_t n, int32_t seqs, int32_t kv_heads, int32_t dim, int dtype, const int32_t* q_offsets,
+// bytes: of a cache's element.
+int check_paged(int64_t n, int32_t seqs, int32_t kv_heads, int32_t dim, const int32_t* q_offsets,
                 const int32_t* kv_lens, const int32_t* page_table, int64_t table_stride, int32_t table_width,
                 int32_t page, int64_t num_pages, int64_t page_stride, int64_t head_stride, const void* k_cache,
-                const void* v_cache, int32_t* status, Paged* p) {
+                const void* v_cache, int32_t* status, Paged* p, int bytes = 2) {
   if (seqs < 0 || (n > 0 && (!q_offsets || (seqs > 0 && !kv_lens)))) return DLRM_E_INVAL;
   if (table_width < 0 || table_stride < 0 || num_pages < 0 || num_pages > kI32Max)
     return DLRM_E_INVAL;
@@ -82,7 +83,7 @@ int check_paged(int64_t n, int32_t seqs, int32_t kv_heads, int32_t dim, int dtyp
   if (page < 16 || page > 65536 || (page & (page - 1))) return DLRM_E_UNSUPPORTED;
   // entries and sequences
   if (static_cast<int64_t>(table_width) * page > kMostCounted || seqs > kMostCounted) return DLRM_E_UNSUPPORTED;
-  const int64_t per16 = 16 / bytes_of(dtype);
+  const int64_t per16 = 16 / bytes;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || page_stride % per16 || head_stride % per16) return DLRM_E_ALIGN;
   if (!aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(page_table, 4) || !aligned(status, 4))
     return DLRM_E_ALIGN;
@@ -118,6 +119,17 @@ int check_attn(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32
   if (seqs < 0 || window < 0 || (window > 0 && !causal) || max_q < 0 || max_kv < 0) return DLRM_E_INVAL;
   // rows and sequences
   if (q_heads / kv_heads > 1024 || n * q_heads > kMostCounted || seqs > kMostCounted) return DLRM_E_UNSUPPORTED;
+  return DLRM_OK;
+}
+
+// The scales of an 8-bit cache: two bytes a block, blocks of a head and page contiguous.
+int check_scales(int64_t n, int32_t kv_heads, int32_t page, int64_t num_pages, const uint8_t* scales,
+                 int64_t page_stride, int64_t head_stride) {
+  if (n > 0 && num_pages > 0 && !scales) return DLRM_E_INVAL;
+  if (!aligned(scales, 2) || page_stride % 2 || head_stride % 2) return DLRM_E_ALIGN;
+  const int64_t own = 2 * (page / DLRM_KV_BLOCK);
+  if (kv_heads > 1 && head_stride < own) return DLRM_E_INVAL;
+  if (num_pages > 1 && page_stride < (kv_heads - 1) * head_stride + own) return DLRM_E_INVAL;
   return DLRM_OK;
 }
 
@@ -231,7 +243,7 @@ int dlrm_kv_append(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, i
   TRY(check_tensor(k, k_stride, k_head_stride, dtype, n));
   TRY(check_tensor(v, v_stride, v_head_stride, dtype, n));
   if (!aligned(q_out, 16)) return DLRM_E_ALIGN;
-  TRY(check_paged(n, seqs, kv_heads, dim, dtype, q_offsets, kv_lens, page_table, table_stride, table_width, page,
+  TRY(check_paged(n, seqs, kv_heads, dim, q_offsets, kv_lens, page_table, table_stride, table_width, page,
                   num_pages, cache_page_stride, cache_head_stride, k_cache, v_cache, status, &a.paged));
   a.n = n; a.q_heads = q_heads; a.kv_heads = kv_heads; a.dim = dim; a.dtype = dtype;
   a.q = {q, q_stride, q_head_stride};
@@ -262,7 +274,7 @@ int dlrm_paged_attn(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, 
   if (bytes_of(dtype) != 2) return DLRM_E_UNSUPPORTED;
   if (!(scale > 0.f && scale < INFINITY) || (n > 0 && !out)) return DLRM_E_INVAL;
   TRY(check_tensor(q, q_stride, q_head_stride, dtype, n));
-  TRY(check_paged(n, seqs, kv_heads, dim, dtype, q_offsets, kv_lens, page_table, table_stride, table_width, page,
+  TRY(check_paged(n, seqs, kv_heads, dim, q_offsets, kv_lens, page_table, table_stride, table_width, page,
                   num_pages, cache_page_stride, cache_head_stride, k_cache, v_cache, status, &a.paged));
   if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return DLRM_E_ALIGN;
   const size_t need = attn_workspace(n, seqs, q_heads, kv_heads, dim, causal, window, max_q, max_kv);
@@ -274,6 +286,44 @@ int dlrm_paged_attn(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, 
   a.causal = causal != 0; a.window = window; a.max_q = max_q; a.max_kv = max_kv; a.scale = scale;
   a.out = out; a.lse = lse; a.workspace = workspace;
   return from_hip(launch_paged_attn(a, static_cast<hipStream_t>(stream)));
+}
+
+int dlrm_paged_attn_q8_workspace_bytes(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                                       int32_t causal, int32_t window, int32_t max_q, int32_t max_kv, size_t* bytes) {
+  if (!bytes) return DLRM_E_INVAL;
+  TRY(check_attn(n, seqs, q_heads, kv_heads, dim, causal, window, max_q, max_kv));
+  *bytes = attn_q8_workspace(n, seqs, q_heads, kv_heads, dim, causal, window, max_q, max_kv);
+  return DLRM_OK;
+}
+
+int dlrm_paged_attn_q8(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t dtype,
+                       const void* q, int64_t q_stride, int64_t q_head_stride, const void* k_cache,
+                       const void* v_cache, int32_t page, int64_t num_pages, int64_t cache_page_stride,
+                       int64_t cache_head_stride, const uint8_t* kv_scales, int64_t scale_page_stride,
+                       int64_t scale_head_stride, const int32_t* q_offsets, const int32_t* kv_lens,
+                       const int32_t* page_table, int64_t table_stride, int32_t table_width, int32_t causal,
+                       int32_t window, float scale, int32_t max_q, int32_t max_kv, void* out, float* lse,
+                       void* workspace, size_t ws_bytes, int32_t* status, void* stream) {
+  AttnArgs a;
+  memset(&a, 0, sizeof(a));
+  TRY(check_attn(n, seqs, q_heads, kv_heads, dim, causal, window, max_q, max_kv));
+  if (bytes_of(dtype) != 2) return DLRM_E_UNSUPPORTED;
+  if (!(scale > 0.f && scale < INFINITY) || (n > 0 && !out)) return DLRM_E_INVAL;
+  TRY(check_tensor(q, q_stride, q_head_stride, dtype, n));
+  TRY(check_paged(n, seqs, kv_heads, dim, q_offsets, kv_lens, page_table, table_stride, table_width, page, num_pages,
+                  cache_page_stride, cache_head_stride, k_cache, v_cache, status, &a.paged, 1));
+  TRY(check_scales(n, kv_heads, page, num_pages, kv_scales, scale_page_stride, scale_head_stride));
+  if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return DLRM_E_ALIGN;
+  const size_t need = attn_q8_workspace(n, seqs, q_heads, kv_heads, dim, causal, window, max_q, max_kv);
+  if (ws_bytes < need) return DLRM_E_WORKSPACE;
+  if (need > 0 && !workspace) return DLRM_E_INVAL;
+  a.n = n; a.q_heads = q_heads; a.kv_heads = kv_heads; a.dim = dim; a.dtype = dtype;
+  a.q = {q, q_stride, q_head_stride};
+  a.k_cache = k_cache; a.v_cache = v_cache;
+  a.kv_scales = kv_scales; a.scale_page_stride = scale_page_stride; a.scale_head_stride = scale_head_stride;
+  a.causal = causal != 0; a.window = window; a.max_q = max_q; a.max_kv = max_kv; a.scale = scale;
+  a.out = out; a.lse = lse; a.workspace = workspace;
+  return from_hip(launch_paged_attn_q8(a, static_cast<hipStream_t>(stream)));
 }
 
 int dlrm_pages_workspace_bytes(int32_t seqs, size_t* bytes) {

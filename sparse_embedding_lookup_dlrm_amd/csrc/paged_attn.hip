@@ -28,9 +28,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
   constexpr int F = D / 32;      // k steps of the first product
   constexpr int E = D / 16;      // elements of a value row that a lane takes, and 16-wide pieces of O
   constexpr int Rows = 16;
-  constexpr int Pitch = D + 4;   // floats; a row of O in LDS
   constexpr int Ahead = 64 / TT; // tiles whose pages a wave holds
-  __shared__ float lds_o[kWaves][Rows * Pitch];
+  __shared__ float lds_o[kWaves][Rows * kPitch<D>];
   __shared__ float2 lds_ml[kWaves][Rows];
   const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, c16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -243,51 +242,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
         work(k0, tile, tile, std::false_type{});
       }
 
-      // join the waves
-      l = add_halves(add_quarters(l));
-      if (g == 0) lds_ml[wave][c16] = make_float2(m, l);
-      __syncthreads();
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_ml[w][c16].x);
-      const float keep = m == -INFINITY ? 0.f : exp2f((m - top) * c);
-      // lane (g, c16) holds elements 4 E g .. 4 E (g + 1) of its row, E at a time
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int e = 0; e < E; ++e) lds_o[wave][c16 * Pitch + (4 * g + r) * E + e] = o[e][r] * keep;
-      __syncthreads();
-      constexpr int Pieces = D / 8;
-      for (int i = threadIdx.x; i < Rows * Pieces; i += kThreads) {
-        const int r16 = i / Pieces, at = i % Pieces * 8;
-        const int out_row = row0 + r16;
-        if (out_row >= row_end) continue;
-        float mt = -INFINITY, lt = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) mt = fmaxf(mt, lds_ml[w][r16].x);
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          const float2 ml = lds_ml[w][r16];
-          lt += ml.y * (ml.x == -INFINITY ? 0.f : exp2f((ml.x - mt) * c));
-        }
-        float x[8];
-#pragma unroll
-        for (int d = 0; d < 8; ++d) {
-          x[d] = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w) x[d] += lds_o[w][r16 * Pitch + at + d];
-        }
-        const int tok = out_row / group, gi = out_row - tok * group;
-        const long long to = static_cast<long long>(sq.first + tok) * a.q_heads + head * group + gi;
-        if (rc.parts == 1) {
-          finish<DT>(a, to, at, x, mt, lt);
-        } else {
-          float* p = cut.o + (split * a.n * a.q_heads + to) * D + at;
-          *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-          if (at == 0) cut.ml[to * cut.splits + split] = make_float2(mt, lt);
-        }
-      }
+      join_waves<DT, D>(a, cut, rc, sq, row0, row_end, group, head, split, m, l, o, lds_o, lds_ml);
       __syncthreads();
     }
   }
@@ -357,22 +312,8 @@ Cut cut_call(long long all_rows, long long max_rows, int seqs, int kv_heads, int
 template <int DT, int D>
 hipError_t run(const AttnArgs& a, hipStream_t s) {
   const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
-  Cut cut = cut_call(a.n * a.q_heads, rows, a.paged.seqs, a.kv_heads, D, a.causal, a.window, a.max_q, a.max_kv);
-  cut.o = static_cast<float*>(a.workspace);
-  cut.ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) +
-                                     round256(static_cast<size_t>(a.n) * a.q_heads * cut.splits * D * sizeof(float)));
-  const dim3 grid(a.kv_heads, cut.q_tiles * cut.splits, a.paged.seqs < 65535 ? a.paged.seqs : 65535);
-  const int tile = tile_rows(rows);
-  if (tile == 16)
-    hipLaunchKernelGGL((attn_rows_kernel<DT, D>), grid, dim3(kThreads), 0, s, a, cut);
-  else
-    hipLaunchKernelGGL((attn_tile_kernel<DT, D>), grid, dim3(kTileThreads<D>), 0, s, a, cut);
-  const long long all_rows = rows * a.kv_heads * a.paged.seqs;
-  if (cut.splits > 16 && all_rows <= 512)
-    join<DT, D, kThreads / (D / 8)>(a, cut, tile, s);
-  else if (cut.splits > 1)
-    join<DT, D, 1>(a, cut, tile, s);
-  return hipGetLastError();
+  const Cut cut = cut_call(a.n * a.q_heads, rows, a.paged.seqs, a.kv_heads, D, a.causal, a.window, a.max_q, a.max_kv);
+  return launch_cut<DT, D>(a, cut, attn_rows_kernel<DT, D>, attn_tile_kernel<DT, D, false>, kTileThreads<D>, s);
 }
 
 template <int DT>

@@ -1,0 +1,378 @@
+// Attention of new tokens over a paged cache of 8-bit codes (formulas in attn_device.h): e4m3 codes with a power of
+// two for each block of 16 entries of a head, one for the keys and one for the values.
+//
+// Codes are widened to the 16-bit type of the queries, which is exact, by an instruction that takes two of them and
+// their scale, so that the matrix products, the softmax and the joins are those of the 16-bit cache.
+#include "attn_tile.h"
+
+namespace dlrm {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Rows kernel: 16 rows of one head to a workgroup, as for the 16-bit cache: the four waves take the tiles of the history
+// in turn, a wave's next tile is on the way from global memory to registers while one is worked on, and the waves join
+// their (m, l, O) through LDS at the end. Scores are formed transposed, S^T = K Q^T, so that the weights are the second
+// product's right operand where they lie: lane (g, c16) holds entries 4 g .. 4 g + 3 of each block of 16.
+// The order of the elements in a score's sum is free: a lane takes 16 neighbouring codes of a key, which serve two
+// steps of the product, and the queries are read to fit. Of the values it takes D / 16 neighbouring codes of its
+// entries; a byte permutation of two entries' words gives the pairs of two elements, one widening each.
+// ---------------------------------------------------------------------------
+template <int DT, int D>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_q8_kernel(AttnArgs a, Cut cut) {
+  constexpr int TT = D >= 128 ? 2 : 4;  // blocks of 16 entries to a tile
+  constexpr int K = 16 * TT;
+  constexpr int F = D / 32;       // k steps of the first product
+  constexpr int Chunk = D == 32 ? 8 : 16, Chunks = D / (4 * Chunk);  // codes of a key that a lane takes at once
+  constexpr int E = D / 16;       // codes of a value that a lane takes, and 16-wide pieces of O
+  constexpr int VW = (E + 3) / 4;  // their words
+  constexpr int Rows = 16;
+  constexpr int Ahead = 64 / TT;  // tiles whose pages a wave holds
+  __shared__ float lds_o[kWaves][Rows * kPitch<D>];
+  __shared__ float2 lds_ml[kWaves][Rows];
+  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, c16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int group = a.q_heads / a.kv_heads;
+  const float c = a.scale * kLog2e;
+  const Paged& pg = a.paged;
+  const int page_mask = (1 << pg.page_shift) - 1;
+  const int head = blockIdx.x, split = blockIdx.y % cut.splits;
+  const uint8_t* kh = static_cast<const uint8_t*>(a.k_cache) + head * pg.head_stride + (c16 * D + g * Chunk);
+  const uint8_t* vh = static_cast<const uint8_t*>(a.v_cache) + head * pg.head_stride + (4 * g * D + c16 * E);
+  const uint8_t* sh = a.kv_scales + head * a.scale_head_stride;
+
+  for (int seq = blockIdx.z; seq < pg.seqs; seq += gridDim.z) {
+    const Seq sq = load_seq(pg, a.n, seq);
+    const int rows = sq.tokens * group;
+    const int32_t* table = pg.page_table + seq * pg.table_stride;
+
+    for (long long first_row = static_cast<long long>(blockIdx.y / cut.splits) * Rows; first_row < rows;
+         first_row += static_cast<long long>(cut.q_tiles) * Rows) {
+      const int row0 = static_cast<int>(first_row), row_end = rows - row0 > Rows ? row0 + Rows : rows;
+      const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut);
+      if (split >= rc.parts) continue;
+      const int k_first = rc.first + split * rc.part;
+      const int hi = rc.hi - k_first < rc.part ? rc.hi : k_first + rc.part;
+      const int k_begin = k_first + K * wave;
+
+      // Pages of the blocks of this wave's next Ahead tiles, one to a lane, and their scales; past the end: of the
+      // last entry.
+      const auto key_of = [&](int k0, int block) { return k0 + block / TT * (K * kWaves) + block % TT * 16; };
+      const auto look_up = [&](int k0) {
+        const int key = key_of(k0, lane);
+        return table[(key < hi ? key : hi - 1) >> pg.page_shift];
+      };
+      const auto good_pages = [&](int k0, int page) {  // bit i: the page of block i is good
+        const bool good = static_cast<uint32_t>(page) < static_cast<uint32_t>(pg.num_pages);
+        const int key = key_of(k0, lane);
+        if (!good && key < hi && key + 16 > rc.lo) flag(pg.status, DLRM_STATUS_BAD_PAGE);
+        return __ballot(good);
+      };
+      const auto look_up_scales = [&](int k0, int page, uint64_t good) {
+        const int key = key_of(k0, lane), from = good >> lane & 1 ? page : 0;
+        return static_cast<int>(*reinterpret_cast<const uint16_t*>(
+            sh + from * a.scale_page_stride + ((key < hi ? key : hi - 1) & page_mask) / kScaleBlock * 2));
+      };
+      int pages = 0;
+      if (k_begin < hi) pages = look_up(k_begin);
+
+      u32x4 qf[F];
+#pragma unroll
+      for (int f = 0; f < F; ++f) qf[f] = u32x4{0, 0, 0, 0};
+      const int row = row0 + c16;
+      int row_lo = 0, row_hi = 0, row_tok = -1;
+      if (row < row_end) {
+        row_tok = row / group;
+        const int gi = row - row_tok * group;
+        const Span s = seen_by(sq, row_tok, a.causal, a.window);
+        row_lo = s.lo;
+        row_hi = s.hi;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q.ptr) + (sq.first + row_tok) * a.q.stride +
+                            (head * group + gi) * a.q.head_stride + g * Chunk;
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+          qf[f] = *reinterpret_cast<const u32x4*>(q + f * 8 / Chunk * 4 * Chunk + f * 8 % Chunk);
+      }
+
+      float m = -INFINITY, l = 0.f;
+      f32x4 o[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = f32x4{0, 0, 0, 0};
+
+      // Where the blocks of a tile are, and whether their pages are good. Past the end and in place of a bad page
+      // another page of the cache is read and masked.
+      struct Tile {
+        long long at[TT];
+        int good;
+      };
+      uint64_t good64 = 0;
+      int scales = 0;
+      const auto find = [&](int k0, int index) {
+        Tile t;
+        t.good = static_cast<int>(good64 >> (index * TT)) & ((1 << TT) - 1);
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+          const int key = k0 + 16 * i < hi ? k0 + 16 * i : hi - 1;
+          const int page = t.good >> i & 1 ? __builtin_amdgcn_readlane(pages, index * TT + i) : 0;
+          t.at[i] = page * pg.page_stride + (key & page_mask & ~15) * D;
+        }
+        return t;
+      };
+      uint32_t kf[TT][Chunks][Chunk / 4];
+      uint32_t v[4 * TT][VW];
+      const auto load_keys = [&](const Tile& t) {
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+          for (int f = 0; f < Chunks; ++f)
+            __builtin_memcpy(kf[i][f], __builtin_assume_aligned(kh + t.at[i] + f * 4 * Chunk, Chunk), Chunk);
+      };
+      const auto load_values = [&](const Tile& t) {
+#pragma unroll
+        for (int j = 0; j < 4 * TT; ++j) {
+          const uint8_t* from = vh + t.at[j / 4] + j % 4 * D;
+          if constexpr (E == 2)
+            v[j][0] = *reinterpret_cast<const uint16_t*>(from);
+          else
+            __builtin_memcpy(v[j], __builtin_assume_aligned(from, E), E);
+        }
+      };
+
+      // One tile at k0 with the scales `two`; with More, the loads of the next one at its places.
+      const auto work = [&](int k0, const Tile& tile, const int (&two)[TT], const Tile& next, auto more) {
+        constexpr bool More = decltype(more)::value;
+        f32x4 s[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          s[t] = f32x4{0, 0, 0, 0};
+          const float scale = key_scale(two[t]);
+#pragma unroll
+          for (int f = 0; f < F; ++f) {
+            const uint32_t* w = &kf[t][f * 8 / Chunk][f * 8 % Chunk / 4];
+            s[t] = mfma16<DT>(u32x4{widen_codes<DT, false>(w[0], scale), widen_codes<DT, true>(w[0], scale),
+                                    widen_codes<DT, false>(w[1], scale), widen_codes<DT, true>(w[1], scale)},
+                              qf[f], s[t]);
+          }
+        }
+        if constexpr (More) load_keys(next);
+        const bool edge = k0 < rc.all_lo || k0 + K > rc.all_hi || k0 + K > hi || tile.good != (1 << TT) - 1;
+        if (edge) {
+#pragma unroll
+          for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int key = k0 + 16 * t + 4 * g + r;
+              if (!(tile.good >> t & 1) || key < row_lo || key >= row_hi || key >= hi) s[t][r] = -INFINITY;
+            }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) top = fmaxf(top, s[t][r]);
+        const float now = fmaxf(m, max_halves(max_quarters(top)));
+        // O and l stay relative to an older maximum until a row's grows by 2^8 (fp16, with its lift: 2^7)
+        if (__any((now - m) * c > (DT == DLRM_F16 ? 7.f : 8.f))) {
+          const float keep = m == -INFINITY ? 0.f : exp2f((m - now) * c);
+          m = now;
+          l *= keep;
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] *= keep;
+        }
+        const float base = m == -INFINITY ? 0.f : m * c - kLift<DT>;
+        uint32_t pw[TT][2];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          float p[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) p[r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -base));
+          l += (p[0] + p[1]) + (p[2] + p[3]);
+          pw[t][0] = pack2<DT>(p[0], p[1]);
+          pw[t][1] = pack2<DT>(p[2], p[3]);
+        }
+
+        // Entries that no row sees are zero, whatever they and their scale hold. If one that only some rows see
+        // holds a NaN (or a value that fp16 does not), the second product runs token by token, with what the token
+        // does not see set to zero, and only the token's own rows take the sum.
+        float vs[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) vs[t] = value_scale(two[t]);
+        bool apart = false;
+        if (edge) {
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            const int first = k0 + 16 * t;
+            if (first + 16 <= rc.lo || first >= hi || !(tile.good >> t & 1)) vs[t] = 1.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int j = 4 * t + r, key = first + 4 * g + r;
+              const bool none = key < rc.lo || key >= hi || !(tile.good >> t & 1);
+#pragma unroll
+              for (int i = 0; i < VW; ++i) {
+                if (none) v[j][i] = 0;
+                apart |= (not_finite_halves<DT>(widen_codes<DT, false>(v[j][i], vs[t])) |
+                          not_finite_halves<DT>(widen_codes<DT, true>(v[j][i], vs[t]))) != 0;
+              }
+            }
+          }
+          apart = rc.tok1 > rc.tok0 && __any(apart);
+        }
+        const auto product = [&](auto seen, bool mine) {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const uint32_t pick = e % 4 ? 0x07030602u : 0x05010400u;
+            f32x4 sum0 = o[e], sum1 = o[e + 1];
+#pragma unroll
+            for (int t = 0; t < TT; t += 2) {
+              u32x4 v0, v1;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int j = 4 * t + 2 * i;
+                const uint32_t codes = __builtin_amdgcn_perm(v[j + 1][e / 4] & seen(j + 1), v[j][e / 4] & seen(j), pick);
+                v0[i] = widen_codes<DT, false>(codes, vs[j / 4]);
+                v1[i] = widen_codes<DT, true>(codes, vs[j / 4]);
+              }
+              const u32x4 p = {pw[t][0], pw[t][1], pw[t + 1][0], pw[t + 1][1]};
+              sum0 = mfma16<DT>(v0, p, sum0);
+              sum1 = mfma16<DT>(v1, p, sum1);
+            }
+            if (mine) {
+              o[e] = sum0;
+              o[e + 1] = sum1;
+            }
+          }
+        };
+        if (!apart) {
+          product([](int) { return 0xffffffffu; }, true);
+        } else {
+#pragma unroll 1
+          for (int tok = rc.tok0; tok <= rc.tok1; ++tok) {
+            const Span sp = seen_by(sq, tok, a.causal, a.window);
+            // a scale that is not finite would make zeros of the entries that the token does not see NaN
+            float own[TT];
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+              own[t] = vs[t];
+              if (k0 + 16 * t + 16 <= sp.lo || k0 + 16 * t >= sp.hi) vs[t] = 1.f;
+            }
+            product([&](int j) {
+              const int key = k0 + 16 * (j / 4) + 4 * g + j % 4;
+              return key >= sp.lo && key < sp.hi ? 0xffffffffu : 0u;
+            }, row_tok == tok);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) vs[t] = own[t];
+          }
+        }
+        if constexpr (More) load_values(next);
+      };
+
+      if (k_begin < hi) {
+        good64 = good_pages(k_begin, pages);
+        int index = 0;
+        Tile tile = find(k_begin, 0);
+        scales = look_up_scales(k_begin, pages, good64);
+        load_keys(tile);
+        load_values(tile);
+        int two[TT];
+        const auto pick_scales = [&] {
+#pragma unroll
+          for (int i = 0; i < TT; ++i) two[i] = __builtin_amdgcn_readlane(scales, index * TT + i);
+        };
+        int k0 = k_begin;
+        for (; k0 + K * kWaves < hi; k0 += K * kWaves) {
+          const int k_next = k0 + K * kWaves;
+          pick_scales();
+          if (++index == Ahead) {
+            index = 0;
+            pages = look_up(k_next);
+            good64 = good_pages(k_next, pages);
+            scales = look_up_scales(k_next, pages, good64);
+          }
+          const Tile next = find(k_next, index);
+          work(k0, tile, two, next, std::true_type{});
+          tile = next;
+        }
+        pick_scales();
+        work(k0, tile, two, tile, std::false_type{});
+      }
+
+      join_waves<DT, D>(a, cut, rc, sq, row0, row_end, group, head, split, m, l, o, lds_o, lds_ml);
+      __syncthreads();
+    }
+  }
+}
+
+// Where the workgroups of a call would not fill the chip, or histories may be of unequal length, every history is split
+// into parts.
+Cut cut_call(long long all_rows, long long max_rows, int seqs, int kv_heads, int dim, int causal, int window, int max_q,
+             int max_kv) {
+  Cut c;
+  const int rows = tile_rows(max_rows);
+  long long tiles = max_rows > rows ? (max_rows + rows - 1) / rows : 1;
+  if (tiles > 65535) tiles = 65535;  // a workgroup takes further tiles in turn
+  c.q_tiles = static_cast<int>(tiles);
+  const long long whole = tiles * seqs * kv_heads;
+  long long span = max_kv > 0 ? max_kv : 1;
+  if (span > 0x7fffffffLL - (1 << 17)) span = 0x7fffffffLL - (1 << 17);  // no history is longer
+  const long long seen = static_cast<long long>(window) + max_q + 32;
+  if (causal && window && span > seen) span = seen;
+  long long splits;
+  const long long units = whole > 0 ? whole : 1;
+  const long long held = (all_rows + rows - 1) / rows, busy = held > units ? held : units;  // tiles of all rows
+  if (rows == 16) {
+    const long long least = 131072 / dim, fill = 256 / units, finest = (span + 511) / 512, most = 16384 / units;
+    splits = (span + least - 1) / least;
+    if (splits < fill) splits = fill < finest ? fill : finest;
+    if (splits > most) splits = most;
+    if (splits > 4 * 16384 / busy) splits = 4 * 16384 / busy;
+  } else {
+    const long long places = dim == 256 ? 256 : dim == 128 ? 512 : 768, finest = (span + 511) / 512;
+    splits = 2 * places / units;
+    if (splits > finest) splits = finest;
+    const long long coarse = 4 * places / units < span / 1024 ? 4 * places / units : span / 1024;
+    if (dim < 256 && splits < coarse) splits = coarse < 20 ? coarse : splits < 20 ? 20 : splits;
+    if (splits > 4 * 4 * places / busy) splits = 4 * 4 * places / busy;
+  }
+  if (splits < 1) splits = 1;
+  if (splits > 1) splits |= 1;
+  if (tiles > 1) c.q_tiles = static_cast<int>(tiles |= 1);
+  if (splits > kMaxSplits) splits = kMaxSplits - 1;
+  if (splits > 65535 / tiles) splits = 65535 / tiles;
+  c.splits = static_cast<int>(splits);
+  c.part = static_cast<int>(((span + splits - 1) / splits + 63) & ~63LL);
+  c.o = nullptr;
+  c.ml = nullptr;
+  return c;
+}
+
+template <int DT, int D>
+hipError_t run(const AttnArgs& a, hipStream_t s) {
+  const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
+  const Cut cut = cut_call(a.n * a.q_heads, rows, a.paged.seqs, a.kv_heads, D, a.causal, a.window, a.max_q, a.max_kv);
+  return launch_cut<DT, D>(a, cut, attn_rows_q8_kernel<DT, D>, attn_tile_kernel<DT, D, true>, kTileThreads<D>, s);
+}
+
+template <int DT>
+hipError_t run_dim(const AttnArgs& a, hipStream_t s) {
+  switch (a.dim) {
+    case 32: return run<DT, 32>(a, s);
+    case 64: return run<DT, 64>(a, s);
+    case 128: return run<DT, 128>(a, s);
+    default: return run<DT, 256>(a, s);
+  }
+}
+
+}  // namespace
+
+size_t attn_q8_workspace(int64_t n, int seqs, int q_heads, int kv_heads, int dim, int causal, int window, int max_q,
+                         int max_kv) {
+  if (n == 0 || seqs == 0) return 0;
+  const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
+  return cut_bytes(cut_call(n * q_heads, rows, seqs, kv_heads, dim, causal, window, max_q, max_kv), n, q_heads, dim);
+}
+
+hipError_t launch_paged_attn_q8(const AttnArgs& a, hipStream_t s) {
+  if (a.n == 0 || a.paged.seqs == 0) return hipSuccess;
+  return a.dtype == DLRM_F16 ? run_dim<DLRM_F16>(a, s) : run_dim<DLRM_BF16>(a, s);
+}
+
+}  // namespace dlrm

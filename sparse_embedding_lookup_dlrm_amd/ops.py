@@ -30,6 +30,7 @@ STATUS_NO_ROOM = 8
 STATUS_BAD_USER = 16
 MAX_TABLES = 128
 MAX_AXES = 8
+KV_BLOCK = 16  # entries of a head that share a scale in an 8-bit cache
 
 _TORCH_DT = {torch.float32: DLRM_F32, torch.float16: DLRM_F16, torch.bfloat16: DLRM_BF16}
 
@@ -94,6 +95,12 @@ _SIGNATURES = {
     "dlrm_paged_attn": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, *_HEADS, _c_void_p, _c_void_p, _i32, _i64,
                                        _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _i64, _i32, _i32, _i32, _f32, _i32,
                                        _i32, _c_void_p, _c_void_p, _c_void_p, _size_t, _c_void_p, _c_void_p]),
+    "dlrm_paged_attn_q8_workspace_bytes": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                                          _P(_size_t)]),
+    "dlrm_paged_attn_q8": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, *_HEADS, _c_void_p, _c_void_p, _i32,
+                                          _i64, _i64, _i64, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
+                                          _i64, _i32, _i32, _i32, _f32, _i32, _i32, _c_void_p, _c_void_p, _c_void_p,
+                                          _size_t, _c_void_p, _c_void_p]),
     "dlrm_pages_workspace_bytes": (ctypes.c_int, [_i32, _P(_size_t)]),
     "dlrm_pages_assign": (ctypes.c_int, [_i64, _i32, _i32, *[_c_void_p] * 5, _i64, _i32, _i32, _c_void_p, _i64,
                                          *[_c_void_p] * 5, _i32, *[_c_void_p] * 3, _size_t, _c_void_p, _c_void_p]),
@@ -863,23 +870,16 @@ def paged_attn_workspace_bytes(N: int, S: int, Hq: int, Hk: int, D: int, causal:
     return out.value
 
 
-def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, q_offsets: torch.Tensor,
-               kv_lens: torch.Tensor, page_table: torch.Tensor, *, causal: bool = True, window: int = 0,
-               scale: Optional[float] = None, max_q: Optional[int] = None, max_kv: Optional[int] = None,
-               want_lse: bool = False, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-               workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
-    """Attention of the new tokens q [N, Hq, D] over the paged caches [pages, Hk, page, D]
-    (dlrm_paged_attn); the sequences as in kv_append. window > 0 (with causal): a token sees the last
-    `window` entries up to its own. max_q, max_kv: the most new tokens and the longest history of a
-    sequence, for how the work is cut; without them N and the page table's width are taken, which is
-    right for one sequence and slow for many of one token each. Returns
-    out [N, Hq, D], or (out, lse [N, Hq] fp32) with want_lse."""
+def _attn(q8: bool, q, k_cache, v_cache, kv_scales, q_offsets, kv_lens, page_table, causal, window, scale, max_q, max_kv,
+          want_lse, out, lse, workspace, status, stream):
+    """dlrm_paged_attn, or with q8 dlrm_paged_attn_q8."""
     shape, qa = _heads_of(q, "q")
     N, Hq, D = shape
     dt, dev, where = q.dtype, q.get_device(), q.device
     Hk = k_cache.shape[1] if k_cache.dim() == 4 else 0
     (S, page, pages, by_page, by_head, by_seq, width), (offsets_at, lens_at, table_at, status_at) = _paged_args(
-        dt, dev, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk, D)
+        torch.float8_e4m3fn if q8 else dt, dev, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk, D)
+    scales = _scale_args(kv_scales, dev, pages, Hk, page) if q8 else ()
     if max_q is None:
         max_q = N
     if max_kv is None:
@@ -888,7 +888,7 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, q_
         scale = D ** -0.5 if D > 0 else 1.0
     if window > _I32_MAX or max_q > _I32_MAX or max_kv > _I32_MAX or window < 0 or max_q < 0 or max_kv < 0:
         raise ValueError(f"window {window}, max_q {max_q} and max_kv {max_kv} must lie between 0 and {_I32_MAX}")
-    need = paged_attn_workspace_bytes(N, S, Hq, Hk, D, causal, window, max_q, max_kv)
+    need = (paged_attn_q8_workspace_bytes if q8 else paged_attn_workspace_bytes)(N, S, Hq, Hk, D, causal, window, max_q, max_kv)
     if out is not None:
         _plain(out, "out", dt, N * Hq * D, dev)
     if lse is not None:
@@ -902,12 +902,64 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, q_
             lse = q.new_empty((N, Hq), dtype=torch.float32)
         if workspace is None and need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=where)
-        _check(lib().dlrm_paged_attn(N, S, Hq, Hk, D, _TORCH_DT[dt], *qa, k_cache.data_ptr(), v_cache.data_ptr(), page,
-                                     pages, by_page, by_head, offsets_at, lens_at, table_at, by_seq, width,
-                                     1 if causal else 0, window, scale, max_q, max_kv, out.data_ptr(), _ptr(lse),
-                                     _ptr(workspace), 0 if workspace is None else workspace.numel(), status_at, s),
-               "dlrm_paged_attn")
+        fn, name = (lib().dlrm_paged_attn_q8, "dlrm_paged_attn_q8") if q8 else (lib().dlrm_paged_attn, "dlrm_paged_attn")
+        _check(fn(N, S, Hq, Hk, D, _TORCH_DT[dt], *qa, k_cache.data_ptr(), v_cache.data_ptr(), page, pages, by_page, by_head,
+                  *scales, offsets_at, lens_at, table_at, by_seq, width, 1 if causal else 0, window, scale, max_q, max_kv,
+                  out.data_ptr(), _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel(), status_at, s),
+               name)
     return (out, lse) if want_lse else out
+
+
+def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, q_offsets: torch.Tensor,
+               kv_lens: torch.Tensor, page_table: torch.Tensor, *, causal: bool = True, window: int = 0,
+               scale: Optional[float] = None, max_q: Optional[int] = None, max_kv: Optional[int] = None,
+               want_lse: bool = False, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Attention of the new tokens q [N, Hq, D] over the paged caches [pages, Hk, page, D]
+    (dlrm_paged_attn); the sequences as in kv_append. window > 0 (with causal): a token sees the last
+    `window` entries up to its own. max_q, max_kv: the most new tokens and the longest history of a
+    sequence, for how the work is cut; without them N and the page table's width are taken, which is
+    right for one sequence and slow for many of one token each. Returns
+    out [N, Hq, D], or (out, lse [N, Hq] fp32) with want_lse."""
+    return _attn(False, q, k_cache, v_cache, None, q_offsets, kv_lens, page_table, causal, window, scale, max_q, max_kv, want_lse,
+                 out, lse, workspace, status, stream)
+
+
+def _scale_args(kv_scales, dev: int, pages: int, Hk: int, page: int):
+    """Checks the scales of an 8-bit cache; returns their address and page and head stride."""
+    shape, strides = kv_scales.shape, kv_scales.stride()
+    per = page // KV_BLOCK
+    if tuple(shape) != (pages, Hk, per, 2):
+        raise ValueError(f"kv_scales must be [{pages}, {Hk}, {per}, 2], got {tuple(shape)}")
+    if kv_scales.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+        raise ValueError(f"kv_scales must be {torch.float8_e8m0fnu} or its bytes, got {kv_scales.dtype}")
+    if kv_scales.get_device() != dev:
+        raise ValueError(f"kv_scales is on {kv_scales.device}, not on device {dev}")
+    if strides[3] != 1 or (per > 1 and strides[2] != 2):
+        raise ValueError("the scales of a head and page must be contiguous")
+    return kv_scales.data_ptr(), strides[0] if pages > 1 else 0, strides[1] if Hk > 1 else 0
+
+
+@functools.lru_cache(maxsize=1024)
+def paged_attn_q8_workspace_bytes(N: int, S: int, Hq: int, Hk: int, D: int, causal: bool, window: int, max_q: int,
+                                  max_kv: int) -> int:
+    out = _size_t(0)
+    _check(lib().dlrm_paged_attn_q8_workspace_bytes(N, S, Hq, Hk, D, 1 if causal else 0, window, max_q, max_kv,
+                                                    ctypes.byref(out)), "dlrm_paged_attn_q8_workspace_bytes")
+    return out.value
+
+
+def paged_attn_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales: torch.Tensor,
+                  q_offsets: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor, *, causal: bool = True,
+                  window: int = 0, scale: Optional[float] = None, max_q: Optional[int] = None,
+                  max_kv: Optional[int] = None, want_lse: bool = False, out: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None):
+    """paged_attn over caches of torch.float8_e4m3fn with kv_scales [pages, Hk, page / KV_BLOCK, 2] of
+    torch.float8_e8m0fnu (or uint8), one of the keys and one of the values for each KV_BLOCK entries of a head
+    (dlrm_paged_attn_q8)."""
+    return _attn(True, q, k_cache, v_cache, kv_scales, q_offsets, kv_lens, page_table, causal, window, scale, max_q, max_kv,
+                 want_lse, out, lse, workspace, status, stream)
 
 
 @functools.lru_cache(maxsize=1024)

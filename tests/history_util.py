@@ -122,3 +122,32 @@ class History:
     def args(self):
         return (self.q.cuda(), self.k_cache.cuda(), self.v_cache.cuda(), self.q_offsets.cuda(),
                 torch.tensor(self.kv_lens, dtype=torch.int32).cuda(), self.page_table.cuda())
+
+
+class History8(History):
+    """Sequences over an 8-bit cache: codes and scale bytes, and in k_cache and v_cache the values they stand for. Slots
+    past each history hold the code NaN, blocks without entries the byte 255 as well."""
+
+    def __init__(self, *args, bytes_from=(118, 123), **kw):
+        super().__init__(*args, **kw)
+        g = torch.Generator().manual_seed(args[7] if len(args) > 7 else kw["seed"])
+        pages, Hk, page, D = self.k_cache.shape
+        self.scales = torch.randint(*bytes_from, (pages, Hk, page // 16, 2), generator=g, dtype=torch.int32).to(torch.uint8)
+        self.codes = []
+        for j, x in enumerate((self.k_cache, self.v_cache)):
+            x = x.float().unflatten(2, (-1, 16))
+            power = torch.exp2(self.scales[..., j].float() - 127)[..., None, None]
+            code = (x / power).clamp(-448, 448).to(torch.float8_e4m3fn)
+            self.codes.append(code.flatten(2, 3))
+            empty = x.isnan().all(-1).all(-1)
+            self.scales[..., j][empty] = 255
+        self.values()
+
+    def values(self):
+        """k_cache and v_cache from the codes and scales."""
+        power = self.scales.view(torch.float8_e8m0fnu).double().repeat_interleave(16, 2)
+        self.k_cache, self.v_cache = (c.double() * power[..., j, None] for j, c in enumerate(self.codes))
+
+    def args(self):
+        return (self.q.cuda(), *(c.cuda() for c in self.codes), self.scales.view(torch.float8_e8m0fnu).cuda(),
+                self.q_offsets.cuda(), torch.tensor(self.kv_lens, dtype=torch.int32).cuda(), self.page_table.cuda())
