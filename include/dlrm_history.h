@@ -182,6 +182,26 @@ int dlrm_paged_attn(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, 
  */
 #define DLRM_KV_BLOCK 16
 
+/*
+ * dlrm_kv_append with the cache in 8 bits: keys (normed and rotated) and values are scaled and rounded from fp32,
+ * once. A block's byte b is the smallest >= 1 under which the largest finite |x| of its new entries is a code:
+ * |x| <= 448 * 2^(b - 127). Where the block also holds entries from before this call, it is at least what it was, and
+ * if it grows their codes are rounded again to the new scale. Rounding is to nearest even; an element that is not
+ * finite becomes NaN and counts for no scale. A block under byte 255 stays NaN.
+ * The pages of different sequences must be different in blocks where new tokens fall. A token that several
+ * sequences share because offsets are bad is stored for each of them.
+ */
+int dlrm_kv_append_q8(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t rot,
+                      int32_t dtype, const void* q, int64_t q_stride, int64_t q_head_stride, const void* k,
+                      int64_t k_stride, int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride,
+                      const int32_t* positions, int64_t pos_stride, int32_t axes, const int32_t* sections,
+                      const float* inv_freq, const float* w_q, const float* w_k, float eps, int32_t interleaved,
+                      const int32_t* q_offsets, const int32_t* kv_lens, const int32_t* page_table,
+                      int64_t table_stride, int32_t table_width, int32_t page, int64_t num_pages,
+                      int64_t cache_page_stride, int64_t cache_head_stride, void* k_cache, void* v_cache,
+                      uint8_t* kv_scales, int64_t scale_page_stride, int64_t scale_head_stride, void* q_out,
+                      int32_t* status, void* stream);
+
 /* Workspace of dlrm_paged_attn_q8 for these sizes (0 where no history is split). */
 int dlrm_paged_attn_q8_workspace_bytes(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t dim,
                                        int32_t causal, int32_t window, int32_t max_q, int32_t max_kv, size_t* bytes);

@@ -187,3 +187,69 @@ def pages_release(users, keep, held, tables, free, count, page):
         count += b - a
         held[u] = k
     return 0, held, free, count
+
+
+def e4m3_values():
+    """What the 256 codes stand for: sign, 4 bits of exponent with bias 7, 3 of significand; 0x7f and 0xff are NaN."""
+    out = np.empty(256)
+    for c in range(256):
+        e, f = c >> 3 & 15, c & 7
+        x = f / 8 * 2.0 ** -6 if e == 0 else (1 + f / 8) * 2.0 ** (e - 7)
+        out[c] = np.nan if c & 127 == 127 else -x if c & 128 else x
+    return out
+
+
+def e4m3_round(x):
+    """Codes of finite x, |x| <= 448, to nearest even; NaN of what is not finite."""
+    x = np.asarray(x, dtype=np.float64)
+    table = e4m3_values()[:127]
+    a = np.abs(np.where(np.isfinite(x), x, 0.0))
+    hi = np.minimum(np.searchsorted(table, a), 126)
+    lo = np.maximum(hi - 1, 0)
+    low, high = a - table[lo], table[hi] - a
+    code = np.where((low < high) | ((low == high) & (lo % 2 == 0)), lo, hi)
+    code = np.where(a == table[hi], hi, code)
+    return np.where(np.isfinite(x), code + 128 * np.signbit(x), 127).astype(np.uint8)
+
+
+def scale_byte(top):
+    """The smallest b >= 1 with top <= 448 * 2^(b - 127)."""
+    b = 1
+    while b < 254 and top > 448 * 2.0 ** (b - 127):
+        b += 1
+    return b
+
+
+def append_q8(x, codes, scales, q_offsets, kv_lens, page_table):
+    """Stores x [N, Hk, D] (normed and rotated) in codes [pages, Hk, page, D] and scales [pages, Hk, page / 16], uint8,
+    in place, for good offsets, lengths and pages; a page outside the cache is passed over. Returns the exact values in
+    code units (NaN where nothing was stored) and, in their shape, the largest |x| of each block and head."""
+    pages, Hk, page, D = codes.shape
+    exact, tops = np.full(codes.shape, np.nan), np.zeros(scales.shape)
+    values = e4m3_values()
+    for s, held in enumerate(kv_lens):
+        m = q_offsets[s + 1] - q_offsets[s]
+        start = max(held - m, 0)
+        for first in range(start // 16 * 16, held if m else 0, 16):
+            pg = int(page_table[s][first // page])
+            if not 0 <= pg < pages:
+                continue
+            lo, hi, at = max(first, start), min(first + 16, held), first % page
+            token = q_offsets[s + 1] - held + lo
+            for h in range(Hk):
+                new = x[token:token + hi - lo, h].astype(np.float64)
+                fine = np.isfinite(new)
+                top = np.abs(new[fine]).max(initial=0.0)
+                b, had = scale_byte(top), int(scales[pg, h, at // 16])
+                if lo > first:
+                    b = max(b, had)
+                    if b > had:
+                        old = values[codes[pg, h, at:at + lo - first]]
+                        sign = codes[pg, h, at:at + lo - first] & 128
+                        codes[pg, h, at:at + lo - first] = e4m3_round(old * 2.0 ** (had - b)) | sign
+                tops[pg, h, at // 16] = top
+                scales[pg, h, at // 16] = b
+                units = new / 2.0 ** (b - 127)
+                exact[pg, h, at + lo - first:at + hi - first] = units
+                codes[pg, h, at + lo - first:at + hi - first] = e4m3_round(units)
+    return exact, tops

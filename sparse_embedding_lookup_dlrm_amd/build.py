@@ -23,7 +23,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdlrm_embbag.so")
 
 SOURCES = ["embbag_fwd.hip", "embbag_bwd.hip", "offsets.hip", "noalloc.hip", "probe.hip", "api.cpp",
-           "norm_rope.hip", "paged_attn.hip", "paged_attn_q8.hip", "pages.hip",
+           "norm_rope.hip", "paged_attn.hip", "kv_append_q8.hip", "paged_attn_q8.hip", "pages.hip",
            "history_api.cpp"]
 ARCH = "gfx950"
 

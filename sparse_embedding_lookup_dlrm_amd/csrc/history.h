@@ -47,6 +47,9 @@ struct NormRopeArgs {
   // append: k and v go to the cache instead of k_out
   Paged paged;
   void *k_cache, *v_cache;
+  // the 8-bit cache: two bytes a block of 16 entries
+  uint8_t* kv_scales;
+  int64_t scale_page_stride, scale_head_stride;
 };
 
 struct NormRopeBwdArgs {
@@ -63,6 +66,7 @@ struct NormRopeBwdArgs {
 
 hipError_t launch_norm_rope(const NormRopeArgs& a, hipStream_t s);
 hipError_t launch_kv_append(const NormRopeArgs& a, hipStream_t s);
+hipError_t launch_kv_append_q8(const NormRopeArgs& a, hipStream_t s);
 size_t norm_rope_bwd_workspace(int64_t n, int dim, bool norm);
 hipError_t launch_norm_rope_bwd(const NormRopeBwdArgs& a, hipStream_t s);
 

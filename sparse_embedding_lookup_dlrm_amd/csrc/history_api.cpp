@@ -133,6 +133,33 @@ int check_scales(int64_t n, int32_t kv_heads, int32_t page, int64_t num_pages, c
   return DLRM_OK;
 }
 
+// Arguments of the append that both caches share; bytes: of a cache's element.
+int check_append(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t rot, int32_t dtype,
+                 const Heads& q, const Heads& k, const Heads& v, const int32_t* positions, int64_t pos_stride,
+                 int32_t axes, const int32_t* sections, const float* inv_freq, const float* w_q, const float* w_k,
+                 float eps, int32_t interleaved, const int32_t* q_offsets, const int32_t* kv_lens,
+                 const int32_t* page_table, int64_t table_stride, int32_t table_width, int32_t page, int64_t num_pages,
+                 int64_t cache_page_stride, int64_t cache_head_stride, void* k_cache, void* v_cache, int bytes,
+                 void* q_out, int32_t* status, NormRopeArgs* a) {
+  memset(a, 0, sizeof(*a));
+  TRY(check_heads(n, q_heads, kv_heads, dim, dtype, true));
+  if (q_heads > 0 && (!w_q != !w_k || (n > 0 && !q_out))) return DLRM_E_INVAL;
+  if (q_heads == 0 && (q.ptr || q_out || w_q)) return DLRM_E_INVAL;
+  TRY(check_rotation(n, dim, rot, positions, pos_stride, axes, sections, inv_freq, interleaved, &a->rope));
+  TRY(check_norm(w_q, w_k, eps));
+  if (q_heads > 0) TRY(check_tensor(q.ptr, q.stride, q.head_stride, dtype, n));
+  TRY(check_tensor(k.ptr, k.stride, k.head_stride, dtype, n));
+  TRY(check_tensor(v.ptr, v.stride, v.head_stride, dtype, n));
+  if (!aligned(q_out, 16)) return DLRM_E_ALIGN;
+  TRY(check_paged(n, seqs, kv_heads, dim, q_offsets, kv_lens, page_table, table_stride, table_width, page, num_pages,
+                  cache_page_stride, cache_head_stride, k_cache, v_cache, status, &a->paged, bytes));
+  a->n = n; a->q_heads = q_heads; a->kv_heads = kv_heads; a->dim = dim; a->dtype = dtype;
+  a->q = q; a->k = k; a->v = v;
+  a->w_q = w_q; a->w_k = w_k; a->eps = eps; a->q_out = q_out;
+  a->k_cache = k_cache; a->v_cache = v_cache;
+  return DLRM_OK;
+}
+
 // What assignment and release of pages share.
 int check_pages(int32_t seqs, int32_t users, const int32_t* who, const int32_t* held, const int32_t* held_out,
                 const int32_t* tables, int64_t table_stride, int32_t table_width, int32_t page,
@@ -233,25 +260,31 @@ int dlrm_kv_append(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, i
                    int64_t cache_head_stride, void* k_cache, void* v_cache, void* q_out, int32_t* status,
                    void* stream) {
   NormRopeArgs a;
-  memset(&a, 0, sizeof(a));
-  TRY(check_heads(n, q_heads, kv_heads, dim, dtype, true));
-  if (q_heads > 0 && (!w_q != !w_k || (n > 0 && !q_out))) return DLRM_E_INVAL;
-  if (q_heads == 0 && (q || q_out || w_q)) return DLRM_E_INVAL;
-  TRY(check_rotation(n, dim, rot, positions, pos_stride, axes, sections, inv_freq, interleaved, &a.rope));
-  TRY(check_norm(w_q, w_k, eps));
-  if (q_heads > 0) TRY(check_tensor(q, q_stride, q_head_stride, dtype, n));
-  TRY(check_tensor(k, k_stride, k_head_stride, dtype, n));
-  TRY(check_tensor(v, v_stride, v_head_stride, dtype, n));
-  if (!aligned(q_out, 16)) return DLRM_E_ALIGN;
-  TRY(check_paged(n, seqs, kv_heads, dim, q_offsets, kv_lens, page_table, table_stride, table_width, page,
-                  num_pages, cache_page_stride, cache_head_stride, k_cache, v_cache, status, &a.paged));
-  a.n = n; a.q_heads = q_heads; a.kv_heads = kv_heads; a.dim = dim; a.dtype = dtype;
-  a.q = {q, q_stride, q_head_stride};
-  a.k = {k, k_stride, k_head_stride};
-  a.v = {v, v_stride, v_head_stride};
-  a.w_q = w_q; a.w_k = w_k; a.eps = eps; a.q_out = q_out;
-  a.k_cache = k_cache; a.v_cache = v_cache;
+  TRY(check_append(n, seqs, q_heads, kv_heads, dim, rot, dtype, {q, q_stride, q_head_stride}, {k, k_stride, k_head_stride},
+                   {v, v_stride, v_head_stride}, positions, pos_stride, axes, sections, inv_freq, w_q, w_k, eps,
+                   interleaved, q_offsets, kv_lens, page_table, table_stride, table_width, page, num_pages,
+                   cache_page_stride, cache_head_stride, k_cache, v_cache, 2, q_out, status, &a));
   return from_hip(launch_kv_append(a, static_cast<hipStream_t>(stream)));
+}
+
+int dlrm_kv_append_q8(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t rot,
+                      int32_t dtype, const void* q, int64_t q_stride, int64_t q_head_stride, const void* k,
+                      int64_t k_stride, int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride,
+                      const int32_t* positions, int64_t pos_stride, int32_t axes, const int32_t* sections,
+                      const float* inv_freq, const float* w_q, const float* w_k, float eps, int32_t interleaved,
+                      const int32_t* q_offsets, const int32_t* kv_lens, const int32_t* page_table,
+                      int64_t table_stride, int32_t table_width, int32_t page, int64_t num_pages,
+                      int64_t cache_page_stride, int64_t cache_head_stride, void* k_cache, void* v_cache,
+                      uint8_t* kv_scales, int64_t scale_page_stride, int64_t scale_head_stride, void* q_out,
+                      int32_t* status, void* stream) {
+  NormRopeArgs a;
+  TRY(check_append(n, seqs, q_heads, kv_heads, dim, rot, dtype, {q, q_stride, q_head_stride}, {k, k_stride, k_head_stride},
+                   {v, v_stride, v_head_stride}, positions, pos_stride, axes, sections, inv_freq, w_q, w_k, eps,
+                   interleaved, q_offsets, kv_lens, page_table, table_stride, table_width, page, num_pages,
+                   cache_page_stride, cache_head_stride, k_cache, v_cache, 1, q_out, status, &a));
+  TRY(check_scales(n, kv_heads, page, num_pages, kv_scales, scale_page_stride, scale_head_stride));
+  a.kv_scales = kv_scales; a.scale_page_stride = scale_page_stride; a.scale_head_stride = scale_head_stride;
+  return from_hip(launch_kv_append_q8(a, static_cast<hipStream_t>(stream)));
 }
 
 int dlrm_paged_attn_workspace_bytes(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t dim,

@@ -95,6 +95,10 @@ _SIGNATURES = {
     "dlrm_paged_attn": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, *_HEADS, _c_void_p, _c_void_p, _i32, _i64,
                                        _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _i64, _i32, _i32, _i32, _f32, _i32,
                                        _i32, _c_void_p, _c_void_p, _c_void_p, _size_t, _c_void_p, _c_void_p]),
+    "dlrm_kv_append_q8": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, *_HEADS, *_HEADS, *_HEADS, *_TURN,
+                                         _c_void_p, _c_void_p, _c_void_p, _i64, _i32, _i32, _i64, _i64, _i64,
+                                         _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p,
+                                         _c_void_p]),
     "dlrm_paged_attn_q8_workspace_bytes": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                                                           _P(_size_t)]),
     "dlrm_paged_attn_q8": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, *_HEADS, _c_void_p, _c_void_p, _i32,
@@ -823,17 +827,24 @@ def _paged_args(dtype, dev: int, k_cache, v_cache, q_offsets, kv_lens, page_tabl
     return (S, shape[2], shape[0], by_page, by_head, by_seq, width), where
 
 
-def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
-              q_offsets: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor, *,
-              q: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
-              inv_freq: Optional[torch.Tensor] = None, w_q: Optional[torch.Tensor] = None,
-              w_k: Optional[torch.Tensor] = None, eps: float = 1e-6, sections: Optional[Sequence[int]] = None,
-              interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
-              status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
-    """Appends k (normed and rotated as by qk_norm_rope) and v, [N, Hk, D], to the paged caches
-    [pages, Hk, page, D] in place, and norms and rotates q in the same launch (dlrm_kv_append).
-    Sequence s has tokens q_offsets[s] .. q_offsets[s + 1], the last entries of its kv_lens[s].
-    Returns the new q, contiguous, or None without q (then w_q is not taken)."""
+def _scale_args(kv_scales, dev: int, pages: int, Hk: int, page: int):
+    """Checks the scales of an 8-bit cache; returns their address and page and head stride."""
+    shape, strides = kv_scales.shape, kv_scales.stride()
+    per = page // KV_BLOCK
+    if tuple(shape) != (pages, Hk, per, 2):
+        raise ValueError(f"kv_scales must be [{pages}, {Hk}, {per}, 2], got {tuple(shape)}")
+    if kv_scales.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+        raise ValueError(f"kv_scales must be {torch.float8_e8m0fnu} or its bytes, got {kv_scales.dtype}")
+    if kv_scales.get_device() != dev:
+        raise ValueError(f"kv_scales is on {kv_scales.device}, not on device {dev}")
+    if strides[3] != 1 or (per > 1 and strides[2] != 2):
+        raise ValueError("the scales of a head and page must be contiguous")
+    return kv_scales.data_ptr(), strides[0] if pages > 1 else 0, strides[1] if Hk > 1 else 0
+
+
+def _append(q8: bool, k, v, k_cache, v_cache, kv_scales, q_offsets, kv_lens, page_table, q, positions, inv_freq, w_q, w_k, eps,
+            sections, interleaved, q_out, status, stream):
+    """dlrm_kv_append, or with q8 dlrm_kv_append_q8."""
     shape, ka = _heads_of(k, "k")
     N, Hk, D = shape
     _, va = _heads_of(v, "v", k, shape, Hk)
@@ -849,16 +860,46 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     if q is None:
         turn = turn[:5] + (None,) + turn[6:]
     (S, page, pages, by_page, by_head, by_seq, width), (offsets_at, lens_at, table_at, status_at) = _paged_args(
-        dt, dev, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk, D)
+        torch.float8_e4m3fn if q8 else dt, dev, k_cache, v_cache, q_offsets, kv_lens, page_table, status, Hk, D)
+    scales = _scale_args(kv_scales, dev, pages, Hk, page) if q8 else ()
     if q_out is not None:
         _plain(q_out, "q_out", dt, N * Hq * D, dev)
     with _on(dev, where, stream) as s:
         if q is not None and q_out is None:
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _check(lib().dlrm_kv_append(N, S, Hq, Hk, D, rot, _TORCH_DT[dt], *qa, *ka, *va, *turn, offsets_at, lens_at,
-                                    table_at, by_seq, width, page, pages, by_page, by_head, k_cache.data_ptr(),
-                                    v_cache.data_ptr(), _ptr(q_out), status_at, s), "dlrm_kv_append")
+        fn, name = (lib().dlrm_kv_append_q8, "dlrm_kv_append_q8") if q8 else (lib().dlrm_kv_append, "dlrm_kv_append")
+        _check(fn(N, S, Hq, Hk, D, rot, _TORCH_DT[dt], *qa, *ka, *va, *turn, offsets_at, lens_at, table_at, by_seq, width,
+                  page, pages, by_page, by_head, k_cache.data_ptr(), v_cache.data_ptr(), *scales, _ptr(q_out), status_at, s),
+               name)
     return q_out
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              q_offsets: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor, *,
+              q: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+              inv_freq: Optional[torch.Tensor] = None, w_q: Optional[torch.Tensor] = None,
+              w_k: Optional[torch.Tensor] = None, eps: float = 1e-6, sections: Optional[Sequence[int]] = None,
+              interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Appends k (normed and rotated as by qk_norm_rope) and v, [N, Hk, D], to the paged caches
+    [pages, Hk, page, D] in place, and norms and rotates q in the same launch (dlrm_kv_append).
+    Sequence s has tokens q_offsets[s] .. q_offsets[s + 1], the last entries of its kv_lens[s].
+    Returns the new q, contiguous, or None without q (then w_q is not taken)."""
+    return _append(False, k, v, k_cache, v_cache, None, q_offsets, kv_lens, page_table, q, positions, inv_freq, w_q, w_k, eps,
+                   sections, interleaved, q_out, status, stream)
+
+
+def kv_append_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 kv_scales: torch.Tensor, q_offsets: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor, *,
+                 q: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                 inv_freq: Optional[torch.Tensor] = None, w_q: Optional[torch.Tensor] = None,
+                 w_k: Optional[torch.Tensor] = None, eps: float = 1e-6, sections: Optional[Sequence[int]] = None,
+                 interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """kv_append to caches of torch.float8_e4m3fn and their kv_scales [pages, Hk, page / KV_BLOCK, 2] of
+    torch.float8_e8m0fnu (or uint8), which grow with what is stored (dlrm_kv_append_q8)."""
+    return _append(True, k, v, k_cache, v_cache, kv_scales, q_offsets, kv_lens, page_table, q, positions, inv_freq, w_q, w_k,
+                   eps, sections, interleaved, q_out, status, stream)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -923,21 +964,6 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, q_
     out [N, Hq, D], or (out, lse [N, Hq] fp32) with want_lse."""
     return _attn(False, q, k_cache, v_cache, None, q_offsets, kv_lens, page_table, causal, window, scale, max_q, max_kv, want_lse,
                  out, lse, workspace, status, stream)
-
-
-def _scale_args(kv_scales, dev: int, pages: int, Hk: int, page: int):
-    """Checks the scales of an 8-bit cache; returns their address and page and head stride."""
-    shape, strides = kv_scales.shape, kv_scales.stride()
-    per = page // KV_BLOCK
-    if tuple(shape) != (pages, Hk, per, 2):
-        raise ValueError(f"kv_scales must be [{pages}, {Hk}, {per}, 2], got {tuple(shape)}")
-    if kv_scales.dtype not in (torch.float8_e8m0fnu, torch.uint8):
-        raise ValueError(f"kv_scales must be {torch.float8_e8m0fnu} or its bytes, got {kv_scales.dtype}")
-    if kv_scales.get_device() != dev:
-        raise ValueError(f"kv_scales is on {kv_scales.device}, not on device {dev}")
-    if strides[3] != 1 or (per > 1 and strides[2] != 2):
-        raise ValueError("the scales of a head and page must be contiguous")
-    return kv_scales.data_ptr(), strides[0] if pages > 1 else 0, strides[1] if Hk > 1 else 0
 
 
 @functools.lru_cache(maxsize=1024)

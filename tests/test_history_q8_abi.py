@@ -1,0 +1,136 @@
+"""The 8-bit cache's checks of arguments, which need no GPU: bad sizes, strides and addresses are refused before any HIP
+call, the binding refuses wrong tensors; and pins of the oracle."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import history_oracle as ho
+from sparse_embedding_lookup_dlrm_amd import ops
+from test_history_abi import A, E_ALIGN, E_INVAL, E_UNSUPPORTED, E_WORKSPACE, _secs
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return ops.lib()
+
+
+def _append(lib, n=4, S=2, Hq=4, Hk=2, D=64, dt=2, q=A, k=A, v=A, wq=A, wk=A, off=A, lens=A, table=A, ts=8, width=8, page=32, pages=10,
+            by_page=2 * 32 * 64, by_head=32 * 64, kc=A, vc=A, sc=A, s_page=8, s_head=4, qo=A, status=None, rot=64, eps=1e-6):
+    return lib.dlrm_kv_append_q8(n, S, Hq, Hk, D, rot, dt, q, 256, 64, k, 128, 64, v, 128, 64, A, 4, 1, _secs(rot // 2), A, wq, wk, eps, 0,
+                                 off, lens, table, ts, width, page, pages, by_page, by_head, kc, vc, sc, s_page, s_head, qo, status, None)
+
+
+def _attn(lib, n=4, S=2, Hq=4, Hk=2, D=64, dt=2, q=A, qs=256, qh=64, kc=A, vc=A, page=32, pages=10, by_page=2 * 32 * 64, by_head=32 * 64,
+          sc=A, s_page=8, s_head=4, off=A, lens=A, table=A, width=8, causal=1, window=0, scale=0.1, max_q=2, max_kv=128, out=A, lse=A, ws=A,
+          ws_bytes=1 << 30):
+    return lib.dlrm_paged_attn_q8(n, S, Hq, Hk, D, dt, q, qs, qh, kc, vc, page, pages, by_page, by_head, sc, s_page, s_head, off, lens,
+                                  table, width, width, causal, window, scale, max_q, max_kv, out, lse, ws, ws_bytes, None, None)
+
+
+BOTH = [(dict(sc=None), E_INVAL), (dict(s_head=2), E_INVAL), (dict(s_page=6), E_INVAL), (dict(s_head=-4), E_INVAL), (dict(sc=A + 1), E_ALIGN),
+        (dict(s_page=9), E_ALIGN), (dict(s_head=5), E_ALIGN), (dict(kc=None), E_INVAL), (dict(vc=None), E_INVAL), (dict(kc=A + 8), E_ALIGN),
+        (dict(vc=A + 4), E_ALIGN), (dict(by_page=2 * 32 * 64 + 8), E_ALIGN), (dict(by_head=32 * 64 + 4), E_ALIGN),
+        (dict(by_head=32 * 64 - 16), E_INVAL), (dict(by_page=2 * 32 * 64 - 16), E_INVAL), (dict(page=8), E_UNSUPPORTED), (dict(page=48), E_UNSUPPORTED),
+        (dict(dt=0), E_UNSUPPORTED), (dict(dt=4), E_UNSUPPORTED), (dict(D=80), E_UNSUPPORTED), (dict(S=-1), E_INVAL), (dict(n=-1), E_INVAL),
+        (dict(S=2 ** 31 - 2), E_UNSUPPORTED), (dict(off=None), E_INVAL), (dict(lens=None), E_INVAL), (dict(table=None), E_INVAL),
+        (dict(pages=-1), E_INVAL), (dict(pages=2 ** 31), E_INVAL), (dict(width=-1), E_INVAL), (dict(width=1 << 28), E_UNSUPPORTED),
+        (dict(Hk=0), E_INVAL), (dict(Hq=65535), E_UNSUPPORTED), (dict(q=A + 8), E_ALIGN), (dict(q=None), E_INVAL), (dict(off=A + 2), E_ALIGN)]
+
+
+@pytest.mark.parametrize("kw,code", BOTH)
+def test_bad_arguments_of_both(lib, kw, code):
+    assert _append(lib, **kw) == code
+    if kw != dict(Hq=65535):
+        assert _attn(lib, **kw) == code
+
+
+def test_bad_arguments_of_each(lib):
+    for kw, code in [(dict(k=None), E_INVAL), (dict(v=None), E_INVAL), (dict(qo=None), E_INVAL), (dict(wq=None), E_INVAL), (dict(Hq=0), E_INVAL),
+                     (dict(rot=-16), E_INVAL), (dict(rot=40), E_UNSUPPORTED), (dict(k=A + 8), E_ALIGN), (dict(qo=A + 8), E_ALIGN),
+                     (dict(status=A + 2), E_ALIGN), (dict(eps=-1.0), E_INVAL), (dict(ts=-1), E_INVAL)]:
+        assert _append(lib, **kw) == code, kw
+    for kw, code in [(dict(Hq=0), E_INVAL), (dict(Hq=5), E_INVAL), (dict(window=-1), E_INVAL), (dict(causal=0, window=4), E_INVAL),
+                     (dict(scale=0.0), E_INVAL), (dict(scale=float("nan")), E_INVAL), (dict(max_q=-1), E_INVAL), (dict(max_kv=-1), E_INVAL),
+                     (dict(out=None), E_INVAL), (dict(Hq=4096, Hk=2), E_UNSUPPORTED), (dict(qs=252), E_ALIGN), (dict(out=A + 8), E_ALIGN),
+                     (dict(lse=A + 2), E_ALIGN), (dict(ws=A + 64), E_ALIGN)]:
+        assert _attn(lib, **kw) == code, kw
+    need = ctypes.c_size_t(0)
+    ask = lib.dlrm_paged_attn_q8_workspace_bytes
+    assert ask(1, 1, 8, 1, 128, 1, 0, 1, 100_000, ctypes.byref(need)) == 0 and need.value > 0
+    kw = dict(n=1, S=1, Hq=8, Hk=1, D=128, max_q=1, max_kv=100_000, width=4000, by_head=32 * 128, by_page=32 * 128)
+    assert _attn(lib, **kw, ws_bytes=need.value - 1) == E_WORKSPACE
+    assert _attn(lib, **kw, ws=None) == E_INVAL
+    assert ask(1, 1, 8, 3, 128, 1, 0, 1, 100, ctypes.byref(need)) == E_INVAL
+    assert ask(1, 1, 8, 1, 128, 1, 0, 1, 100, None) == E_INVAL
+    assert ask(4, 2 ** 31 - 2, 4, 2, 64, 1, 0, 2, 128, ctypes.byref(need)) == E_UNSUPPORTED
+
+
+def test_workspace_stays_bounded(lib):
+    """Hints that are too small, or many tokens past the last sequence: no workspace of many GB."""
+    need = ctypes.c_size_t(0)
+    for n in (4096, 65536, 1 << 20, 1 << 24):
+        for S in (1, 8, 300):
+            for Hq, Hk in ((32, 8), (16, 1), (4, 4), (64, 64)):
+                for D in (32, 64, 128, 256):
+                    for max_q in (0, 1, 5, 17, 129):
+                        for max_kv in (4096, 131072, 1 << 30):
+                            if n * Hq < 1 << 31:
+                                assert lib.dlrm_paged_attn_q8_workspace_bytes(n, S, Hq, Hk, D, 1, 0, max_q, max_kv, ctypes.byref(need)) == 0
+                                assert need.value < 8 * D * 1_000_000, (n, S, Hq, Hk, D, max_q, max_kv, need.value)
+
+
+def test_binding_rejects_wrong_tensors():
+    z = torch.zeros
+    e4, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    q, k = z(4, 4, 64, dtype=torch.bfloat16), z(4, 2, 64, dtype=torch.bfloat16)
+    cache, scales = z(6, 2, 32, 64, dtype=e4), z(6, 2, 2, 2, dtype=torch.uint8).view(e8)
+    off, lens, table = (z(s, dtype=torch.int32) for s in ((3,), (2,), (2, 4)))
+    rest = (off, lens, table)
+    for caches, match in [((cache.view(torch.uint8), cache, scales), "caches must be"), ((cache, z(6, 2, 32, 64, dtype=torch.bfloat16), scales), "caches must be"),
+                          ((cache, cache, scales[:5]), "kv_scales must be"), ((cache, cache, scales[:, :, :1]), "kv_scales must be"),
+                          ((cache, cache, scales.view(torch.uint8).float()), "or its bytes"),
+                          ((cache, cache, z(6, 2, 2, 4, dtype=torch.uint8)[..., ::2]), "contiguous"), ((cache, cache, z(6, 2, 2, 2, dtype=torch.uint8).transpose(2, 3)), "contiguous"),
+                          ((cache[:, :1], cache, scales), "cache must"), ((cache, cache[:5], scales), "v_cache must"), ((cache, cache, scales), "CUDA")]:
+        with pytest.raises(ValueError, match=match):
+            ops.paged_attn_q8(q, *caches, *rest)
+        with pytest.raises(ValueError, match=match):
+            ops.kv_append_q8(k, k, *caches, *rest)
+    with pytest.raises(ValueError, match="must lie between"):
+        ops.paged_attn_q8(q, cache, cache, scales, *rest, window=2 ** 32 + 5)
+    for kw, match in [(dict(q_out=q), "q_out without q"), (dict(w_q=z(64)), "w_q without q"), (dict(inv_freq=z(32)), "positions")]:
+        with pytest.raises(ValueError, match=match):
+            ops.kv_append_q8(k, k, cache, cache, scales, *rest, **kw)
+
+
+def test_oracle_codes():
+    """Codes by hand, torch's own conversion for all others, and rounding to even between neighbours."""
+    v = ho.e4m3_values()
+    for code, x in [(0, 0.0), (1, 2.0 ** -9), (7, 7 * 2.0 ** -9), (8, 2.0 ** -6), (0x38, 1.0), (0x39, 1.125), (0x7E, 448.0), (0xC0, -2.0)]:
+        assert v[code] == x and ho.e4m3_round(x) == code
+    assert np.isnan(v[0x7F]) and np.isnan(v[0xFF])
+    all_codes = torch.arange(256, dtype=torch.uint8)
+    assert np.array_equal(v, all_codes.view(torch.float8_e4m3fn).double().numpy(), equal_nan=True)
+    mid = (v[:126] + v[1:127]) / 2
+    x = np.concatenate([mid, -mid, np.linspace(-448, 448, 10001), np.linspace(-0.02, 0.02, 10001)]).astype(np.float32)
+    assert np.array_equal(ho.e4m3_round(x), torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+    assert ho.e4m3_round(17 * 2.0 ** -4 * 1.0) == 0x38 and ho.e4m3_round(19 * 2.0 ** -4) == 0x3A  # between 1, 1.125 and 1.25
+
+
+def test_oracle_scale_by_hand():
+    for top, b in [(448.0, 127), (448.1, 128), (1.75, 119), (1.7501, 120), (3.5, 120), (1.0, 119), (0.0, 1), (2.0 ** -133, 1), (2.0 ** 127, 246), (1.9 * 2.0 ** 127, 247)]:
+        assert ho.scale_byte(top) == b, top
+
+
+def test_oracle_block_by_hand():
+    """One old entry of 1.0 under scale 1 (code 0x38) and a new one of 2 * 448: the scale doubles, the old code is 0.5."""
+    codes, scales = np.zeros((1, 1, 16, 32), dtype=np.uint8), np.full((1, 1, 1), 127, dtype=np.uint8)
+    codes[0, 0, 0] = 0x38
+    codes[0, 0, 0, 1] = 0x01  # 2^-9, halfway to nothing under the new scale: even
+    x = np.full((1, 1, 32), 896.0)
+    ho.append_q8(x, codes, scales, [0, 1], [2], [[0]])
+    assert scales[0, 0, 0] == 128 and codes[0, 0, 0, 0] == 0x30 and codes[0, 0, 0, 1] == 0 and (codes[0, 0, 1] == 0x7E).all()
+    # a smaller one later leaves the scale
+    ho.append_q8(x / 64, codes, scales, [0, 1], [3], [[0]])
+    assert scales[0, 0, 0] == 128 and (ho.e4m3_values()[codes[0, 0, 2]] == 7).all()
