@@ -56,6 +56,32 @@ __device__ __forceinline__ uint32_t widen_codes(uint32_t codes, float scale) {
 __device__ __forceinline__ float key_scale(int bytes) { return __uint_as_float((bytes & 0xff) << 23); }
 __device__ __forceinline__ float value_scale(int bytes) { return __uint_as_float((bytes >> 8 & 0xff) << 23); }
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <int DT>
+__device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f32x16& c) {
+  if constexpr (DT == DLRM_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+
+// Tiles of the tile kernels lie in LDS in rows of D 16-bit elements, D / 8 pieces of 16 bytes; piece c of entry r lies at
+// place c ^ swizzle(r).
+// Keys are read as rows (32 entries, the same piece): neighbours differ in every place bit.
+template <int D>
+__device__ __forceinline__ int key_swizzle(int r) {
+  return D == 32 ? r >> 1 & 3 : D == 64 ? r & 7 : r & 15;
+}
+// Values are read as blocks of 4 entries x 2 (or, with the neighbouring lanes, 4) pieces.
+template <int D>
+__device__ __forceinline__ int value_swizzle(int r) {
+  return D == 32 ? r & 2 : D == 64 ? (r & 1) << 2 | (r & 2) : (r & 1) << 2 | (r & 2) | (r & 2) << 2;
+}
+
 // All bits of those of the two 16-bit values of a dword that are infinite or NaN.
 template <int DT>
 __device__ __forceinline__ uint32_t not_finite_halves(uint32_t w) {
@@ -127,12 +153,23 @@ __device__ __forceinline__ float add_quarters(float x) {
 }
 
 // How a call is cut: q_tiles tiles of rows per sequence and head, splits parts of a tile's entries. The
-// grid is heads x (tiles x parts) x sequences.
+// grid is heads x (tiles x parts) x sequences. A sequence of fewer tiles than there are places for them has up to
+// `spread` parts in their stead, if that is more.
 struct Cut {
   int q_tiles, splits, part;  // part: entries of a part, unless the history is longer than announced
-  float* o;                   // [splits][n][q_heads][dim], not yet divided by the sums
-  float2* ml;                 // [n][q_heads][splits]: maximum and sum
+  int spread;
+  float* o;                   // [splits or spread][n][q_heads][dim], not yet divided by the sums
+  float2* ml;                 // [n][q_heads][splits or spread]: maximum and sum
+  __host__ __device__ __forceinline__ int most() const { return spread > splits ? spread : splits; }
+  // Parts that a sequence of so many rows may have, in tiles of tile_rows.
+  __device__ __forceinline__ int parts_of(int rows, int tile_rows) const {
+    if (spread <= splits) return splits;
+    const int tiles = (rows + tile_rows - 1) / tile_rows, fit = tiles > 0 ? q_tiles * splits / tiles : spread;
+    return fit < splits ? splits : fit < spread ? fit : spread;
+  }
 };
+
+constexpr int kLeastPart = 512;  // entries of a part that a sequence of few rows is spread to
 
 // Entries that the rows [row0, row_end) of a sequence see between them, and their parts.
 struct Reach {
@@ -141,7 +178,7 @@ struct Reach {
   int all_lo, all_hi;  // every row sees these
   int first, part, parts;
   __device__ __forceinline__ Reach(const Seq& s, int row0, int row_end, int group, int causal, int window,
-                                   const Cut& cut) {
+                                   const Cut& cut, int may) {  // may: most parts
     tok0 = row0 / group;
     tok1 = (row_end - 1) / group;
     const Span s0 = seen_by(s, tok0, causal, window), s1 = seen_by(s, tok1, causal, window);
@@ -151,10 +188,10 @@ struct Reach {
     all_hi = s0.hi;
     first = lo & ~31;
     const int span = hi > first ? hi - first : 0;
-    part = cut.part;
+    part = may > cut.splits && cut.part > kLeastPart ? kLeastPart : cut.part;
     // spans stay below 2^31 - 2^17, so the sums below fit 32 bits
-    if (span > static_cast<long long>(part) * cut.splits)
-      part = ((static_cast<uint32_t>(span) + cut.splits - 1) / static_cast<uint32_t>(cut.splits) + 63) & ~63u;
+    if (span > static_cast<long long>(part) * may)
+      part = ((static_cast<uint32_t>(span) + may - 1) / static_cast<uint32_t>(may) + 63) & ~63u;
     parts = span > part ? (static_cast<uint32_t>(span) + part - 1) / static_cast<uint32_t>(part) : 1;
   }
 };
@@ -167,6 +204,24 @@ __device__ __forceinline__ void finish(const AttnArgs& a, long long to, int at, 
   for (int d = 0; d < 8; ++d) x[d] *= inv;
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + to * a.dim + at) = narrow<DT>(x);
   if (at == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : fmaf(m, a.scale, logf(l) - kLift<DT> * kLn2);
+}
+
+// The sequence that comes `at`-th if those whose parts are longest come first, where a wave can look at all of them
+// (up to 64); else the at-th. Equal ones keep their order. tile_rows: rows of a tile.
+__device__ __forceinline__ int longest_first(const AttnArgs& a, const Cut& cut, int at, int tile_rows) {
+  const Paged& p = a.paged;
+  if (p.seqs > kWave) return at;
+  const int lane = threadIdx.x & (kWave - 1), i = lane < p.seqs ? lane : 0, group = a.q_heads / a.kv_heads;
+  const int held = p.kv_lens[i], tokens = p.q_offsets[i + 1] - p.q_offsets[i];  // bad ones count as they may
+  const int seen = a.window > 0 && held > a.window ? a.window : held;
+  const bool some = lane < p.seqs && tokens > 0 && tokens <= a.n;
+  const int work = some && seen > 0 ? seen / cut.parts_of(tokens * group, tile_rows) + 1 : lane < p.seqs ? 0 : -1;
+  int before = 0;
+  for (int j = 0; j < p.seqs; ++j) {
+    const int other = __builtin_amdgcn_readlane(work, j);
+    before += other > work || (other == work && j < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < p.seqs && before == at));
 }
 
 template <int D>
@@ -223,7 +278,7 @@ __device__ __forceinline__ void join_waves(const AttnArgs& a, const Cut& cut, co
       float* p = cut.o + (split * a.n * a.q_heads + to) * D + at;
       *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
       *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-      if (at == 0) cut.ml[to * cut.splits + split] = make_float2(mt, lt);
+      if (at == 0) cut.ml[to * cut.most() + split] = make_float2(mt, lt);
     }
   }
 }
@@ -245,17 +300,18 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, Cut cut
   const int at = threadIdx.x % Lanes * 8, slot = threadIdx.x / Lanes % Slots;
   for (int seq = blockIdx.y; seq < a.paged.seqs; seq += gridDim.y) {
     const Seq sq = load_seq(a.paged, a.n, seq);
-    const int rows = sq.tokens * a.q_heads;
+    const int rows = sq.tokens * a.q_heads, may = cut.parts_of(sq.tokens * group, tile_rows);
+    if (may == 1) continue;
     for (long long first = static_cast<long long>(blockIdx.x) * Rows; first < rows;
          first += static_cast<long long>(gridDim.x) * Rows) {
       const int row = static_cast<int>(first) + threadIdx.x / (Lanes * Slots);
       if (row >= rows) continue;  // with Slots > 1 there is one row, and no thread leaves it
       const int tok = row / a.q_heads, in_head = tok * group + (row - tok * a.q_heads) % group;
       const int row0 = in_head / tile_rows * tile_rows, in_all = sq.tokens * group;
-      const Reach rc(sq, row0, in_all - row0 > tile_rows ? row0 + tile_rows : in_all, group, a.causal, a.window, cut);
+      const Reach rc(sq, row0, in_all - row0 > tile_rows ? row0 + tile_rows : in_all, group, a.causal, a.window, cut, may);
       if (rc.parts == 1) continue;
       const long long to = static_cast<long long>(sq.first) * a.q_heads + row;
-      const float2* ml = cut.ml + to * cut.splits;
+      const float2* ml = cut.ml + to * cut.most();
       const float* o = cut.o + to * D + at;
       const long long step = a.n * a.q_heads * D;
       float m = -INFINITY, l = 0.f, x[8] = {};
@@ -313,29 +369,24 @@ int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
 constexpr size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t cut_bytes(const Cut& c, int64_t n, int q_heads, int dim) {
-  if (c.splits == 1) return 0;
-  const size_t rows = static_cast<size_t>(n) * q_heads * c.splits;
+  if (c.most() == 1) return 0;
+  const size_t rows = static_cast<size_t>(n) * q_heads * c.most();
   return round256(rows * dim * sizeof(float)) + rows * sizeof(float2);
 }
 
-// The kernel of a call that is cut into parts, and their join.
+// The kernel of a call that is cut into tiles of `tile` rows and into parts, and their join.
 template <int DT, int D>
-hipError_t launch_cut(const AttnArgs& a, Cut cut, void (*rows_kernel)(AttnArgs, Cut), void (*tile_kernel)(AttnArgs, Cut),
-                      int tile_threads, hipStream_t s) {
+hipError_t launch_cut(const AttnArgs& a, Cut cut, int tile, void (*kernel)(AttnArgs, Cut), int threads, hipStream_t s) {
   const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
   cut.o = static_cast<float*>(a.workspace);
   cut.ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) +
-                                     round256(static_cast<size_t>(a.n) * a.q_heads * cut.splits * D * sizeof(float)));
-  const dim3 grid(a.kv_heads, cut.q_tiles * cut.splits, a.paged.seqs < 65535 ? a.paged.seqs : 65535);
-  const int tile = tile_rows(rows);
-  if (tile == 16)
-    hipLaunchKernelGGL(rows_kernel, grid, dim3(kThreads), 0, s, a, cut);
-  else
-    hipLaunchKernelGGL(tile_kernel, grid, dim3(tile_threads), 0, s, a, cut);
+                                     round256(static_cast<size_t>(a.n) * a.q_heads * cut.most() * D * sizeof(float)));
+  const unsigned seqs = a.paged.seqs < 65535 ? a.paged.seqs : 65535;
+  hipLaunchKernelGGL(kernel, dim3(a.kv_heads, cut.q_tiles * cut.splits, seqs), dim3(threads), 0, s, a, cut);
   const long long all_rows = rows * a.kv_heads * a.paged.seqs;
-  if (cut.splits > 16 && all_rows <= 512)
+  if (cut.most() > 16 && all_rows <= 512)
     join<DT, D, kThreads / (D / 8)>(a, cut, tile, s);
-  else if (cut.splits > 1)
+  else if (cut.most() > 1)
     join<DT, D, 1>(a, cut, tile, s);
   return hipGetLastError();
 }

@@ -3,7 +3,7 @@
 //
 // Codes are widened to the 16-bit type of the queries, which is exact, by an instruction that takes two of them and
 // their scale, so that the matrix products, the softmax and the joins are those of the 16-bit cache.
-#include "attn_tile.h"
+#include "attn_device.h"
 
 namespace dlrm {
 namespace {
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_q8_kerne
     for (long long first_row = static_cast<long long>(blockIdx.y / cut.splits) * Rows; first_row < rows;
          first_row += static_cast<long long>(cut.q_tiles) * Rows) {
       const int row0 = static_cast<int>(first_row), row_end = rows - row0 > Rows ? row0 + Rows : rows;
-      const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut);
+      const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut, cut.splits);
       if (split >= rc.parts) continue;
       const int k_first = rc.first + split * rc.part;
       const int hi = rc.hi - k_first < rc.part ? rc.hi : k_first + rc.part;
@@ -301,6 +301,343 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_q8_kerne
   }
 }
 
+// ---------------------------------------------------------------------------
+// Tile kernel: 128 rows of one head to a workgroup, 32 to a wave, tiles of 64 entries in LDS that every wave reads all
+// of. Products are 32x32x16: the score of row lane % 32 with entries 8 i + 4 h + j (h = lane / 32, i, j = 0 .. 3) lies in
+// one lane, which again is the second product's right operand as it stands; its left operand V^T is read by the transposing
+// LDS load: sixteen lanes take a block of 4 entries x 16 elements and get one element of the 4 entries each.
+//
+// Codes are widened on their way to LDS, once for the workgroup and not by each of its waves: a wave brings 16 entries of
+// a tile, loaded while the tile before is worked on, in pieces of 8 codes that become 16 bytes.
+// ---------------------------------------------------------------------------
+template <int DT, int D>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_q8_kernel(AttnArgs a, Cut cut) {
+  constexpr int K = 16 * kWaves;    // entries of a tile: a wave brings 16, which lie in one page
+  constexpr int Q = D / 16;         // steps of the first product, and of the second, for 32 entries
+  constexpr int C = D / 32;         // 32-wide pieces of O
+  constexpr int P = D / 8;          // pieces of a row
+  constexpr int T = D == 256 ? 1 : 2;  // blocks of 32 entries worked on at once
+  constexpr int Loads = 16 * D / (kWave * 8);  // of a wave's keys, and of its values
+  constexpr int Rows = 32 * kWaves;
+  constexpr int Ahead = 64 / kWaves;           // tiles whose pages a wave holds
+  static_assert(2 * Loads == Q, "a piece goes to LDS beside each matrix instruction of the first scores");
+  __shared__ __align__(16) uint16_t lds_k[2][K * D];
+  __shared__ __align__(16) uint16_t lds_v[2][K * D];
+  const int lane = threadIdx.x & (kWave - 1), h = lane >> 5, c32 = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int group = a.q_heads / a.kv_heads;
+  const float c = a.scale * kLog2e;
+  const Paged& pg = a.paged;
+  const int page_mask = (1 << pg.page_shift) - 1;
+  const int head = blockIdx.x;
+  const char* kh = static_cast<const char*>(a.k_cache) + head * pg.head_stride;
+  const char* vh = static_cast<const char*>(a.v_cache) + head * pg.head_stride;
+  const uint8_t* sh = a.kv_scales + head * a.scale_head_stride;
+
+  for (int at_seq = blockIdx.z; at_seq < pg.seqs; at_seq += gridDim.z) {
+    const int seq = longest_first(a, cut, at_seq, Rows);
+    const Seq sq = load_seq(pg, a.n, seq);
+    const int rows = sq.tokens * group;
+    const int32_t* table = pg.page_table + seq * pg.table_stride;
+
+    // the last rows of a causal chunk see the most: they start first
+    const int may = cut.parts_of(rows, Rows), split = blockIdx.y % may, step = gridDim.y / may;
+    for (int tile = (rows + Rows - 1) / Rows - 1 - blockIdx.y / may; tile >= 0; tile -= step) {
+      const int row0 = tile * Rows, row_end = rows - row0 > Rows ? row0 + Rows : rows;
+      const Reach rc(sq, row0, row_end, group, a.causal, a.window, cut, may);
+      if (split >= rc.parts) continue;
+      const int k_first = rc.first + split * rc.part;
+      const int hi = rc.hi - k_first < rc.part ? rc.hi : k_first + rc.part;
+      // what this wave's rows see: some of them [w_lo, w_hi), all of them [w_all_lo, w_all_hi)
+      const int w0 = row0 + 32 * wave, w1 = w0 + 32 < row_end ? w0 + 32 : row_end;
+      int w_lo = 0, w_hi = 0, w_all_lo = 0, w_all_hi = 0;
+      if (w0 < w1) {
+        const Span s0 = seen_by(sq, w0 / group, a.causal, a.window), s1 = seen_by(sq, (w1 - 1) / group, a.causal, a.window);
+        w_lo = s0.lo;
+        w_hi = s1.hi;
+        w_all_lo = s1.lo;
+        w_all_hi = s0.hi;
+      }
+      const int row = w0 + c32;
+      int row_lo = 0, row_hi = 0;
+      long long to = 0;  // row of the output
+      u32x4 qf[Q];
+#pragma unroll
+      for (int s = 0; s < Q; ++s) qf[s] = u32x4{0, 0, 0, 0};
+      if (row < w1) {
+        const int tok = row / group, gi = row - tok * group;
+        const Span s = seen_by(sq, tok, a.causal, a.window);
+        row_lo = s.lo;
+        row_hi = s.hi;
+        to = static_cast<long long>(sq.first + tok) * a.q_heads + head * group + gi;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q.ptr) + (sq.first + tok) * a.q.stride +
+                            (head * group + gi) * a.q.head_stride + h * 8;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) qf[i] = *reinterpret_cast<const u32x4*>(q + i * 16);
+      }
+
+      float m = -INFINITY, l = 0.f;
+      f32x16 o[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
+
+      // Pages of 64 blocks of 16 entries (Ahead tiles) at a time, one to a lane, read as many tiles ahead, and their
+      // scales; past the end: of the last entry.
+      const auto look_up = [&](int k0) {
+        const int key = k0 + 16 * lane;
+        return table[(key < hi ? key : hi - 1) >> pg.page_shift];
+      };
+      int pages = 0, pages_next = 0, scales = 0, at = 0;
+      uint64_t good64 = 0;  // bit i: the page of block i is good
+      const auto next_pages = [&](int k0) {  // the tile at k0 is the first of the next Ahead
+        pages = pages_next;
+        const bool good = static_cast<uint32_t>(pages) < static_cast<uint32_t>(pg.num_pages);
+        if (!good && k0 + 16 * lane < hi && k0 + 16 * lane + 16 > rc.lo) flag(pg.status, DLRM_STATUS_BAD_PAGE);
+        good64 = __ballot(good);
+        pages_next = look_up(k0 + Ahead * K < hi ? k0 + Ahead * K : k0);
+        const int key = k0 + 16 * lane, known = (key < hi ? key : hi - 1) & page_mask;
+        scales = *reinterpret_cast<const uint16_t*>(sh + (good ? pages : 0) * a.scale_page_stride + known / kScaleBlock * 2);
+      };
+      // This wave's 16 entries of the tile at k0, block kWaves at + wave of the pages at hand: a contiguous piece of the
+      // cache. Past the end and in place of a bad page other entries are read, and masked.
+      uint2 raw[2][Loads];
+      const auto fetch_tile = [&](int k0) {
+        const int key = k0 + 16 * wave, known = key < hi ? key : hi - 1, block = kWaves * at + wave;
+        const int page = good64 >> block & 1 ? __builtin_amdgcn_readlane(pages, block) : 0;
+        const long long from = page * pg.page_stride + (known & page_mask & ~15) * D + lane * 8;
+#pragma unroll
+        for (int i = 0; i < Loads; ++i) {
+          raw[0][i] = *reinterpret_cast<const uint2*>(kh + from + i * kWave * 8);
+          raw[1][i] = *reinterpret_cast<const uint2*>(vh + from + i * kWave * 8);
+        }
+      };
+      float put_scale[2] = {1.f, 1.f};  // of the keys and values in registers
+      const auto put_scales = [&] {
+        const int two = __builtin_amdgcn_readlane(scales, kWaves * at + wave);
+        put_scale[0] = key_scale(two);
+        put_scale[1] = value_scale(two);
+      };
+      // Piece n of what the registers hold goes to LDS. Sixteen lanes fill places of all banks (with 16 codes a lane it is
+      // every other place of a row of values, 18 % of the time in conflicts).
+      const auto put_one = [&](int n, int buf) {
+        const int value = n / Loads, i = n % Loads, r = (i * kWave + lane) / P, piece = lane % P;
+        uint16_t* rows16 = (value ? lds_v[buf] : lds_k[buf]) + (16 * wave + r) * D;
+        uint2 w = raw[value][i];
+        asm volatile("" : "+v"(w.x), "+v"(w.y));  // widened here, not ahead of the branches that come to this
+        const float scale = put_scale[value];
+        *reinterpret_cast<uint4*>(rows16 + (piece ^ (value ? value_swizzle<D>(r) : key_swizzle<D>(r))) * 8) =
+            make_uint4(widen_codes<DT, false>(w.x, scale), widen_codes<DT, true>(w.x, scale),
+                       widen_codes<DT, false>(w.y, scale), widen_codes<DT, true>(w.y, scale));
+      };
+      constexpr int kAllGood = (1 << (K / 16)) - 1;
+
+      __syncthreads();  // the tiles of the rows before are no longer read
+      int good_next = 0;
+      if (k_first < hi) {
+        pages_next = look_up(k_first);
+        next_pages(k_first);
+        fetch_tile(k_first);
+        put_scales();
+#pragma unroll
+        for (int n = 0; n < Q; ++n) put_one(n, 0);
+        good_next = static_cast<int>(good64) & kAllGood;
+        if (k_first + K < hi) {
+          at = 1;
+          fetch_tile(k_first + K);
+        }
+      }
+      for (int k0 = k_first, buf = 0; k0 < hi; k0 += K, buf ^= 1) {
+        __syncthreads();  // this tile is in LDS, and the other one is no longer read
+        const int good = good_next;
+        // The next tile, in registers, goes to LDS between the matrix instructions of the first scores (past the last
+        // tile: what the registers hold, for nobody); then the one after it is asked for.
+        if (k0 + K < hi) {
+          put_scales();
+          good_next = static_cast<int>(good64 >> (kWaves * at)) & kAllGood;
+        }
+        const auto fetch_next = [&] {
+          if (k0 + 2 * K < hi) {
+            at = (at + 1) % Ahead;
+            if (at == 0) next_pages(k0 + 2 * K);
+            fetch_tile(k0 + 2 * K);
+          }
+        };
+        // A tile that some rows do not see whole: a value that is infinite or NaN would reach the rows that
+        // do not see it as 0 x inf, so it counts as zero in the product, and is added after it to the rows
+        // that see it.
+        bool special = false;
+        if (k0 < rc.all_lo || k0 + K > rc.all_hi || k0 + K > hi || good != kAllGood) {
+          bool found = false;
+#pragma unroll 4
+          for (int i = 0; i < K * P / kThreads; ++i) {
+            uint4* piece = reinterpret_cast<uint4*>(lds_v[buf]) + i * kThreads + threadIdx.x;
+            uint4 w = *piece;
+            const uint4 odd = make_uint4(not_finite_halves<DT>(w.x), not_finite_halves<DT>(w.y),
+                                         not_finite_halves<DT>(w.z), not_finite_halves<DT>(w.w));
+            if (odd.x | odd.y | odd.z | odd.w) {
+              *piece = make_uint4(w.x & ~odd.x, w.y & ~odd.y, w.z & ~odd.z, w.w & ~odd.w);
+              found = true;
+            }
+          }
+          special = __syncthreads_or(found) != 0;
+        }
+
+        if (k0 >= w_hi || k0 + K <= w_lo) {  // this wave's rows see none of these entries
+#pragma unroll
+          for (int n = 0; n < Q; ++n) put_one(n, buf ^ 1);
+          fetch_next();
+        } else {
+          // pieces of keys and values are read KW and VW ahead of the matrix unit
+          constexpr int KW = Q > 8 ? 4 : Q < 8 ? Q : 8, VW = KW;
+          const auto key_frag = [&](int b0, int n) {  // block b0 + n % T of 32 entries, step n / T
+            const int r = 32 * (b0 + n % T) + c32, place = (n / T * 2 + h) ^ key_swizzle<D>(r);
+            return *reinterpret_cast<const u32x4*>(lds_k[buf] + r * D + place * 8);
+          };
+          // V^T of 16 entries (step n / C) and 32 elements (piece n % C): entries 4 h .. and 8 + 4 h .. of the step
+          const auto value_frag = [&](int b0, int n) {
+            u32x4 w;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int r = 32 * b0 + 16 * (n / C) + 8 * k + 4 * h + (lane & 15) / 4;
+              const int place = (n % C * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1)) ^ value_swizzle<D>(r);
+              const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                  (__attribute__((address_space(3))) s16x4*)(lds_v[buf] + r * D + place * 8 + (lane & 1) * 4));
+              const uint2 u = __builtin_bit_cast(uint2, x);
+              w[2 * k] = u.x;
+              w[2 * k + 1] = u.y;
+            }
+            return w;
+          };
+          const auto mask = [&](f32x16& s, int b) {  // block b of 32 entries
+            const int e0 = k0 + 32 * b;
+            if (e0 < w_all_lo || e0 + 32 > w_all_hi || e0 + 32 > hi || (good >> (2 * b) & 3) != 3) {
+#pragma unroll
+              for (int r = 0; r < 16; ++r) {
+                const int e = 8 * (r / 4) + 4 * h + r % 4, key = e0 + e;
+                if (key < row_lo || key >= row_hi || key >= hi || !(good >> (2 * b + e / 16) & 1)) s[r] = -INFINITY;
+              }
+            }
+          };
+#pragma unroll
+          for (int b0 = 0; b0 < 2; b0 += T) {
+            u32x4 kf[KW], vf[VW];
+#pragma unroll
+            for (int n = 0; n < KW; ++n) kf[n] = key_frag(b0, n);
+            // the blocks' chains in turn: a matrix instruction waits for the one before it in its sum
+            f32x16 s[T];
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) s[t][r] = 0.f;
+#pragma unroll
+            for (int n = 0; n < T * Q; ++n) {
+              s[n % T] = mfma32<DT>(kf[n % KW], qf[n / T], s[n % T]);
+              if (n + KW < T * Q) kf[n % KW] = key_frag(b0, n + KW);
+              if (b0 == 0 && n < Q) put_one(n, buf ^ 1);
+              if (b0 == 0 && n == Q - 1) fetch_next();
+            }
+#pragma unroll
+            for (int n = 0; n < VW; ++n) vf[n] = value_frag(b0, n);
+#pragma unroll
+            for (int t = 0; t < T; ++t) mask(s[t], b0 + t);
+            float tops[4] = {s[0][0], s[0][1], s[0][2], s[0][3]};
+#pragma unroll
+            for (int r = 4; r < 16 * T; ++r) tops[r % 4] = fmaxf(tops[r % 4], s[r / 16][r % 16]);
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+            const float next = fmaxf(m, max_halves(top));
+            // O and l stay relative to an older maximum until a row's grows by 2^8: weights are then at most
+            // 2^8 (fp16: 2^15 with its lift)
+            if (__any((next - m) * c > (DT == DLRM_F16 ? 7.f : 8.f))) {
+              const float keep = m == -INFINITY ? 0.f : exp2f((m - next) * c);
+              m = next;
+              l *= keep;
+#pragma unroll
+              for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[i][r] *= keep;
+            }
+            const float base = m == -INFINITY ? 0.f : m * c - kLift<DT>;
+            float sum[4] = {};
+            u32x4 pw[2 * T];  // weights of 16 entries each
+            const auto weigh = [&](int pair) {
+              const int r = 2 * (pair % 8);
+              const float p_0 = __builtin_amdgcn_exp2f(fmaf(s[pair / 8][r], c, -base));
+              const float p_1 = __builtin_amdgcn_exp2f(fmaf(s[pair / 8][r + 1], c, -base));
+              sum[r % 4] += p_0;
+              sum[r % 4 + 1] += p_1;
+              pw[pair / 4][pair % 4] = pack2<DT>(p_0, p_1);
+            };
+            // the product of 16 entries beside the weights of the next 16
+#pragma unroll
+            for (int pair = 0; pair < 4; ++pair) weigh(pair);
+#pragma unroll
+            for (int n = 0; n < 2 * T * C; ++n) {
+              o[n % C] = mfma32<DT>(vf[n % VW], pw[n / C], o[n % C]);
+              if (n + VW < 2 * T * C) vf[n % VW] = value_frag(b0, n + VW);
+              if (n < (2 * T - 1) * C) {
+#pragma unroll
+                for (int k = n % C * 4 / C; k < (n % C + 1) * 4 / C; ++k) weigh(4 * (n / C + 1) + k);
+              }
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          }
+        }
+
+        if (special) {
+#pragma unroll 1
+          for (int e = 0; e < K; ++e) {
+            const int key = k0 + e;
+            const int page = key < hi ? scalar_load(table, key >> pg.page_shift) : -1;
+            if (page < 0 || page >= pg.num_pages) continue;
+            const char* v = vh + page * pg.page_stride + static_cast<long long>(key & page_mask) * D + 4 * h;
+            const float scale =
+                value_scale(sh[page * a.scale_page_stride + (key & page_mask) / kScaleBlock * 2 + 1] << 8);
+            const bool mine = key >= row_lo && key < row_hi;
+#pragma unroll
+            for (int i = 0; i < 4 * C; ++i) {
+              const uint32_t codes = *reinterpret_cast<const uint32_t*>(v + 8 * i);
+              const uint32_t w[2] = {widen_codes<DT, false>(codes, scale), widen_codes<DT, true>(codes, scale)};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t u = w[j / 2] >> (j % 2 * 16) & 0xffffu;
+                const float x = DT == DLRM_BF16 ? bf16_lo(u) : f16_lo(u);
+                o[i / 4][4 * (i % 4) + j] += mine && not_finite_halves<DT>(u) ? x : 0.f;
+              }
+            }
+          }
+        }
+      }
+
+      l = add_halves(l);
+      if (row < w1) {
+        const bool part = rc.parts > 1;
+        const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int at_d = 32 * i + 8 * q + 4 * h;
+            const float x0 = o[i][4 * q] * inv, x1 = o[i][4 * q + 1] * inv, x2 = o[i][4 * q + 2] * inv,
+                        x3 = o[i][4 * q + 3] * inv;
+            if (part)
+              *reinterpret_cast<float4*>(cut.o + (split * a.n * a.q_heads + to) * D + at_d) = make_float4(x0, x1, x2, x3);
+            else
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to * D + at_d) =
+                  make_uint2(pack2<DT>(x0, x1), pack2<DT>(x2, x3));
+          }
+        if (h == 0) {
+          if (part)
+            cut.ml[to * cut.most() + split] = make_float2(m, l);
+          else if (a.lse)
+            a.lse[to] = l == 0.f ? -INFINITY : fmaf(m, a.scale, logf(l) - kLift<DT> * kLn2);
+        }
+      }
+    }
+  }
+}
+
 // Where the workgroups of a call would not fill the chip, or histories may be of unequal length, every history is split
 // into parts.
 Cut cut_call(long long all_rows, long long max_rows, int seqs, int kv_heads, int dim, int causal, int window, int max_q,
@@ -339,6 +676,9 @@ Cut cut_call(long long all_rows, long long max_rows, int seqs, int kv_heads, int
   if (splits > 65535 / tiles) splits = 65535 / tiles;
   c.splits = static_cast<int>(splits);
   c.part = static_cast<int>(((span + splits - 1) / splits + 63) & ~63LL);
+  // sequences of few rows beside those of many: up to 16 parts, as long as there are sums of a million rows at most
+  const long long room = (1LL << 20) / (all_rows > 0 ? all_rows : 1);
+  c.spread = rows == 16 || tiles == 1 ? 0 : room < 16 ? static_cast<int>(room) : 16;
   c.o = nullptr;
   c.ml = nullptr;
   return c;
@@ -348,7 +688,9 @@ template <int DT, int D>
 hipError_t run(const AttnArgs& a, hipStream_t s) {
   const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
   const Cut cut = cut_call(a.n * a.q_heads, rows, a.paged.seqs, a.kv_heads, D, a.causal, a.window, a.max_q, a.max_kv);
-  return launch_cut<DT, D>(a, cut, attn_rows_q8_kernel<DT, D>, attn_tile_kernel<DT, D, true>, kTileThreads<D>, s);
+  const int tile = tile_rows(rows);
+  if (tile == 16) return launch_cut<DT, D>(a, cut, tile, attn_rows_q8_kernel<DT, D>, kThreads, s);
+  return launch_cut<DT, D>(a, cut, tile, attn_tile_q8_kernel<DT, D>, kThreads, s);
 }
 
 template <int DT>
