@@ -358,7 +358,10 @@ template <int DT, int D, int Slots>
 void join(const AttnArgs& a, const Cut& cut, int tile_rows, hipStream_t s) {
   constexpr int Rows = kThreads / (D / 8 * Slots);
   const long long rows = static_cast<long long>(a.max_q) * a.q_heads, groups = (rows + Rows - 1) / Rows;
-  const unsigned x = static_cast<unsigned>(groups < 1 ? 1 : groups < 65535 ? groups : 65535);
+  // where only sequences of few rows are in parts, the workgroups of all others would come for nothing (16384 of them: 25
+  // us, 1024: 6)
+  const long long most = cut.splits > 1 ? 65535 : 256;
+  const unsigned x = static_cast<unsigned>(groups < 1 ? 1 : groups < most ? groups : most);
   const unsigned y = static_cast<unsigned>(a.paged.seqs < 65535 / 8 ? a.paged.seqs : 65535 / 8);
   hipLaunchKernelGGL((attn_join_kernel<DT, D, Slots>), dim3(x, y), dim3(kThreads), 0, s, a, cut, tile_rows);
 }

@@ -37,7 +37,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_q8_kerne
   const int page_mask = (1 << pg.page_shift) - 1;
   const int head = blockIdx.x, split = blockIdx.y % cut.splits;
   const uint8_t* kh = static_cast<const uint8_t*>(a.k_cache) + head * pg.head_stride + (c16 * D + g * Chunk);
-  const uint8_t* vh = static_cast<const uint8_t*>(a.v_cache) + head * pg.head_stride + (4 * g * D + c16 * E);
+  const uint8_t* value_head = static_cast<const uint8_t*>(a.v_cache) + head * pg.head_stride;
+  const uint8_t* vh = value_head + (4 * g * D + c16 * E);
   const uint8_t* sh = a.kv_scales + head * a.scale_head_stride;
 
   for (int seq = blockIdx.z; seq < pg.seqs; seq += gridDim.z) {
@@ -79,14 +80,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_q8_kerne
 #pragma unroll
       for (int f = 0; f < F; ++f) qf[f] = u32x4{0, 0, 0, 0};
       const int row = row0 + c16;
-      int row_lo = 0, row_hi = 0, row_tok = -1;
+      int row_lo = 0, row_hi = 0;
       if (row < row_end) {
-        row_tok = row / group;
-        const int gi = row - row_tok * group;
-        const Span s = seen_by(sq, row_tok, a.causal, a.window);
+        const int tok = row / group, gi = row - tok * group;
+        const Span s = seen_by(sq, tok, a.causal, a.window);
         row_lo = s.lo;
         row_hi = s.hi;
-        const uint16_t* q = static_cast<const uint16_t*>(a.q.ptr) + (sq.first + row_tok) * a.q.stride +
+        const uint16_t* q = static_cast<const uint16_t*>(a.q.ptr) + (sq.first + tok) * a.q.stride +
                             (head * group + gi) * a.q.head_stride + g * Chunk;
 #pragma unroll
         for (int f = 0; f < F; ++f)
@@ -190,14 +190,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_q8_kerne
           pw[t][1] = pack2<DT>(p[2], p[3]);
         }
 
-        // Entries that no row sees are zero, whatever they and their scale hold. If one that only some rows see
-        // holds a NaN (or a value that fp16 does not), the second product runs token by token, with what the token
-        // does not see set to zero, and only the token's own rows take the sum.
+        // Entries that no row sees are zero, whatever they and their scale hold. What only some rows see and is NaN (or
+        // a value that fp16 does not hold) counts as zero in the product, and is added after it to the rows that see it.
         float vs[TT];
 #pragma unroll
         for (int t = 0; t < TT; ++t) vs[t] = value_scale(two[t]);
-        bool apart = false;
+        bool special = false;
         if (edge) {
+          const bool apart = rc.tok1 > rc.tok0;
 #pragma unroll
           for (int t = 0; t < TT; ++t) {
             const int first = k0 + 16 * t;
@@ -209,57 +209,55 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_q8_kerne
 #pragma unroll
               for (int i = 0; i < VW; ++i) {
                 if (none) v[j][i] = 0;
-                apart |= (not_finite_halves<DT>(widen_codes<DT, false>(v[j][i], vs[t])) |
-                          not_finite_halves<DT>(widen_codes<DT, true>(v[j][i], vs[t]))) != 0;
+                const uint32_t odd = __builtin_amdgcn_perm(not_finite_halves<DT>(widen_codes<DT, true>(v[j][i], vs[t])),
+                                                           not_finite_halves<DT>(widen_codes<DT, false>(v[j][i], vs[t])),
+                                                           0x06040200u);
+                if (apart && odd) {
+                  v[j][i] &= ~odd;
+                  special = true;
+                }
               }
             }
+            if (apart && (two[t] >> 8 & 0xff) == 0xff) vs[t] = 1.f;  // zeros under a scale of NaN would be NaN
           }
-          apart = rc.tok1 > rc.tok0 && __any(apart);
+          special = __any(special);
         }
-        const auto product = [&](auto seen, bool mine) {
 #pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const uint32_t pick = e % 4 ? 0x07030602u : 0x05010400u;
-            f32x4 sum0 = o[e], sum1 = o[e + 1];
+        for (int e = 0; e < E; e += 2) {
+          const uint32_t pick = e % 4 ? 0x07030602u : 0x05010400u;
 #pragma unroll
-            for (int t = 0; t < TT; t += 2) {
-              u32x4 v0, v1;
+          for (int t = 0; t < TT; t += 2) {
+            u32x4 v0, v1;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int j = 4 * t + 2 * i;
-                const uint32_t codes = __builtin_amdgcn_perm(v[j + 1][e / 4] & seen(j + 1), v[j][e / 4] & seen(j), pick);
-                v0[i] = widen_codes<DT, false>(codes, vs[j / 4]);
-                v1[i] = widen_codes<DT, true>(codes, vs[j / 4]);
-              }
-              const u32x4 p = {pw[t][0], pw[t][1], pw[t + 1][0], pw[t + 1][1]};
-              sum0 = mfma16<DT>(v0, p, sum0);
-              sum1 = mfma16<DT>(v1, p, sum1);
+            for (int i = 0; i < 4; ++i) {
+              const int j = 4 * t + 2 * i;
+              const uint32_t codes = __builtin_amdgcn_perm(v[j + 1][e / 4], v[j][e / 4], pick);
+              v0[i] = widen_codes<DT, false>(codes, vs[j / 4]);
+              v1[i] = widen_codes<DT, true>(codes, vs[j / 4]);
             }
-            if (mine) {
-              o[e] = sum0;
-              o[e + 1] = sum1;
-            }
+            const u32x4 p = {pw[t][0], pw[t][1], pw[t + 1][0], pw[t + 1][1]};
+            o[e] = mfma16<DT>(v0, p, o[e]);
+            o[e + 1] = mfma16<DT>(v1, p, o[e + 1]);
           }
-        };
-        if (!apart) {
-          product([](int) { return 0xffffffffu; }, true);
-        } else {
+        }
+        if (special) {
 #pragma unroll 1
-          for (int tok = rc.tok0; tok <= rc.tok1; ++tok) {
-            const Span sp = seen_by(sq, tok, a.causal, a.window);
-            // a scale that is not finite would make zeros of the entries that the token does not see NaN
-            float own[TT];
+          for (int e0 = 0; e0 < K; ++e0) {
+            const int key = k0 + e0;
+            const int page = key < hi ? scalar_load(table, key >> pg.page_shift) : -1;
+            if (page < 0 || page >= pg.num_pages) continue;
+            const int in = key & page_mask;
+            const uint8_t* from = value_head + page * pg.page_stride + static_cast<long long>(in) * D + 4 * g * E;
+            const float scale = value_scale(sh[page * a.scale_page_stride + in / kScaleBlock * 2 + 1] << 8);
+            const bool mine = key >= row_lo && key < row_hi;
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-              own[t] = vs[t];
-              if (k0 + 16 * t + 16 <= sp.lo || k0 + 16 * t >= sp.hi) vs[t] = 1.f;
-            }
-            product([&](int j) {
-              const int key = k0 + 16 * (j / 4) + 4 * g + j % 4;
-              return key >= sp.lo && key < sp.hi ? 0xffffffffu : 0u;
-            }, row_tok == tok);
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int t = 0; t < TT; ++t) vs[t] = own[t];
+              for (int e = 0; e < E; ++e) {  // lane (g, c16) holds element (4 g + r) E + e of its row
+                const uint32_t u = widen_codes<DT, false>(from[r * E + e], scale) & 0xffffu;
+                const float x = DT == DLRM_BF16 ? bf16_lo(u) : f16_lo(u);
+                o[e][r] += mine && not_finite_halves<DT>(u) ? x : 0.f;
+              }
           }
         }
         if constexpr (More) load_values(next);
@@ -639,7 +637,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_q8_kerne
 }
 
 // Where the workgroups of a call would not fill the chip, or histories may be of unequal length, every history is split
-// into parts.
+// into parts, by the rules for the 16-bit cache, but for the rows kernel's: 256 KB of keys are twice the entries (64
+// histories of up to 16k entries of 128: 128 us in 9 parts, 130 in 17).
 Cut cut_call(long long all_rows, long long max_rows, int seqs, int kv_heads, int dim, int causal, int window, int max_q,
              int max_kv) {
   Cut c;
@@ -656,7 +655,7 @@ Cut cut_call(long long all_rows, long long max_rows, int seqs, int kv_heads, int
   const long long units = whole > 0 ? whole : 1;
   const long long held = (all_rows + rows - 1) / rows, busy = held > units ? held : units;  // tiles of all rows
   if (rows == 16) {
-    const long long least = 131072 / dim, fill = 256 / units, finest = (span + 511) / 512, most = 16384 / units;
+    const long long least = 262144 / dim, fill = 256 / units, finest = (span + 511) / 512, most = 16384 / units;
     splits = (span + least - 1) / least;
     if (splits < fill) splits = fill < finest ? fill : finest;
     if (splits > most) splits = most;
