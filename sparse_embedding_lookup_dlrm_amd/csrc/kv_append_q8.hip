@@ -77,12 +77,17 @@ struct BlockTask {
       : a(a_), split(threadIdx.x % Lanes, KEY ? a_.rope.rot : 0, a_.rope.interleaved),
         slot(threadIdx.x % kWave / Lanes % kBlock) {}
 
+  // The new entry of this lane in pass p, counted from the first. A lane without one takes its neighbour's, which
+  // changes no maximum, and stores nothing: a load within a branch would be waited for at its end.
+  __device__ __forceinline__ int entry(const Unit& u, int p) const {
+    const int e = u.first + p * Slots + slot;
+    return (e < u.from ? u.from : e < u.to ? e : u.to - 1) - u.from;
+  }
+
   __device__ __forceinline__ void load(const Unit& u, int head) {
 #pragma unroll
     for (int p = 0; p < Passes; ++p) {
-      const int e = u.first + p * Slots + slot;
-      if (e < u.from || e >= u.to) continue;
-      const char* x = head_at<DT>(KEY ? a.k : a.v, u.token + (e - u.from), head);
+      const char* x = head_at<DT>(KEY ? a.k : a.v, u.token + entry(u, p), head);
 #pragma unroll
       for (int i = 0; i < 2; ++i) raw[p][i] = *reinterpret_cast<const uint4*>(x + split.at[i] * Storage<DT>::bytes);
     }
@@ -102,12 +107,10 @@ struct BlockTask {
     }
 #pragma unroll
     for (int p = 0; p < Passes; ++p) {
-      const int e = u.first + p * Slots + slot;
-      if (e < u.from || e >= u.to) continue;
       widen<DT>(raw[p][0], y[p]);
       widen<DT>(raw[p][1], y[p] + V);
       if constexpr (KEY)
-        norm_turn<DT, D>(y[p], wv, norm, a.eps, cs + (e - u.from) * (a.rope.rot / 2), split, a.rope.interleaved);
+        norm_turn<DT, D>(y[p], wv, norm, a.eps, cs + entry(u, p) * (a.rope.rot / 2), split, a.rope.interleaved);
 #pragma unroll
       for (int i = 0; i < 2 * V; ++i) {
         const float x = fabsf(y[p][i]);
