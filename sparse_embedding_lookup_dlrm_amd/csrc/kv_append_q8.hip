@@ -19,8 +19,8 @@ constexpr int kBlock = DLRM_KV_BLOCK;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kQueryTokens = 4;  // most tokens of a workgroup of the queries
 
-// How a call is cut: workgroups of the queries, `per` tokens to each step; then, for the keys and values, `lanes`
-// workgroups to a sequence that take its blocks in turn, times `parts` that share the heads.
+// How a call is cut: for the keys and values `lanes` workgroups to a sequence that take its blocks in turn, times `parts`
+// that share the heads; then workgroups of the queries, `per` tokens to each step.
 struct AppendGrid {
   long long query_steps, units;  // steps of all workgroups; lanes x sequences x parts
   int query_groups, unit_groups, per, lanes, parts;
@@ -210,21 +210,22 @@ __device__ __forceinline__ void append_unit(const NormRopeArgs& a, const AppendG
 template <int DT, int D>
 __global__ __launch_bounds__(kThreads) void kv_append_q8_kernel(NormRopeArgs a, AppendGrid grid) {
   __shared__ float2 cs[kBlock * D / 2];
-  if (blockIdx.x < grid.query_groups) {
-    for (long long step = blockIdx.x; step < grid.query_steps; step += grid.query_groups) {
-      const long long t0 = step * grid.per;
-      const int count = static_cast<int>(a.n - t0 < grid.per ? a.n - t0 : grid.per);
-      Walk<DT, D, true> q(a, a.q, a.q_heads, a.w_q, t0, count, 0);
-      __syncthreads();  // the angles of the tokens before are no longer read
-      angles(a.rope, t0, count, cs);
+  // keys and values first: their workgroups take longer
+  if (blockIdx.x < grid.unit_groups) {
+    for (long long unit = blockIdx.x; unit < grid.units; unit += grid.unit_groups) {
       __syncthreads();
-      q.run(a, cs, a.q_out, nullptr);
+      append_unit<DT, D>(a, grid, unit, cs);
     }
     return;
   }
-  for (long long unit = blockIdx.x - grid.query_groups; unit < grid.units; unit += grid.unit_groups) {
+  for (long long step = blockIdx.x - grid.unit_groups; step < grid.query_steps; step += grid.query_groups) {
+    const long long t0 = step * grid.per;
+    const int count = static_cast<int>(a.n - t0 < grid.per ? a.n - t0 : grid.per);
+    Walk<DT, D, true> q(a, a.q, a.q_heads, a.w_q, t0, count, 0);
+    __syncthreads();  // the angles of the tokens before are no longer read
+    angles(a.rope, t0, count, cs);
     __syncthreads();
-    append_unit<DT, D>(a, grid, unit, cs);
+    q.run(a, cs, a.q_out, nullptr);
   }
 }
 
@@ -238,8 +239,9 @@ AppendGrid append_grid(const NormRopeArgs& a) {
   g.per = static_cast<int>(per < 1 ? 1 : per > kQueryTokens ? kQueryTokens : per);
   g.query_steps = a.q_heads > 0 ? (a.n + g.per - 1) / g.per : 0;
   g.query_groups = static_cast<int>(g.query_steps < kMostGroups ? g.query_steps : kMostGroups);
-  // blocks that a sequence can have, four times what they have on average, and 1024 workgroups in all
-  const long long most = a.n / kBlock + 2, average = 4 * (a.n / (kBlock * seqs) + 1), fill = 1024 / seqs;
+  // Workgroups of a sequence: twice the blocks that sequences have on average, more where there are few, and no more
+  // than blocks it can have. Those that find none cost as well: chunks of 12 users 71 us with 4 times as many, 88 with 8.
+  const long long most = a.n / kBlock + 2, average = 2 * (a.n / (kBlock * seqs) + 1), fill = 512 / seqs;
   long long lanes = average > fill ? average : fill;
   if (lanes > most) lanes = most;
   g.lanes = static_cast<int>(lanes < 1 ? 1 : lanes);
