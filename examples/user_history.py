@@ -7,7 +7,8 @@ and rotated by place and time) and the values go to a paged cache, so that a new
 and one attention over the user's history, not the history again. The last event's attention output is the
 user's vector, a feature of the pairwise interaction like a pooled bag. Candidates are ranked by letting each
 attend to the whole history without being stored. Training the per-head norms takes the backward of norm and
-rotation.
+rotation. The last part keeps the cache in 8 bits, and hands out its pages on the GPU: no list of pages and no page
+table is made on the host.
 """
 from __future__ import annotations
 
@@ -61,6 +62,38 @@ class HistoryCache:
         return (offsets.to(dev), lens.to(dev), table.to(dev)), most
 
 
+class HistoryCache8:
+    """Keys and values of many users in 8 bits, their pages handed out and taken back on the GPU, and the hour of each
+    event beside them."""
+
+    def __init__(self, users: int, pages: int, kv_heads: int, page: int, dim: int, max_events: int, device):
+        self.page, self.max_events = page, max_events
+        codes = lambda: torch.zeros((pages, kv_heads, page, dim), dtype=torch.float8_e4m3fn, device=device)
+        self.k, self.v = codes(), codes()
+        self.scales = torch.zeros((pages, kv_heads, page // ops.KV_BLOCK, 2), dtype=torch.uint8, device=device)
+        self.hours = torch.zeros(pages * page, dtype=torch.int32, device=device)
+        i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)
+        self.held, self.tables, self.status = i32(users), i32(users, -(-max_events // page)), i32(1)
+        self.free = torch.arange(pages, dtype=torch.int32, device=device)
+        self.count = torch.full((1,), pages, dtype=torch.int32, device=device)
+
+    def state(self):
+        return self.held, self.tables, self.free, self.count, self.page
+
+    def grow(self, users: torch.Tensor, new: torch.Tensor, events: int):
+        """Room for new[i] events of users[i], `events` in all; returns (q_offsets, kv_lens, page_table), slots and places.
+        Without room nothing changes, no event has a slot, and status says so."""
+        *call, slots, places = ops.pages_assign(new, *self.state(), events, users=users, status=self.status)
+        return call, slots, places
+
+    def drop(self, users: torch.Tensor, keep=None):
+        """Histories cut to their first keep[i] events, or dropped."""
+        ops.pages_release(*self.state(), users=users, keep=keep, status=self.status)
+
+    def parts(self):
+        return self.k, self.v, self.scales
+
+
 class HistoryEncoder:
     """One attention layer over item embeddings: a joint projection, per-head norms, and a rotation whose first
     pairs turn by the event's place in the history and whose last ones by its hour."""
@@ -107,6 +140,17 @@ class HistoryEncoder:
         q, _ = ops.qk_norm_rope(q, k, torch.stack([place, hours.to(torch.int32)]), self.inv_freq, self.w_q, self.w_k,
                                 sections=self.sections)
         return ops.paged_attn(q, cache.k, cache.v, offsets, lens, table, causal=False, **most).flatten(1)
+
+    def step8(self, cache: HistoryCache8, users, ids, hours, new, most_new: int):
+        """step over an 8-bit cache; users and new are int32 tensors, most_new the largest of new."""
+        call, slots, places = cache.grow(users, new, ids.shape[0])
+        stored = slots >= 0
+        cache.hours.scatter_(0, slots.clamp(min=0), torch.where(stored, hours.to(torch.int32), cache.hours[slots.clamp(min=0)]))
+        q, k, v = self.project(ids)
+        q = ops.kv_append_q8(k, v, *cache.parts(), *call, q=q, status=cache.status,
+                             **self.turn(torch.stack([places, hours.to(torch.int32)])))
+        return ops.paged_attn_q8(q, *cache.parts(), *call, max_q=most_new, max_kv=cache.max_events,
+                                 status=cache.status).flatten(1)
 
     def train_norms(self, ids, place, hours, d_q, d_k, lr: float):
         """One SGD step on the norm weights from the gradients of the normed and rotated queries and keys;
@@ -159,6 +203,17 @@ def main() -> None:
     d_k = torch.randn((n, 2, 64), generator=g).to(dev, torch.bfloat16)
     g_q, _ = enc.train_norms(ids, torch.arange(n, device=dev), torch.arange(n, device=dev) * 7, d_q, d_k, 1e-3)
     print("norm weights moved by", float((enc.w_q - 1).abs().max()), "query gradients", tuple(g_q.shape))
+
+    # the same histories in 8 bits: filled, one event more, and the first user gone again
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+    cache8 = HistoryCache8(users, pages=256, kv_heads=2, page=16, dim=64, max_events=512, device=dev)
+    everyone = i32(list(range(users)))
+    ids = torch.randint(0, 10_000, (sum(past),), generator=g, dtype=torch.int32).to(dev)
+    hours = torch.cat([torch.arange(n) * 7 for n in past]).to(dev)
+    enc.step8(cache8, everyone, ids, hours, i32(past), max(past))
+    user8 = enc.step8(cache8, everyone, ids[:users], now, i32([1] * users), 1)
+    cache8.drop(i32([0]))
+    print("8-bit cache", tuple(user8.shape), "held", cache8.held.tolist(), "free pages", int(cache8.count))
 
 
 if __name__ == "__main__":
