@@ -278,3 +278,37 @@ def test_another_stream_and_graph_replays():
         got = [x.clone() for x in captured]
         for a, b in zip(got, ops.paged_attn_q8(*args, want_lse=True, max_q=30, max_kv=2000)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("max_q,max_kv", [(None, 5000), (600, 5000), (100, 5000), (2000, 600), (600, 1)])
+@pytest.mark.parametrize("D,window", [(64, 0), (128, 0), (32, 900)])
+def test_few_rows_over_long_histories_beside_many(D, window, max_q, max_kv):
+    """Sequences of few rows are in parts where others are not; with hints of all sizes. One has no tokens, one no
+    entries, one fewer entries than tokens."""
+    h = History8([600, 3, 40, 0, 5, 33], [700, 5000, 3000, 4000, 0, 20], 8, 2, D, 16, "bf16", seed=D)
+    check(h, window=window, max_q=max_q, max_kv=max_kv)
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_more_sequences_than_lanes(D):
+    """Chunks of 70 sequences, more than a wave orders by length."""
+    rng = np.random.default_rng(D)
+    q = rng.integers(0, 30, 70)
+    check(History8(q, q + rng.integers(0, 300, 70), 4, 2, D, 16, "f16", seed=3), max_q=30, max_kv=330)
+
+
+@pytest.mark.parametrize("m,max_q", [(3, 3), (3, 1 << 24), (40, 40), (40, 1 << 24)])
+def test_entries_counted_up_to_31_bits(m, max_q):
+    """The window lies in the last two of 32765 pages of 65536 entries; a hint of many new tokens makes
+    parts that would end past 31 bits."""
+    page, width = 65536, 32765
+    h = History8([m], [2 * page - 5], 2, 1, 32, page, "bf16", seed=51)
+    q, k, v, scales, offsets, _, _ = h.args()
+    table = torch.full((1, width), -1, dtype=torch.int32)
+    table[0, -2:] = h.page_table[0, :2]
+    lens = torch.tensor([width * page - 5], dtype=torch.int32).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = ops.paged_attn_q8(q, k, v, scales, offsets, lens, table.cuda(), causal=True, window=70000, want_lse=True,
+                            status=status, max_q=max_q)
+    assert status.item() == 0
+    check(h, window=70000, got=got)
