@@ -69,9 +69,9 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4& a, const u32x4& b, const f
                                                   0);
 }
 
-// Tiles of the tile kernels lie in LDS in rows of D 16-bit elements, D / 8 pieces of 16 bytes; piece c of entry r lies at
-// place c ^ swizzle(r).
-// Keys are read as rows (32 entries, the same piece): neighbours differ in every place bit.
+// Tiles of the tile kernels lie in LDS in rows of D 16-bit elements, D / 8 pieces of 16 bytes; piece c of entry r
+// lies at place c ^ swizzle(r). Keys are read as rows (32 entries, the same piece): neighbours differ in every place
+// bit.
 template <int D>
 __device__ __forceinline__ int key_swizzle(int r) {
   return D == 32 ? r >> 1 & 3 : D == 64 ? r & 7 : r & 15;
@@ -308,7 +308,8 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, Cut cut
       if (row >= rows) continue;  // with Slots > 1 there is one row, and no thread leaves it
       const int tok = row / a.q_heads, in_head = tok * group + (row - tok * a.q_heads) % group;
       const int row0 = in_head / tile_rows * tile_rows, in_all = sq.tokens * group;
-      const Reach rc(sq, row0, in_all - row0 > tile_rows ? row0 + tile_rows : in_all, group, a.causal, a.window, cut, may);
+      const Reach rc(sq, row0, in_all - row0 > tile_rows ? row0 + tile_rows : in_all, group, a.causal, a.window, cut,
+                     may);
       if (rc.parts == 1) continue;
       const long long to = static_cast<long long>(sq.first) * a.q_heads + row;
       const float2* ml = cut.ml + to * cut.most();
@@ -358,8 +359,8 @@ template <int DT, int D, int Slots>
 void join(const AttnArgs& a, const Cut& cut, int tile_rows, hipStream_t s) {
   constexpr int Rows = kThreads / (D / 8 * Slots);
   const long long rows = static_cast<long long>(a.max_q) * a.q_heads, groups = (rows + Rows - 1) / Rows;
-  // where only sequences of few rows are in parts, the workgroups of all others would come for nothing (16384 of them: 25
-  // us, 1024: 6)
+  // where only sequences of few rows are in parts, the workgroups of all others would come for nothing (16384 of
+  // them: 25 us, 1024: 6)
   const long long most = cut.splits > 1 ? 65535 : 256;
   const unsigned x = static_cast<unsigned>(groups < 1 ? 1 : groups < most ? groups : most);
   const unsigned y = static_cast<unsigned>(a.paged.seqs < 65535 / 8 ? a.paged.seqs : 65535 / 8);

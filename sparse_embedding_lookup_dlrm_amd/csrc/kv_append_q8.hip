@@ -2,14 +2,14 @@
 // rotation of the queries in the same launch.
 //
 // A block of 16 entries of a head has one power of two, 2^(b - 127), for its keys and one for its values. With A the
-// largest finite |x| of the new entries in it, b is the smallest for which A <= 448 x 2^(b - 127), 448 = 1.75 x 2^8 being
-// the largest code: the biased exponent of A less 8, and one more if its significand is above 1.75. A block that holds
-// older entries keeps its b where that is larger; else their codes are rounded again to the new one. The scale is a power
-// of two, so that this second rounding only shortens codes that become subnormal: a code of k significant bits
-// stays as it is as long as it keeps them.
+// largest finite |x| of the new entries in it, b is the smallest for which A <= 448 x 2^(b - 127), 448 = 1.75 x 2^8
+// being the largest code: the biased exponent of A less 8, and one more if its significand is above 1.75. A block
+// that holds older entries keeps its b where that is larger; else their codes are rounded again to the new one. The
+// scale is a power of two, so that this second rounding only shortens codes that become subnormal: a code of k
+// significant bits stays as it is as long as it keeps them.
 //
-// A wave takes the block of one head: 16 entries in registers, one maximum, and the codes. Blocks that new entries touch
-// are known on the device only, so each sequence has a fixed number of workgroups that take its blocks in turn.
+// A wave takes the block of one head: 16 entries in registers, one maximum, and the codes. Blocks that new entries
+// touch are known on the device only, so each sequence has a fixed number of workgroups that take its blocks in turn.
 //
 // Bound by memory: 11937 tokens of 12 users, 32 + 2 x 8 heads of 128 fp16: 62 us for 269 MB, 4.3 TB/s (the queries, 195
 // MB, would take 36 at the rate of the 16-bit append; keys and values wait for their blocks' maxima between load and
@@ -23,8 +23,8 @@ constexpr int kBlock = DLRM_KV_BLOCK;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kQueryTokens = 4;  // most tokens of a workgroup of the queries
 
-// How a call is cut: for the keys and values `lanes` workgroups to a sequence that take its blocks in turn, times `parts`
-// that share the heads; then workgroups of the queries, `per` tokens to each step.
+// How a call is cut: for the keys and values `lanes` workgroups to a sequence that take its blocks in turn, times
+// `parts` that share the heads; then workgroups of the queries, `per` tokens to each step.
 struct AppendGrid {
   long long query_steps, units;  // steps of all workgroups; lanes x sequences x parts
   int query_groups, unit_groups, per, lanes, parts;
@@ -32,7 +32,8 @@ struct AppendGrid {
 
 // Eight fp32 values as codes, and back. The conversion rounds to nearest even, what is not finite to NaN.
 __device__ __forceinline__ uint2 to_codes(const float* x) {
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false), hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], 0, false);
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], 0, false);
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true);
   hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], hi, true);
   return make_uint2(lo, hi);

@@ -9,13 +9,18 @@ namespace dlrm {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Rows kernel: 16 rows of one head to a workgroup, as for the 16-bit cache: the four waves take the tiles of the history
-// in turn, a wave's next tile is on the way from global memory to registers while one is worked on, and the waves join
-// their (m, l, O) through LDS at the end. Scores are formed transposed, S^T = K Q^T, so that the weights are the second
-// product's right operand where they lie: lane (g, c16) holds entries 4 g .. 4 g + 3 of each block of 16.
-// The order of the elements in a score's sum is free: a lane takes 16 neighbouring codes of a key, which serve two
-// steps of the product, and the queries are read to fit. Of the values it takes D / 16 neighbouring codes of its
+// Rows kernel: 16 rows of one head to a workgroup, as for the 16-bit cache: the four waves take the tiles of the
+// history in turn, a wave's next tile is on the way from global memory to registers while one is worked on, and the
+// waves join their (m, l, O) through LDS at the end. Scores are formed transposed, S^T = K Q^T, so that the weights
+// are the second product's right operand where they lie: lane (g, c16) holds entries 4 g .. 4 g + 3 of each block of
+// 16. The order of the elements in a score's sum is free: a lane takes 16 neighbouring codes of a key, which serve
+// two steps of the product, and the queries are read to fit. Of the values it takes D / 16 neighbouring codes of its
 // entries; a byte permutation of two entries' words gives the pairs of two elements, one widening each.
+//
+// Bound by memory: 64 histories of up to 16k entries, 32 / 8 heads of 128, 625 MB: 121 us, 5.2 TB/s (16-bit cache
+// 214). A third wave on each SIMD changes nothing (152 registers are room for it), tiles of 64 entries spill (205 us
+// of the whole call instead of 130); vector units are busy 30 % of the time, matrix units 8 %. A second form of the
+// product, token by token for NaN that only some rows see, took 22 registers more (133 us).
 // ---------------------------------------------------------------------------
 template <int DT, int D>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_q8_kernel(AttnArgs a, Cut cut) {
@@ -190,8 +195,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_q8_kerne
           pw[t][1] = pack2<DT>(p[2], p[3]);
         }
 
-        // Entries that no row sees are zero, whatever they and their scale hold. What only some rows see and is NaN (or
-        // a value that fp16 does not hold) counts as zero in the product, and is added after it to the rows that see it.
+        // Entries that no row sees are zero, whatever they and their scale hold. What only some rows see and is NaN
+        // (or a value that fp16 does not hold) counts as zero in the product, and is added after it to the rows that
+        // see it.
         float vs[TT];
 #pragma unroll
         for (int t = 0; t < TT; ++t) vs[t] = value_scale(two[t]);
@@ -300,13 +306,23 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_q8_kerne
 }
 
 // ---------------------------------------------------------------------------
-// Tile kernel: 128 rows of one head to a workgroup, 32 to a wave, tiles of 64 entries in LDS that every wave reads all
-// of. Products are 32x32x16: the score of row lane % 32 with entries 8 i + 4 h + j (h = lane / 32, i, j = 0 .. 3) lies in
-// one lane, which again is the second product's right operand as it stands; its left operand V^T is read by the transposing
-// LDS load: sixteen lanes take a block of 4 entries x 16 elements and get one element of the 4 entries each.
+// Tile kernel: 128 rows of one head to a workgroup, 32 to a wave, tiles of 64 entries in LDS that every wave reads
+// all of. Products are 32x32x16: the score of row lane % 32 with entries 8 i + 4 h + j (h = lane / 32, i, j = 0 .. 3)
+// lies in one lane, which again is the second product's right operand as it stands; its left operand V^T is read by
+// the transposing LDS load: sixteen lanes take a block of 4 entries x 16 elements and get one element of the 4
+// entries each.
 //
-// Codes are widened on their way to LDS, once for the workgroup and not by each of its waves: a wave brings 16 entries of
-// a tile, loaded while the tile before is worked on, in pieces of 8 codes that become 16 bytes.
+// Codes are widened on their way to LDS, once for the workgroup and not by each of its waves: a wave brings 16
+// entries of a tile, loaded while the tile before is worked on, in pieces of 8 codes that become 16 bytes.
+//
+// 4 sequences of up to 2048 tokens over up to 8192, 32 / 8 heads of 128: 340-345 us, 853-866 TFLOP/s (16-bit cache,
+// same inputs: 447), at 1.94 GHz, to which the clock falls under this load. Matrix units are busy 41 % of the time
+// that a CU has work, vector units 52 %; a CU has work 80 % of the time. Left out: widening 13 us (of 411 then), the
+// pieces to LDS 40, these and the loads 80. Tiles of 128 entries and 256 rows to a workgroup: 430-468 us, for jobs
+// are fewer and longer; the jobs of all sequences in order of length: as long, and 5 us more for short calls. Heads
+// of 256: a wave holds all of O, one to a SIMD, and works on 32 entries at once with 4 pieces read ahead: 102-106 us
+// for 12 sequences of up to 513 tokens with a window of 1024; with 8 pieces ahead, whose registers spill, 127-133,
+// with two waves for the same rows, each with half of O, 120-157 (16-bit cache, which has no codes to hold, 86).
 // ---------------------------------------------------------------------------
 template <int DT, int D>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_q8_kernel(AttnArgs a, Cut cut) {
@@ -350,7 +366,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_q8_kerne
       const int w0 = row0 + 32 * wave, w1 = w0 + 32 < row_end ? w0 + 32 : row_end;
       int w_lo = 0, w_hi = 0, w_all_lo = 0, w_all_hi = 0;
       if (w0 < w1) {
-        const Span s0 = seen_by(sq, w0 / group, a.causal, a.window), s1 = seen_by(sq, (w1 - 1) / group, a.causal, a.window);
+        const Span s0 = seen_by(sq, w0 / group, a.causal, a.window);
+        const Span s1 = seen_by(sq, (w1 - 1) / group, a.causal, a.window);
         w_lo = s0.lo;
         w_hi = s1.hi;
         w_all_lo = s1.lo;
@@ -396,10 +413,11 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_q8_kerne
         good64 = __ballot(good);
         pages_next = look_up(k0 + Ahead * K < hi ? k0 + Ahead * K : k0);
         const int key = k0 + 16 * lane, known = (key < hi ? key : hi - 1) & page_mask;
-        scales = *reinterpret_cast<const uint16_t*>(sh + (good ? pages : 0) * a.scale_page_stride + known / kScaleBlock * 2);
+        scales = *reinterpret_cast<const uint16_t*>(sh + (good ? pages : 0) * a.scale_page_stride +
+                                                    known / kScaleBlock * 2);
       };
-      // This wave's 16 entries of the tile at k0, block kWaves at + wave of the pages at hand: a contiguous piece of the
-      // cache. Past the end and in place of a bad page other entries are read, and masked.
+      // This wave's 16 entries of the tile at k0, block kWaves at + wave of the pages at hand: a contiguous piece of
+      // the cache. Past the end and in place of a bad page other entries are read, and masked.
       uint2 raw[2][Loads];
       const auto fetch_tile = [&](int k0) {
         const int key = k0 + 16 * wave, known = key < hi ? key : hi - 1, block = kWaves * at + wave;
@@ -417,8 +435,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_q8_kerne
         put_scale[0] = key_scale(two);
         put_scale[1] = value_scale(two);
       };
-      // Piece n of what the registers hold goes to LDS. Sixteen lanes fill places of all banks (with 16 codes a lane it is
-      // every other place of a row of values, 18 % of the time in conflicts).
+      // Piece n of what the registers hold goes to LDS. Sixteen lanes fill places of all banks (with 16 codes a lane
+      // it is every other place of a row of values, 18 % of the time in conflicts).
       const auto put_one = [&](int n, int buf) {
         const int value = n / Loads, i = n % Loads, r = (i * kWave + lane) / P, piece = lane % P;
         uint16_t* rows16 = (value ? lds_v[buf] : lds_k[buf]) + (16 * wave + r) * D;
@@ -620,7 +638,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_q8_kerne
             const float x0 = o[i][4 * q] * inv, x1 = o[i][4 * q + 1] * inv, x2 = o[i][4 * q + 2] * inv,
                         x3 = o[i][4 * q + 3] * inv;
             if (part)
-              *reinterpret_cast<float4*>(cut.o + (split * a.n * a.q_heads + to) * D + at_d) = make_float4(x0, x1, x2, x3);
+              *reinterpret_cast<float4*>(cut.o + (split * a.n * a.q_heads + to) * D + at_d) =
+                  make_float4(x0, x1, x2, x3);
             else
               *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to * D + at_d) =
                   make_uint2(pack2<DT>(x0, x1), pack2<DT>(x2, x3));

@@ -9,6 +9,9 @@
 // the two sums, and whether a user appears twice, which it finds by letting every sequence write its number
 // into its user's length and look whether it is still there. The second kernel (fill) writes what is long: page
 // tables, slots and positions, with a workgroup for each sequence and part.
+//
+// Both kernels wait for a few loads in a row and a launch: one event each for 64 users, 1024 pages to a row, 3.5 + 3.9
+// us; chunks of 300 users, 300k tokens (4 MB) 4.9 + 6.2; 256 histories of up to 65536 entries dropped 4.0 + 4.3.
 #include "history_device.h"
 
 namespace dlrm {
@@ -238,7 +241,9 @@ dim3 fill_grid(long long rows, long long longest) {
 }
 
 // Threads of the plan: one to a sequence.
-int plan_threads(int seqs) { return seqs >= kPlanThreads ? kPlanThreads : seqs <= kWave ? kWave : (seqs + kWave - 1) & ~(kWave - 1); }
+int plan_threads(int seqs) {
+  return seqs >= kPlanThreads ? kPlanThreads : seqs <= kWave ? kWave : (seqs + kWave - 1) & ~(kWave - 1);
+}
 
 }  // namespace
 
@@ -247,7 +252,8 @@ size_t pages_workspace(int seqs) { return (sizeof(int32_t) * (2 + 2 * static_cas
 hipError_t launch_pages_assign(const PagesArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(assign_plan_kernel, dim3(1), dim3(plan_threads(a.seqs)), 0, s, a);
   const long long longest = a.out_width > a.n ? a.out_width : a.n;
-  hipLaunchKernelGGL(assign_fill_kernel, fill_grid(static_cast<long long>(a.seqs) + 1, longest), dim3(kFillThreads), 0, s, a);
+  const dim3 grid = fill_grid(static_cast<long long>(a.seqs) + 1, longest);
+  hipLaunchKernelGGL(assign_fill_kernel, grid, dim3(kFillThreads), 0, s, a);
   return hipGetLastError();
 }
 
