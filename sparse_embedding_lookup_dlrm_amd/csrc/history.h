@@ -1,5 +1,6 @@
 // Host-side interface between the C ABI of dlrm_history.h (history_api.cpp) and its kernel
-// launchers (norm_rope.hip, paged_attn.hip, pages.hip). Plain C++: no device code.
+// launchers (norm_rope.hip, kv_append_q8.hip, paged_attn.hip, paged_attn_q8.hip, pages.hip).
+// Plain C++: no device code.
 #pragma once
 
 #include <hip/hip_runtime_api.h>

@@ -257,3 +257,20 @@ def test_one_long_history():
     pages = torch.where(e < 16, torch.full_like(e, 3), 70_000 - (e // 16))
     assert off.tolist() == [0, N] and torch.equal(places[:N].long(), e) and torch.equal(slots[:N], pages * 16 + e % 16)
     assert (slots[N:] == -1).all() and (places[N:] == -1).all()
+
+
+@pytest.mark.parametrize("a,b", [(5, 2900), (5, 5 + 1024), (0, 2999), (63, 64), (1023, 1024)])
+def test_a_user_twice_far_apart(a, b):
+    """In sequences that different lanes, waves and turns of the deciding workgroup look at."""
+    users = 3100
+    st = State(users, 4, 16, [u % 30 for u in range(users)], seed=9, spare=6000)
+    who = list(range(50, 3050))
+    assert st.assign([1] * 3000, who)[0] == 0
+    st.held = st.d[0].tolist()
+    st.tables, st.count = st.d[1].tolist(), st.d[3].item()
+    who[b] = who[a]
+    before = [x.clone() for x in st.d]
+    assert st.assign([1] * 3000, who)[0] == ops.STATUS_BAD_USER
+    assert st.release(who) == ops.STATUS_BAD_USER
+    for x, y in zip(before, st.d):
+        assert torch.equal(x, y)
