@@ -181,6 +181,51 @@ int check_pages(int32_t seqs, int32_t users, const int32_t* who, const int32_t* 
   return DLRM_OK;
 }
 
+// A buffer of a call: its address, its bytes, and whether the call writes it.
+struct Buffer {
+  const void* at;
+  uint64_t bytes;
+  bool written;
+};
+
+// Whether no buffer that is written shares a byte with another one.
+bool apart(const Buffer* b, int count) {
+  for (int i = 0; i < count; ++i)
+    for (int j = i + 1; j < count; ++j) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(b[i].at), y = reinterpret_cast<uintptr_t>(b[j].at);
+      if (!x || !y || !(b[i].written || b[j].written)) continue;
+      if (x <= y ? y - x < b[i].bytes && b[j].bytes > 0 : x - y < b[j].bytes && b[i].bytes > 0) return false;
+    }
+  return true;
+}
+
+// The buffers of an assignment or release: the kernels read lengths and users again after they wrote others, so
+// nothing but the two lengths and the two counts may be one.
+int check_page_buffers(const PagesArgs& a, bool assign, size_t ws_bytes) {
+  const uint64_t seqs = a.seqs, users = a.users, width = a.table_width;
+  const uint64_t rows = users > 1 ? users - 1 : 0, step = users > 1 ? a.table_stride : 0;
+  uint64_t table_bytes;
+  if (__builtin_mul_overflow(rows, step, &table_bytes) || table_bytes > (uint64_t(1) << 60)) return DLRM_E_INVAL;
+  table_bytes = users > 0 ? 4 * (table_bytes + width) : 0;
+  const bool held_apart = a.held != a.held_out, count_apart = a.count != a.count_out;
+  const Buffer all[] = {{a.lens, 4 * seqs, false},
+                        {a.who, 4 * seqs, false},
+                        {held_apart ? a.held : nullptr, 4 * users, false},
+                        {a.held_out, 4 * users, true},
+                        {count_apart ? a.count : nullptr, 4, false},
+                        {a.count_out, 4, true},
+                        {a.tables, table_bytes, assign},
+                        {a.free_pages, 4 * static_cast<uint64_t>(a.num_pages), !assign},
+                        {a.workspace, ws_bytes, true},
+                        {a.status, 4, true},
+                        {a.q_offsets, 4 * (seqs + 1), true},
+                        {a.kv_lens, 4 * seqs, true},
+                        {a.page_table, 4 * seqs * static_cast<uint64_t>(a.out_width), true},
+                        {a.slots, 8 * static_cast<uint64_t>(a.n), true},
+                        {a.positions, 4 * static_cast<uint64_t>(a.n), true}};
+  return apart(all, sizeof(all) / sizeof(all[0])) ? DLRM_OK : DLRM_E_INVAL;
+}
+
 }  // namespace
 
 extern "C" {
@@ -388,6 +433,7 @@ int dlrm_pages_assign(int64_t n, int32_t seqs, int32_t users, const int32_t* new
   a.tables = tables; a.free_pages = const_cast<int32_t*>(free_pages); a.held_out = held_out; a.count_out = count_out;
   a.q_offsets = q_offsets; a.kv_lens = kv_lens; a.page_table = page_table; a.positions = positions; a.slots = slots;
   a.workspace = workspace; a.status = status;
+  TRY(check_page_buffers(a, true, pages_workspace(seqs)));
   return from_hip(launch_pages_assign(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -405,6 +451,7 @@ int dlrm_pages_release(int32_t seqs, int32_t users, const int32_t* keep, const i
   a.lens = keep; a.who = who; a.held = held; a.count = free_count;
   a.tables = const_cast<int32_t*>(tables); a.free_pages = free_pages; a.held_out = held_out; a.count_out = count_out;
   a.workspace = workspace; a.status = status;
+  TRY(check_page_buffers(a, false, pages_workspace(seqs)));
   return from_hip(launch_pages_release(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -274,3 +274,22 @@ def test_a_user_twice_far_apart(a, b):
     assert st.release(who) == ops.STATUS_BAD_USER
     for x, y in zip(before, st.d):
         assert torch.equal(x, y)
+
+
+def test_lengths_that_are_the_state_are_refused():
+    """All entries kept, and every history doubled, by the tensor of the lengths themselves: refused, nothing changes; a
+    copy does it."""
+    st = State(5, 9, 16, [0, 16, 17, 3, 40], seed=1)
+    before = [x.clone() for x in st.d]
+    with pytest.raises(ops.DlrmError):
+        ops.pages_release(*st.d, 16, keep=st.d[0])
+    with pytest.raises(ops.DlrmError):
+        ops.pages_assign(st.d[0], *st.d, 16, 200)
+    with pytest.raises(ops.DlrmError):
+        ops.pages_release(*st.d, 16, users=st.d[0][:1])
+    for a, b in zip(before, st.d):
+        assert torch.equal(a, b)
+    assert st.release(None, st.held) == 0
+    bits, state = st.assign(st.held, None)
+    assert bits == 0
+    st.same(*state[:2], count=state[2])

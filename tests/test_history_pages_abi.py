@@ -95,3 +95,47 @@ def test_oracle_by_hand():
     assert slots == [42, 43, 44, 45, 46, 47] + list(range(16, 25)) + [48, 49, 50, -1, -1]
     assert places == list(range(10, 25)) + [0, 1, 2, -1, -1]
     assert ho.pages_release([1, 2], [16, 0], held, tables, [0, 3, 1, 9, 9], 1, 16) == (0, [5, 16, 0], [0, 1, 3, 9, 9], 3)
+
+
+# Fake buffers far apart, and where each begins in them. Read by the call: new lengths or lengths to keep, users.
+STEP = 1 << 24
+PLACES = {name: A + i * STEP for i, name in enumerate(["new", "keep", "who", "held", "held_out", "tables", "free", "count", "count_out", "off",
+                                                        "lens", "table", "slots", "places", "ws", "status"])}
+IN_PLACE = dict(held_out=PLACES["held"], count_out=PLACES["count"])
+
+
+def _at(names):
+    return {k: PLACES[k] for k in names}
+
+
+ASSIGN = _at([k for k in PLACES if k != "keep"])
+RELEASE = _at(["keep", "who", "held", "held_out", "tables", "free", "count", "count_out", "ws", "status"])
+
+
+@pytest.mark.parametrize("a,b", [("new", "held"), ("who", "held"), ("new", "lens"), ("new", "off"), ("who", "table"), ("who", "slots"),
+                                 ("new", "places"), ("held", "lens"), ("held", "ws"), ("count", "status"), ("free", "tables"), ("off", "lens"),
+                                 ("count", "held"), ("new", "status"), ("tables", "table"), ("slots", "places")])
+def test_assignment_refuses_buffers_that_overlap(lib, a, b):
+    """Lengths are read again after others were written: new_lens that is the buffer of held would become something else on
+    the way. In place, beside, and with the last bytes only."""
+    size = dict(held=20, tables=4 * (4 * 8 + 8), free=40, slots=32, places=16, lens=8, off=12, count=4, table=64, status=4, ws=256)
+    for to in {PLACES[b], PLACES[b] + size[b] - (8 if "slots" in (a, b) else 4)}:
+        if a != "ws" and to % (8 if a == "slots" else 4) == 0:
+            assert _assign(lib, **{**ASSIGN, **IN_PLACE, a: to}, ws_bytes=256) == E_INVAL, (a, b)
+
+
+@pytest.mark.parametrize("a,b", [("keep", "held"), ("who", "held"), ("keep", "free"), ("who", "count"), ("held", "free"), ("tables", "free"), ("keep", "ws"),
+                                 ("who", "status")])
+def test_release_refuses_buffers_that_overlap(lib, a, b):
+    """keep that is the buffer of held (all entries kept) would be read as a sequence's number, and pages before the row."""
+    size = dict(held=20, free=40, count=4, status=4, ws=256)
+    for to in {PLACES[b], PLACES[b] + size[b] - 4}:
+        assert _release(lib, **{**RELEASE, **IN_PLACE, a: to}, ws_bytes=256) == E_INVAL, (a, b)
+    other = {"held": "held_out", "count": "count_out"}.get(b)
+    if other:
+        assert _release(lib, **{**RELEASE, a: PLACES[other]}, ws_bytes=256) == E_INVAL, (a, b)
+
+
+def test_lengths_and_counts_that_overlap_in_part(lib):
+    for kw in (dict(held_out=PLACES["held"] + 4, count_out=PLACES["count"] + STEP // 2), dict(held_out=PLACES["held"] - 16)):
+        assert _assign(lib, **{**ASSIGN, **kw}) == E_INVAL and _release(lib, **{**RELEASE, **kw}) == E_INVAL, kw
