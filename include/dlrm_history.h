@@ -230,10 +230,10 @@ int dlrm_paged_attn_q8(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_head
  * Calls that share a state are ordered by the caller. who is int32 [seqs], the user of each
  * sequence, or NULL: sequence s is user s. held_out and count_out take the lengths of the call's
  * users and the count after the call; with held and free_count themselves the state is updated in
- * place. In other buffers they leave the state as it was, but for places in tables and free_pages
- * that mean nothing then, so that a step may be planned and dropped. No two buffers of a call may
- * overlap where the call writes one of them, but for held with held_out and free_count with
- * count_out, which may each be the same buffer (DLRM_E_INVAL).
+ * place. In other buffers, both of them (DLRM_E_INVAL if one is the state's own), they leave the
+ * state as it was, but for places in tables and free_pages that mean nothing then, so that a step
+ * may be planned and dropped. No other two buffers of a call may overlap where the call writes one
+ * of them (DLRM_E_INVAL).
  */
 
 /* Workspace of dlrm_pages_assign and dlrm_pages_release. */

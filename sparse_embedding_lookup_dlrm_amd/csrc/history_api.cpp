@@ -178,6 +178,8 @@ int check_pages(int32_t seqs, int32_t users, const int32_t* who, const int32_t* 
     return DLRM_E_ALIGN;
   if (ws_bytes < pages_workspace(seqs)) return DLRM_E_WORKSPACE;
   if (!workspace) return DLRM_E_INVAL;
+  // lengths in place and the count beside it, or the other way round, would be half a step
+  if (users > 0 && (held == held_out) != (count == count_out)) return DLRM_E_INVAL;
   return DLRM_OK;
 }
 

@@ -999,6 +999,10 @@ def _pages_args(held, tables, free_pages, free_count, lens, name, users, S, held
     """Checks the state of pages and the sequences of a call. Returns (users, row stride, width, pages) and the
     addresses (lens, users, held, held_out, tables, free_pages, free_count, count_out, workspace, status)."""
     dev = held.get_device()
+    if (held_out is None) != (count_out is None):
+        raise ValueError("held_out and count_out come together")
+    if held_out is None:
+        held_out, count_out = held, free_count
     shape = tables.shape
     if len(shape) != 2 or tables.dtype != torch.int32:
         raise ValueError("tables must be torch.int32 [users, pages]")
@@ -1035,10 +1039,6 @@ def pages_assign(new_lens: torch.Tensor, held: torch.Tensor, tables: torch.Tenso
     None without want_slots). If anything does not fit nothing is handed out, and status says why."""
     S = new_lens.numel()
     where = held.device
-    if held_out is None:
-        held_out = held
-    if count_out is None:
-        count_out = free_count
     (U, by_user, width, pages, need), (lens_at, users_at, held_at, held_out_at, tables_at, free_at, count_at, count_out_at,
                                        workspace_at, status_at) = _pages_args(
         held, tables, free_pages, free_count, new_lens, "new_lens", users, S, held_out, count_out, status, workspace)
@@ -1077,8 +1077,7 @@ def pages_release(held: torch.Tensor, tables: torch.Tensor, free_pages: torch.Te
     S = held.numel() if users is None else users.numel()
     where = held.device
     (U, by_user, width, pages, need), at = _pages_args(held, tables, free_pages, free_count, keep, "keep", users, S,
-                                                       held if held_out is None else held_out,
-                                                       free_count if count_out is None else count_out, status, workspace)
+                                                       held_out, count_out, status, workspace)
     lens_at, users_at, held_at, held_out_at, tables_at, free_at, count_at, count_out_at, workspace_at, status_at = at
     if not 0 < page <= _I32_MAX:
         raise ValueError(f"page {page} out of range")

@@ -139,3 +139,19 @@ def test_release_refuses_buffers_that_overlap(lib, a, b):
 def test_lengths_and_counts_that_overlap_in_part(lib):
     for kw in (dict(held_out=PLACES["held"] + 4, count_out=PLACES["count"] + STEP // 2), dict(held_out=PLACES["held"] - 16)):
         assert _assign(lib, **{**ASSIGN, **kw}) == E_INVAL and _release(lib, **{**RELEASE, **kw}) == E_INVAL, kw
+
+
+@pytest.mark.parametrize("kw", [dict(held_out=PLACES["held"]), dict(count_out=PLACES["count"])])
+def test_a_half_planned_step_is_refused(lib, kw):
+    """Lengths in place and the count beside it, or the other way round: pages would be lost, or handed out twice."""
+    assert _assign(lib, **{**ASSIGN, **kw}) == E_INVAL and _release(lib, **{**RELEASE, **kw}) == E_INVAL
+
+
+def test_binding_refuses_a_half_planned_step():
+    z = lambda *s: torch.zeros(s, dtype=torch.int32)
+    held, tables, free, count = z(5), z(5, 8), z(50), z(1)
+    for kw in (dict(held_out=z(5)), dict(count_out=z(1))):
+        with pytest.raises(ValueError, match="come together"):
+            ops.pages_assign(z(2), held, tables, free, count, 16, 4, users=z(2), **kw)
+        with pytest.raises(ValueError, match="come together"):
+            ops.pages_release(held, tables, free, count, 16, users=z(2), **kw)
