@@ -272,8 +272,8 @@ int dlrm_pages_assign(int64_t n, int32_t seqs, int32_t users, const int32_t* new
  * The way back: the history of sequence s keeps its first min(keep[s], held) entries (keep NULL: none),
  * and the pages past them go to the end of the free list, sequence by sequence, in order. All of it or
  * nothing: a user outside [0, users) or in the call twice (DLRM_STATUS_BAD_USER), a negative length or
- * one past table_width pages (DLRM_STATUS_BAD_OFFSETS), or more free pages than num_pages
- * (DLRM_STATUS_BAD_PAGE).
+ * one past table_width pages (DLRM_STATUS_BAD_OFFSETS), more free pages than num_pages, or a page
+ * outside [0, num_pages) among those that would go back (DLRM_STATUS_BAD_PAGE).
  */
 int dlrm_pages_release(int32_t seqs, int32_t users, const int32_t* keep, const int32_t* who, const int32_t* held,
                        int32_t* held_out, const int32_t* tables, int64_t table_stride, int32_t table_width,

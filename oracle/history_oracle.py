@@ -180,6 +180,8 @@ def pages_release(users, keep, held, tables, free, count, page):
         bits |= 4
     if not bits and len(set(users)) < len(users):
         bits |= 16
+    if not bits and any(not 0 <= p < len(free) for u, a, b, _ in moved for p in tables[u][a:b]):
+        bits |= 4
     if bits:
         return bits, held, free, count
     for u, a, b, k in moved:

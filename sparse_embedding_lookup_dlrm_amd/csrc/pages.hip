@@ -2,7 +2,7 @@
 //
 // Assignment: with had = ceil(held / page) and has = ceil((held + new) / page) of each sequence, the
 // sequences take has - had pages each from the end of the free list, one after the other, so an exclusive
-// sum of those over the sequences says where each begins. Release: pages ceil(keep / page) .. had go to
+// sum of those over the sequences says where each begins. Release: pages ceil(keep / page) .. had - 1 go to
 // the end of the free list, in order.
 //
 // A call changes all of its sequences or nothing, so one workgroup first looks at all of them (plan): checks,
@@ -219,18 +219,32 @@ __global__ __launch_bounds__(kFillThreads) void assign_fill_kernel(PagesArgs a) 
   }
 }
 
+// A page outside the cache in a user's row would reach another user by way of the free list: the workgroup that meets
+// one puts lengths and count back to what they were, the same from every workgroup that does. What the others copied lies
+// past the free pages and means nothing then. So the pages are looked at while they are copied, not ahead of it by the
+// one workgroup that plans.
 __global__ __launch_bounds__(kFillThreads) void release_fill_kernel(PagesArgs a) {
   const Plan* plan = static_cast<const Plan*>(a.workspace);
   if (!plan->ok) return;
   const int page = 1 << a.page_shift;
+  bool bad = false;
   for (long long s = blockIdx.y; s < a.seqs; s += gridDim.y) {
     const int held = plan->at[static_cast<long long>(a.seqs) + s];
     const int stay = (kept(a, s, held) + page - 1) >> a.page_shift, has = (held + page - 1) >> a.page_shift;
     const int u = a.who ? a.who[s] : static_cast<int>(s);
     const int32_t* own = a.tables + u * a.table_stride;
     int32_t* to = a.free_pages + plan->count + (static_cast<long long>(plan->at[s]) - stay);
-    for (int i = stay + blockIdx.x * kFillThreads + threadIdx.x; i < has; i += gridDim.x * kFillThreads) to[i] = own[i];
+    for (int i = stay + blockIdx.x * kFillThreads + threadIdx.x; i < has; i += gridDim.x * kFillThreads) {
+      const int32_t p = own[i];
+      bad |= p < 0 || p >= a.num_pages;
+      to[i] = p;
+    }
   }
+  if (!__syncthreads_or(bad)) return;
+  if (bad) flag(a.status, DLRM_STATUS_BAD_PAGE);
+  for (long long s = threadIdx.x; s < a.seqs; s += kFillThreads)
+    a.held_out[a.who ? a.who[s] : s] = plan->at[static_cast<long long>(a.seqs) + s];
+  if (threadIdx.x == 0) *a.count_out = plan->count;
 }
 
 // Parts of a sequence: as many as take 1024 columns or tokens each, as long as that leaves 4096 workgroups.

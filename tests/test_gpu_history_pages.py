@@ -293,3 +293,42 @@ def test_lengths_that_are_the_state_are_refused():
     bits, state = st.assign(st.held, None)
     assert bits == 0
     st.same(*state[:2], count=state[2])
+
+
+@pytest.mark.parametrize("bad", [-5, 10 ** 6, 46])
+@pytest.mark.parametrize("seqs,at", [(1, 0), (3, 2), (70, 1), (70, 2500), (1100, 7)])
+def test_a_bad_page_is_not_released(bad, seqs, at):
+    """A page outside the cache among those that would go back: the call is refused, in place and planned, whichever
+    workgroup meets it; it goes back without its user, or where the user keeps it."""
+    rng = random.Random(seqs + at)
+    users = seqs + 3
+    held = [rng.randint(1, 60) for _ in range(users)]
+    user = seqs // 2
+    held[user] = 16 * at + rng.randint(1, 16)
+    width = at + 6
+    st = State(users, width, 16, held, seed=seqs, spare=30)
+    bad = len(st.free) if bad == 46 else bad  # the first that does not exist
+    good = st.tables[user][at]
+    st.tables[user][at] = bad
+    st.dev()
+    who = rng.sample([u for u in range(users) if u != user], seqs - 1)
+    who.insert(seqs // 3, user)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    before = [x.clone() for x in st.d]
+    other, more = torch.full_like(st.d[0], -1), torch.full_like(st.d[3], -1)
+    for keep in (None, [16 * at if u == user else rng.randint(0, 9) for u in who]):
+        for kw in (dict(held_out=other, count_out=more), {}):
+            ops.pages_release(*st.d, 16, users=i32(who), keep=None if keep is None else i32(keep), status=status, **kw)
+            assert status.item() == ops.STATUS_BAD_PAGE
+            status.zero_()
+            assert torch.equal(before[0], st.d[0]) and torch.equal(before[1], st.d[1]) and torch.equal(before[3], st.d[3])
+            assert torch.equal(before[2][:st.count], st.d[2][:st.count])
+        assert more.item() == st.count and all(other[u] == held[u] for u in who)
+    bits, want = ho.pages_release(who, [0] * seqs, st.held, st.tables, st.free, st.count, 16)[:2]
+    assert bits == ops.STATUS_BAD_PAGE and want == st.held
+    # kept: the rest goes back
+    st.free = st.d[2].tolist()
+    assert st.release(who, [16 * at + 1 if u == user else 0 for u in who]) == 0
+    st.tables[user][at] = good
+    st.d[1][user, at] = good
+    assert st.release(None) == 0 and sorted(st.free) == list(range(len(st.free)))

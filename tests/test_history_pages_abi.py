@@ -155,3 +155,9 @@ def test_binding_refuses_a_half_planned_step():
             ops.pages_assign(z(2), held, tables, free, count, 16, 4, users=z(2), **kw)
         with pytest.raises(ValueError, match="come together"):
             ops.pages_release(held, tables, free, count, 16, users=z(2), **kw)
+
+
+def test_oracle_refuses_to_release_a_bad_page():
+    args = ([[4, 2], [-5, 1]], [0, 3, 9, 9, 9], 2, 16)
+    assert ho.pages_release([1], [0], [20, 20], *args) == (4, [20, 20], [0, 3, 9, 9, 9], 2)
+    assert ho.pages_release([1], [16], [20, 20], *args) == (0, [20, 16], [0, 3, 1, 9, 9], 3)
