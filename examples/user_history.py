@@ -71,7 +71,7 @@ class HistoryCache8:
         codes = lambda: torch.zeros((pages, kv_heads, page, dim), dtype=torch.float8_e4m3fn, device=device)
         self.k, self.v = codes(), codes()
         self.scales = torch.zeros((pages, kv_heads, page // ops.KV_BLOCK, 2), dtype=torch.uint8, device=device)
-        self.hours = torch.zeros(pages * page, dtype=torch.int32, device=device)
+        self.hours = torch.zeros(pages * page + 1, dtype=torch.int32, device=device)  # the last: of tokens without a slot
         i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)
         self.held, self.tables, self.status = i32(users), i32(users, -(-max_events // page)), i32(1)
         self.free = torch.arange(pages, dtype=torch.int32, device=device)
@@ -144,8 +144,8 @@ class HistoryEncoder:
     def step8(self, cache: HistoryCache8, users, ids, hours, new, most_new: int):
         """step over an 8-bit cache; users and new are int32 tensors, most_new the largest of new."""
         call, slots, places = cache.grow(users, new, ids.shape[0])
-        stored = slots >= 0
-        cache.hours.scatter_(0, slots.clamp(min=0), torch.where(stored, hours.to(torch.int32), cache.hours[slots.clamp(min=0)]))
+        none = cache.hours.numel() - 1  # stays zero
+        cache.hours.scatter_(0, torch.where(slots < 0, none, slots), torch.where(slots < 0, 0, hours.to(torch.int32)))
         q, k, v = self.project(ids)
         q = ops.kv_append_q8(k, v, *cache.parts(), *call, q=q, status=cache.status,
                              **self.turn(torch.stack([places, hours.to(torch.int32)])))

@@ -79,3 +79,14 @@ def test_without_room_nothing_is_stored(example):  # noqa: F811
     cache.drop(i32([0]), keep=i32([16]))
     enc.step8(cache, i32([2, 1]), ids[:30], ids[:30], i32([17, 6]), 17)
     assert cache.status.item() == 0 and cache.held.tolist() == [16, 16, 17] and cache.count.item() == 0
+
+
+def test_tokens_without_a_slot_change_no_hours(example):  # noqa: F811
+    """A padded batch whose one event takes slot 0, the place that tokens without a slot could be sent to."""
+    enc = example.HistoryEncoder(items=500, width=64, q_heads=4, kv_heads=2, dim=64)
+    for padding in (1, 63, 3000):
+        cache = example.HistoryCache8(2, pages=1, kv_heads=2, page=16, dim=64, max_events=16, device="cuda")
+        ids = torch.arange(1 + padding, dtype=torch.int32, device="cuda") % 500
+        enc.step8(cache, i32([1]), ids, ids + 7, i32([1]), 1)
+        assert cache.status.item() == 0 and cache.tables[1, 0] == 0
+        assert cache.hours.tolist() == [7] + [0] * (cache.hours.numel() - 1)
