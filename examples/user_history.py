@@ -142,7 +142,8 @@ class HistoryEncoder:
         return ops.paged_attn(q, cache.k, cache.v, offsets, lens, table, causal=False, **most).flatten(1)
 
     def step8(self, cache: HistoryCache8, users, ids, hours, new, most_new: int):
-        """step over an 8-bit cache; users and new are int32 tensors, most_new the largest of new."""
+        """step over an 8-bit cache; users and new are int32 tensors, most_new the largest of new. The outputs of
+        tokens that belong to no user (a padded batch, a call without room) are zero."""
         call, slots, places = cache.grow(users, new, ids.shape[0])
         none = cache.hours.numel() - 1  # stays zero
         cache.hours.scatter_(0, torch.where(slots < 0, none, slots), torch.where(slots < 0, 0, hours.to(torch.int32)))
@@ -150,7 +151,7 @@ class HistoryEncoder:
         q = ops.kv_append_q8(k, v, *cache.parts(), *call, q=q, status=cache.status,
                              **self.turn(torch.stack([places, hours.to(torch.int32)])))
         return ops.paged_attn_q8(q, *cache.parts(), *call, max_q=most_new, max_kv=cache.max_events,
-                                 status=cache.status).flatten(1)
+                                 out=torch.zeros_like(q), status=cache.status).flatten(1)
 
     def train_norms(self, ids, place, hours, d_q, d_k, lr: float):
         """One SGD step on the norm weights from the gradients of the normed and rotated queries and keys;

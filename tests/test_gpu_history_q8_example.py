@@ -90,3 +90,17 @@ def test_tokens_without_a_slot_change_no_hours(example):  # noqa: F811
         enc.step8(cache, i32([1]), ids, ids + 7, i32([1]), 1)
         assert cache.status.item() == 0 and cache.tables[1, 0] == 0
         assert cache.hours.tolist() == [7] + [0] * (cache.hours.numel() - 1)
+
+
+def test_outputs_without_a_user_are_zero(example):  # noqa: F811
+    """A call without room, and the padding of one that has it, beside memory that holds NaN."""
+    enc = example.HistoryEncoder(items=500, width=64, q_heads=4, kv_heads=2, dim=64)
+    cache = example.HistoryCache8(3, pages=4, kv_heads=2, page=16, dim=64, max_events=64, device="cuda")
+    ids = torch.arange(70, dtype=torch.int32, device="cuda")
+    for new, most, good in ((i32([33, 37]), 37, 0), (i32([16, 20]), 20, 36)):
+        spoilt = [torch.full((70, 4, 64), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+        del spoilt
+        out = enc.step8(cache, i32([2, 1]), ids, ids, new, most)
+        assert cache.status.item() == (0 if good else example.ops.STATUS_NO_ROOM)
+        assert torch.isfinite(out).all() and (out[good:] == 0).all() and (out[:good] != 0).any(1).all()
+        cache.status.zero_()
