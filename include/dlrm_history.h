@@ -202,7 +202,9 @@ int dlrm_kv_append_q8(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads
                       uint8_t* kv_scales, int64_t scale_page_stride, int64_t scale_head_stride, void* q_out,
                       int32_t* status, void* stream);
 
-/* Workspace of dlrm_paged_attn_q8 for these sizes (0 where no history is split). */
+/* Workspace of dlrm_paged_attn_q8 for these sizes (0 where no history can be in parts). Where every history is in
+ * parts it holds their sums, as in dlrm_paged_attn; for parts of those with few new tokens beside others it holds at
+ * most twice as much as out in fp32, or 32 MB, and two words for each row of that. */
 int dlrm_paged_attn_q8_workspace_bytes(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t dim,
                                        int32_t causal, int32_t window, int32_t max_q, int32_t max_kv, size_t* bytes);
 

@@ -154,19 +154,47 @@ __device__ __forceinline__ float add_quarters(float x) {
 
 // How a call is cut: q_tiles tiles of rows per sequence and head, splits parts of a tile's entries. The
 // grid is heads x (tiles x parts) x sequences. A sequence of fewer tiles than there are places for them has up to
-// `spread` parts in their stead, if that is more.
+// `spread` parts in their stead, if that is more and its rows have room.
+//
+// Sums of parts lie in rows of dim elements: with splits > 1 splits x n x q_heads of them, [split][token][head];
+// behind these, with a spread, spare x kv_heads rows for each sequence, [split][token of the sequence][head].
 struct Cut {
   int q_tiles, splits, part;  // part: entries of a part, unless the history is longer than announced
-  int spread;
-  float* o;                   // [splits or spread][n][q_heads][dim], not yet divided by the sums
-  float2* ml;                 // [n][q_heads][splits or spread]: maximum and sum
-  __host__ __device__ __forceinline__ int most() const { return spread > splits ? spread : splits; }
+  int spread, spare;          // spare: rows of a head that a sequence has for the sums of its spread
+  float* o;                   // sums, not yet divided
+  float2* ml;                 // maximum and sum of each: [token][head][split], like the rows in bytes
+  __host__ __device__ __forceinline__ bool in_parts() const { return splits > 1 || spread > splits; }
   // Parts that a sequence of so many rows may have, in tiles of tile_rows.
   __device__ __forceinline__ int parts_of(int rows, int tile_rows) const {
-    if (spread <= splits) return splits;
-    const int tiles = (rows + tile_rows - 1) / tile_rows, fit = tiles > 0 ? q_tiles * splits / tiles : spread;
-    return fit < splits ? splits : fit < spread ? fit : spread;
+    if (spread <= splits || rows <= 0) return splits;
+    const int places = places_of(rows, tile_rows);
+    int most = places < spread ? places : spread;
+    if (most > splits && rows * most > spare) most = spare / rows;
+    return most > splits ? most : splits;
   }
+  // Workgroups of a head for each tile of such a sequence.
+  __device__ __forceinline__ int places_of(int rows, int tile_rows) const {
+    return q_tiles * splits / ((rows - 1) / tile_rows + 1);
+  }
+};
+
+// Where the parts of a sequence that may have so many are: row r of the sequence's (token, head) and part `split`.
+struct Sums {
+  long long first, step, first_ml;
+  int per;
+  __device__ __forceinline__ Sums(const AttnArgs& a, const Cut& cut, const Seq& s, int seq, int may) : per(may) {
+    if (may > cut.splits) {
+      const long long all = cut.splits > 1 ? cut.splits * a.n * a.q_heads : 0;
+      first = first_ml = all + static_cast<long long>(seq) * cut.spare * a.kv_heads;
+      step = static_cast<long long>(s.tokens) * a.q_heads;
+    } else {
+      first = static_cast<long long>(s.first) * a.q_heads;
+      first_ml = first * cut.splits;
+      step = a.n * a.q_heads;
+    }
+  }
+  __device__ __forceinline__ long long row(int r, int split) const { return first + split * step + r; }
+  __device__ __forceinline__ long long ml(int r) const { return first_ml + static_cast<long long>(r) * per; }
 };
 
 constexpr int kLeastPart = 512;  // entries of a part that a sequence of few rows is spread to
@@ -206,8 +234,10 @@ __device__ __forceinline__ void finish(const AttnArgs& a, long long to, int at, 
   if (at == 0 && a.lse) a.lse[to] = l == 0.f ? -INFINITY : fmaf(m, a.scale, logf(l) - kLift<DT> * kLn2);
 }
 
-// The sequence that comes `at`-th if those whose parts are longest come first, where a wave can look at all of them
-// (up to 64); else the at-th. Equal ones keep their order. tile_rows: rows of a tile.
+// The sequence that comes `at`-th if those with the most entries to a workgroup come first, where a wave can look at
+// all of them (up to 64); else the at-th. Equal ones keep their order. tile_rows: rows of a tile. Counted are the
+// workgroups that a sequence has, up to 16 to a tile, also where its parts are fewer (candidates: 23.5 us, by parts
+// 25.8).
 __device__ __forceinline__ int longest_first(const AttnArgs& a, const Cut& cut, int at, int tile_rows) {
   const Paged& p = a.paged;
   if (p.seqs > kWave) return at;
@@ -215,7 +245,8 @@ __device__ __forceinline__ int longest_first(const AttnArgs& a, const Cut& cut, 
   const int held = p.kv_lens[i], tokens = p.q_offsets[i + 1] - p.q_offsets[i];  // bad ones count as they may
   const int seen = a.window > 0 && held > a.window ? a.window : held;
   const bool some = lane < p.seqs && tokens > 0 && tokens <= a.n;
-  const int work = some && seen > 0 ? seen / cut.parts_of(tokens * group, tile_rows) + 1 : lane < p.seqs ? 0 : -1;
+  const int places = some ? cut.places_of(tokens * group, tile_rows) : 1, parts = places < 16 ? places : 16;
+  const int work = some && seen > 0 ? seen / (parts > cut.splits ? parts : cut.splits) + 1 : lane < p.seqs ? 0 : -1;
   int before = 0;
   for (int j = 0; j < p.seqs; ++j) {
     const int other = __builtin_amdgcn_readlane(work, j);
@@ -278,7 +309,7 @@ __device__ __forceinline__ void join_waves(const AttnArgs& a, const Cut& cut, co
       float* p = cut.o + (split * a.n * a.q_heads + to) * D + at;
       *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
       *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-      if (at == 0) cut.ml[to * cut.most() + split] = make_float2(mt, lt);
+      if (at == 0) cut.ml[to * cut.splits + split] = make_float2(mt, lt);
     }
   }
 }
@@ -302,6 +333,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, Cut cut
     const Seq sq = load_seq(a.paged, a.n, seq);
     const int rows = sq.tokens * a.q_heads, may = cut.parts_of(sq.tokens * group, tile_rows);
     if (may == 1) continue;
+    const Sums sums(a, cut, sq, seq, may);
     for (long long first = static_cast<long long>(blockIdx.x) * Rows; first < rows;
          first += static_cast<long long>(gridDim.x) * Rows) {
       const int row = static_cast<int>(first) + threadIdx.x / (Lanes * Slots);
@@ -312,9 +344,9 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, Cut cut
                      may);
       if (rc.parts == 1) continue;
       const long long to = static_cast<long long>(sq.first) * a.q_heads + row;
-      const float2* ml = cut.ml + to * cut.most();
-      const float* o = cut.o + to * D + at;
-      const long long step = a.n * a.q_heads * D;
+      const float2* ml = cut.ml + sums.ml(row);
+      const float* o = cut.o + sums.row(row, 0) * D + at;
+      const long long step = sums.step * D;
       float m = -INFINITY, l = 0.f, x[8] = {};
 #pragma unroll 4
       for (int i = slot; i < rc.parts; i += Slots) m = fmaxf(m, ml[i].x);
@@ -372,10 +404,15 @@ int tile_rows(long long max_rows) { return max_rows <= 16 ? 16 : 32 * kWaves; }
 
 constexpr size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
-size_t cut_bytes(const Cut& c, int64_t n, int q_heads, int dim) {
-  if (c.most() == 1) return 0;
-  const size_t rows = static_cast<size_t>(n) * q_heads * c.most();
-  return round256(rows * dim * sizeof(float)) + rows * sizeof(float2);
+// Rows of sums of a call.
+long long sum_rows(const Cut& c, int64_t n, int seqs, int q_heads, int kv_heads) {
+  return (c.splits > 1 ? c.splits * n * q_heads : 0) +
+         (c.spread > c.splits ? static_cast<long long>(seqs) * c.spare * kv_heads : 0);
+}
+
+size_t cut_bytes(const Cut& c, int64_t n, int seqs, int q_heads, int kv_heads, int dim) {
+  const size_t rows = static_cast<size_t>(sum_rows(c, n, seqs, q_heads, kv_heads));
+  return rows == 0 ? 0 : round256(rows * dim * sizeof(float)) + rows * sizeof(float2);
 }
 
 // The kernel of a call that is cut into tiles of `tile` rows and into parts, and their join.
@@ -383,14 +420,14 @@ template <int DT, int D>
 hipError_t launch_cut(const AttnArgs& a, Cut cut, int tile, void (*kernel)(AttnArgs, Cut), int threads, hipStream_t s) {
   const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
   cut.o = static_cast<float*>(a.workspace);
-  cut.ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) +
-                                     round256(static_cast<size_t>(a.n) * a.q_heads * cut.most() * D * sizeof(float)));
+  const size_t sums = static_cast<size_t>(sum_rows(cut, a.n, a.paged.seqs, a.q_heads, a.kv_heads));
+  cut.ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + round256(sums * D * sizeof(float)));
   const unsigned seqs = a.paged.seqs < 65535 ? a.paged.seqs : 65535;
   hipLaunchKernelGGL(kernel, dim3(a.kv_heads, cut.q_tiles * cut.splits, seqs), dim3(threads), 0, s, a, cut);
   const long long all_rows = rows * a.kv_heads * a.paged.seqs;
-  if (cut.most() > 16 && all_rows <= 512)
+  if (cut.splits > 16 && all_rows <= 512)
     join<DT, D, kThreads / (D / 8)>(a, cut, tile, s);
-  else if (cut.most() > 1)
+  else if (cut.in_parts())
     join<DT, D, 1>(a, cut, tile, s);
   return hipGetLastError();
 }

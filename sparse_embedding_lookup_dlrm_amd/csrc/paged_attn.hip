@@ -675,7 +675,7 @@ Cut cut_call(long long all_rows, long long max_rows, int seqs, int kv_heads, int
   if (splits > 65535 / tiles) splits = 65535 / tiles;
   c.splits = static_cast<int>(splits);
   c.part = static_cast<int>(((span + splits - 1) / splits + 63) & ~63LL);
-  c.spread = 0;
+  c.spread = c.spare = 0;
   c.o = nullptr;
   c.ml = nullptr;
   return c;
@@ -706,7 +706,8 @@ size_t attn_workspace(int64_t n, int seqs, int q_heads, int kv_heads, int dim, i
                       int max_kv) {
   if (n == 0 || seqs == 0) return 0;
   const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
-  return cut_bytes(cut_call(n * q_heads, rows, seqs, kv_heads, dim, causal, window, max_q, max_kv), n, q_heads, dim);
+  return cut_bytes(cut_call(n * q_heads, rows, seqs, kv_heads, dim, causal, window, max_q, max_kv), n, seqs, q_heads,
+                   kv_heads, dim);
 }
 
 hipError_t launch_paged_attn(const AttnArgs& a, hipStream_t s) {

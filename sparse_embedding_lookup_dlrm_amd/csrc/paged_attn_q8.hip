@@ -629,6 +629,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_q8_kerne
       l = add_halves(l);
       if (row < w1) {
         const bool part = rc.parts > 1;
+        const Sums sums(a, cut, sq, seq, may);
+        const int in_seq = static_cast<int>(to - static_cast<long long>(sq.first) * a.q_heads);
         const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int i = 0; i < C; ++i)
@@ -638,15 +640,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_q8_kerne
             const float x0 = o[i][4 * q] * inv, x1 = o[i][4 * q + 1] * inv, x2 = o[i][4 * q + 2] * inv,
                         x3 = o[i][4 * q + 3] * inv;
             if (part)
-              *reinterpret_cast<float4*>(cut.o + (split * a.n * a.q_heads + to) * D + at_d) =
-                  make_float4(x0, x1, x2, x3);
+              *reinterpret_cast<float4*>(cut.o + sums.row(in_seq, split) * D + at_d) = make_float4(x0, x1, x2, x3);
             else
               *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to * D + at_d) =
                   make_uint2(pack2<DT>(x0, x1), pack2<DT>(x2, x3));
           }
         if (h == 0) {
           if (part)
-            cut.ml[to * cut.most() + split] = make_float2(m, l);
+            cut.ml[sums.ml(in_seq) + split] = make_float2(m, l);
           else if (a.lse)
             a.lse[to] = l == 0.f ? -INFINITY : fmaf(m, a.scale, logf(l) - kLift<DT> * kLn2);
         }
@@ -694,9 +695,24 @@ Cut cut_call(long long all_rows, long long max_rows, int seqs, int kv_heads, int
   if (splits > 65535 / tiles) splits = 65535 / tiles;
   c.splits = static_cast<int>(splits);
   c.part = static_cast<int>(((span + splits - 1) / splits + 63) & ~63LL);
-  // sequences of few rows beside those of many: up to 16 parts, as long as there are sums of a million rows at most
-  const long long room = (1LL << 20) / (all_rows > 0 ? all_rows : 1);
-  c.spread = rows == 16 || tiles == 1 ? 0 : room < 16 ? static_cast<int>(room) : 16;
+  // Sequences of few rows beside those of many: up to 16 parts, less in calls of many rows (one of 8192 tokens and 127
+  // of one: 1533 us in 3, 1588 in 16), and none where that gives no history more. Their sums take no more room than
+  // twice the result in fp32, or 32 MB where that is less, and all sums no more than a million rows. The room is shared
+  // out evenly (12 chunks of 256-wide heads: 102 us, with half of it 118); a sequence needs at most what its tiles and
+  // parts fill. A single one is taken to have the n tokens of the call.
+  const long long finest = (span + kLeastPart - 1) / kLeastPart, least_room = (8LL << 20) / dim;
+  const long long filled = static_cast<long long>(c.q_tiles) * c.splits * rows;
+  long long parts = (1LL << 20) / (all_rows > 0 ? all_rows : 1), left = 1LL << 20;
+  if (parts > 16) parts = 16;
+  if (parts > finest) parts = finest;
+  if (c.splits > 1) left -= all_rows * c.splits;
+  long long room = 2 * all_rows > least_room ? 2 * all_rows : least_room;
+  room = (room < left ? room : left) / (static_cast<long long>(seqs) * kv_heads);
+  if (room > filled) room = filled;
+  const bool alone = seqs == 1 && all_rows / kv_heads > filled / (c.splits + 1);
+  const bool spread = rows > 16 && tiles > 1 && parts > c.splits && room > c.splits && !alone;
+  c.spread = spread ? static_cast<int>(parts) : 0;
+  c.spare = spread ? static_cast<int>(room) : 0;
   c.o = nullptr;
   c.ml = nullptr;
   return c;
@@ -727,7 +743,8 @@ size_t attn_q8_workspace(int64_t n, int seqs, int q_heads, int kv_heads, int dim
                          int max_kv) {
   if (n == 0 || seqs == 0) return 0;
   const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
-  return cut_bytes(cut_call(n * q_heads, rows, seqs, kv_heads, dim, causal, window, max_q, max_kv), n, q_heads, dim);
+  return cut_bytes(cut_call(n * q_heads, rows, seqs, kv_heads, dim, causal, window, max_q, max_kv), n, seqs, q_heads,
+                   kv_heads, dim);
 }
 
 hipError_t launch_paged_attn_q8(const AttnArgs& a, hipStream_t s) {

@@ -134,3 +134,27 @@ def test_oracle_block_by_hand():
     # a smaller one later leaves the scale
     ho.append_q8(x / 64, codes, scales, [0, 1], [3], [[0]])
     assert scales[0, 0, 0] == 128 and (ho.e4m3_values()[codes[0, 0, 2]] == 7).all()
+
+
+def _workspace(lib, n, S, Hq, Hk, D, max_q, max_kv, causal=1, window=0):
+    need = ctypes.c_size_t(0)
+    assert lib.dlrm_paged_attn_q8_workspace_bytes(n, S, Hq, Hk, D, causal, window, max_q, max_kv, ctypes.byref(need)) == 0
+    return need.value
+
+
+@pytest.mark.parametrize("n,S,Hq,Hk,D,max_q,max_kv,window", [
+    (2048, 4, 32, 8, 128, 512, 512, 0), (2048, 4, 32, 32, 128, 512, 512, 0), (8192, 8, 64, 8, 256, 1024, 1, 0), (4096, 64, 32, 8, 64, 64, 300, 0),
+    (2048, 4, 32, 32, 128, 400, 100000, 20), (2048, 1, 32, 32, 256, 2048, 100000, 0), (2048, 1, 64, 64, 128, 2048, 1000, 0)])
+def test_no_workspace_where_nothing_can_be_in_parts(lib, n, S, Hq, Hk, D, max_q, max_kv, window):
+    """Histories shorter than the shortest part, or a window that is; a single sequence, which has the tiles it was said to have."""
+    assert _workspace(lib, n, S, Hq, Hk, D, max_q, max_kv, window=window) == 0
+
+
+@pytest.mark.parametrize("n,S,Hq,Hk,D,max_q,max_kv,causal,window", [
+    (6400, 4, 32, 8, 128, 2048, 8192, 1, 0), (3200, 12, 8, 4, 256, 513, 6000, 1, 1024), (2048, 4, 32, 32, 256, 512, 600, 1, 0),
+    (2143, 96, 32, 8, 128, 2048, 16384, 1, 0), (40000, 300, 16, 4, 64, 2000, 131072, 0, 0), (600, 3, 4, 4, 32, 500, 9000, 1, 0)])
+def test_workspace_for_few_rows_beside_many(lib, n, S, Hq, Hk, D, max_q, max_kv, causal, window):
+    """No more than twice the result in fp32, or 32 MB, and a maximum and a sum for each row. Enough tiles that no history
+    of many rows is in parts."""
+    rows = max(2 * n * Hq, (32 << 20) // (4 * D))
+    assert _workspace(lib, n, S, Hq, Hk, D, max_q, max_kv, causal, window) <= rows * (4 * D + 8) + 256
