@@ -723,8 +723,8 @@ hipError_t run(const AttnArgs& a, hipStream_t s) {
   const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
   const Cut cut = cut_call(a.n * a.q_heads, rows, a.paged.seqs, a.kv_heads, D, a.causal, a.window, a.max_q, a.max_kv);
   const int tile = tile_rows(rows);
-  if (tile == 16) return launch_cut<DT, D>(a, cut, tile, attn_rows_q8_kernel<DT, D>, kThreads, s);
-  return launch_cut<DT, D>(a, cut, tile, attn_tile_q8_kernel<DT, D>, kThreads, s);
+  if (tile == 16) return launch_cut<DT, D, false>(a, cut, tile, attn_rows_q8_kernel<DT, D>, kThreads, s);
+  return launch_cut<DT, D, true>(a, cut, tile, attn_tile_q8_kernel<DT, D>, kThreads, s);
 }
 
 template <int DT>

@@ -868,9 +868,11 @@ def _append(q8: bool, k, v, k_cache, v_cache, kv_scales, q_offsets, kv_lens, pag
         if q is not None and q_out is None:
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         fn, name = (lib().dlrm_kv_append_q8, "dlrm_kv_append_q8") if q8 else (lib().dlrm_kv_append, "dlrm_kv_append")
-        _check(fn(N, S, Hq, Hk, D, rot, _TORCH_DT[dt], *qa, *ka, *va, *turn, offsets_at, lens_at, table_at, by_seq, width,
-                  page, pages, by_page, by_head, k_cache.data_ptr(), v_cache.data_ptr(), *scales, _ptr(q_out), status_at, s),
-               name)
+        code = fn(N, S, Hq, Hk, D, rot, _TORCH_DT[dt], *qa, *ka, *va, *turn, offsets_at, lens_at, table_at, by_seq, width, page,
+                  pages, by_page, by_head, k_cache.data_ptr(), v_cache.data_ptr(), *scales,
+                  None if q_out is None else q_out.data_ptr(), status_at, s)
+        if code:
+            _check(code, name)
     return q_out
 
 
@@ -944,10 +946,15 @@ def _attn(q8: bool, q, k_cache, v_cache, kv_scales, q_offsets, kv_lens, page_tab
         if workspace is None and need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=where)
         fn, name = (lib().dlrm_paged_attn_q8, "dlrm_paged_attn_q8") if q8 else (lib().dlrm_paged_attn, "dlrm_paged_attn")
-        _check(fn(N, S, Hq, Hk, D, _TORCH_DT[dt], *qa, k_cache.data_ptr(), v_cache.data_ptr(), page, pages, by_page, by_head,
+        if workspace is None:
+            workspace_at = workspace_bytes = 0
+        else:
+            workspace_at, workspace_bytes = workspace.data_ptr(), workspace.numel()
+        code = fn(N, S, Hq, Hk, D, _TORCH_DT[dt], *qa, k_cache.data_ptr(), v_cache.data_ptr(), page, pages, by_page, by_head,
                   *scales, offsets_at, lens_at, table_at, by_seq, width, 1 if causal else 0, window, scale, max_q, max_kv,
-                  out.data_ptr(), _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel(), status_at, s),
-               name)
+                  out.data_ptr(), None if lse is None else lse.data_ptr(), workspace_at, workspace_bytes, status_at, s)
+        if code:
+            _check(code, name)
     return (out, lse) if want_lse else out
 
 
