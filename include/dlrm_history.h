@@ -60,7 +60,8 @@
  *                            [q_offsets[0], q_offsets[seqs]], counts as having no
  *                            tokens; the others keep theirs. Where some of those
  *                            overlap, a token they share is stored for one of them,
- *                            and its attention output is that of one of them. The
+ *                            and its attention output is that of one of them (where
+ *                            histories are in parts, of parts of both). The
  *                            attention clamps a length to [0, table_width * page];
  *                            the append stores no token of a sequence whose length is
  *                            bad, and none that would fall before the first entry (a
@@ -187,7 +188,9 @@ int dlrm_paged_attn(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, 
  * once. A block's byte b is the smallest >= 1 under which the largest finite |x| of its new entries is a code:
  * |x| <= 448 * 2^(b - 127). Where the block also holds entries from before this call, it is at least what it was, and
  * if it grows their codes are rounded again to the new scale. Rounding is to nearest even; an element that is not
- * finite becomes NaN and counts for no scale. A block under byte 255 stays NaN.
+ * finite becomes NaN and counts for no scale. A block under byte 255 stays NaN. What the cache holds may lie past the
+ * range of dtype: from 63488 on a value rounds to 65536, which the attention in DLRM_F16 takes for infinite, and from
+ * 1.9375 * 2^127 on to 2^128, likewise in DLRM_BF16.
  * The pages of different sequences must be different in blocks where new tokens fall. A token that several
  * sequences share because offsets are bad is stored for each of them.
  */
@@ -211,7 +214,8 @@ int dlrm_paged_attn_q8_workspace_bytes(int64_t n, int32_t seqs, int32_t q_heads,
 /*
  * dlrm_paged_attn over the 8-bit cache: the same attention over the values that the codes stand for. In the
  * products these are of dtype, which holds them exactly within its range: of DLRM_F16 one past 65504 is
- * infinite and one below 2^-14 is a multiple of 2^-24, of DLRM_BF16 one below 2^-126 may count as zero.
+ * infinite and one below 2^-14 is a multiple of 2^-24, of DLRM_BF16 one past 2^128 is infinite and one below
+ * 2^-126 is a multiple of 2^-133 or counts as zero.
  */
 int dlrm_paged_attn_q8(int64_t n, int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t dtype,
                        const void* q, int64_t q_stride, int64_t q_head_stride, const void* k_cache,

@@ -312,3 +312,79 @@ def test_entries_counted_up_to_31_bits(m, max_q):
                             status=status, max_q=max_q)
     assert status.item() == 0
     check(h, window=70000, got=got)
+
+
+def _all_codes(nan):
+    codes = torch.arange(256, dtype=torch.uint8)
+    return codes if nan else torch.where(codes % 128 == 127, 0, codes)
+
+
+def _one_entry(codes, which):
+    """256 histories of one entry, of 256 elements: every code in each, under byte s; the other cache holds zeros under 127."""
+    full = codes.expand(256, 1, 16, 256).contiguous().cuda().view(torch.float8_e4m3fn)
+    none = torch.zeros((256, 1, 16, 256), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    scales = torch.full((256, 1, 1, 2), 127, dtype=torch.uint8, device="cuda")
+    scales[:, 0, 0, which] = torch.arange(256, dtype=torch.uint8, device="cuda")
+    return ((full, none) if which == 0 else (none, full)) + (scales,)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 17])
+def test_values_of_all_codes_under_all_scales(tokens, t):
+    """The weight of a single entry is 1, so its value comes out as the products see it: exactly within the type's range, the
+    nearest multiple of 2^-24 below 2^-14 in fp16, of 2^-133 below 2^-126 in bf16, or zero there. By both kernels."""
+    dt = torch.float16 if t == "f16" else torch.bfloat16
+    i32 = lambda x: x.to(device="cuda", dtype=torch.int32)
+    codes = _all_codes(True)
+    q = torch.zeros((256 * tokens, 1, 256), dtype=dt, device="cuda")
+    got = ops.paged_attn_q8(q, *_one_entry(codes, 1), i32(torch.arange(257) * tokens), i32(torch.ones(256)),
+                            i32(torch.arange(256))[:, None].contiguous(), causal=False, max_q=tokens, max_kv=1)
+    got = got.view(256, tokens, 256).double().cpu()
+    exact = codes.view(torch.float8_e4m3fn).double() * 2.0 ** (torch.arange(256).double()[:, None] - 127)
+    exact[255] = float("nan")
+    exact = exact[:, None].expand(got.shape)
+    assert torch.equal(got.isnan(), exact.isnan())
+    got, exact = got.nan_to_num(nan=0.0, posinf=float("inf"), neginf=-float("inf")), exact.nan_to_num(nan=0.0)
+    top, least = torch.finfo(dt).max, torch.finfo(dt).smallest_normal
+    want = torch.where(exact.abs() > top, exact * float("inf"), exact).nan_to_num(nan=0.0, posinf=float("inf"), neginf=-float("inf"))
+    normal = exact.abs() >= least
+    assert torch.equal(got[normal], want[normal])
+    if t == "f16":
+        assert ((got - exact)[~normal].abs() <= 2.0 ** -25).all()
+    else:
+        # the least code under byte 0 is 2^-136, the least bf16 2^-133: half a step is 2^-134
+        assert (((got - exact).abs() <= 2.0 ** -134) | (got == 0))[~normal].all()
+
+
+@pytest.mark.parametrize("t,lo,hi", [("f16", 112, 134), ("bf16", 10, 246)])
+@pytest.mark.parametrize("heads", [16, 256])
+def test_keys_of_all_codes_under_all_scales(heads, t, lo, hi):
+    """Head i's query picks element i of the key and undoes the scale, so that its score is the code's value. A score of up to
+    448 is off by two roundings of s log2(e), 2^-15 each, in the exponent, and by 2^-16 when it becomes the result. Codes
+    that are not NaN (a NaN is every head's), bytes under which the type holds every code (448 x 2^(246 - 127) = 1.75 x
+    2^127 in bf16) and the power of two that undoes them."""
+    dt = torch.float16 if t == "f16" else torch.bfloat16
+    i32 = lambda x: x.to(device="cuda", dtype=torch.int32)
+    codes = _all_codes(False)
+    undo = 2.0 ** (127 - torch.arange(lo, hi + 1).double())
+    cache = _one_entry(codes, 0)
+    n = hi + 1 - lo
+    for first in range(0, 256, heads):
+        q = torch.zeros((n, heads, 256), dtype=torch.float64)
+        for i in range(heads):
+            q[:, i, first + i] = undo
+        _, lse = ops.paged_attn_q8(q.to(dt).cuda(), *cache, i32(torch.arange(n + 1)), i32(torch.ones(n)),
+                                   i32(torch.arange(lo, hi + 1))[:, None].contiguous(), scale=1.0, max_q=1, max_kv=1, want_lse=True)
+        want = codes.view(torch.float8_e4m3fn).double()[first:first + heads].expand(n, heads)
+        assert ((lse.double().cpu() - want).abs() <= 2.0 ** -13).all()
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,D", [([1] * 40, list(range(1, 4001, 100)), 128), ([600, 3, 40], [700, 5000, 3000], 64), ([33, 5], [900, 40], 256)])
+def test_a_call_repeats_itself(q_lens, kv_lens, D):
+    """The same bits from every call: no sum depends on the order in which workgroups finish."""
+    h = History8(q_lens, kv_lens, 8, 2, D, 16, "bf16", seed=3)
+    args = h.args()
+    first = ops.paged_attn_q8(*args, max_q=max(q_lens), max_kv=max(kv_lens), want_lse=True)
+    for _ in range(5):
+        for a, b in zip(first, ops.paged_attn_q8(*args, max_q=max(q_lens), max_kv=max(kv_lens), want_lse=True)):
+            assert torch.equal(a, b)
