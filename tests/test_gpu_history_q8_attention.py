@@ -388,3 +388,13 @@ def test_a_call_repeats_itself(q_lens, kv_lens, D):
     for _ in range(5):
         for a, b in zip(first, ops.paged_attn_q8(*args, max_q=max(q_lens), max_kv=max(kv_lens), want_lse=True)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("D,Hq,Hk,S,most,few,mid", [(256, 8, 4, 64, 513, 8, 65), (128, 32, 8, 40, 300, 6, 60), (32, 4, 4, 60, 1500, 90, 600)])
+def test_parts_that_room_bounds(D, Hq, Hk, S, most, few, mid, t):
+    """Sequences of few rows beside one of many: their rows times the parts that their places would be are more than the room
+    of each, so that they have fewer; and one that no more than one part fits."""
+    q_lens, kv_lens = [most, mid] + [few, few + 1] * (S // 2 - 1), [most + 30, 900] + [100] * (S - 2)
+    kv_lens[3:8] = [3000, 2600, 1100, 1700, 5000]
+    check(History8(q_lens, kv_lens, Hq, Hk, D, 16, t, seed=D + few), max_q=most, max_kv=8000)
