@@ -183,6 +183,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_q8_kerne
 #pragma unroll
           for (int e = 0; e < E; ++e) o[e] *= keep;
         }
+        // Weights go to the product in its type, half a step off: the matrix unit takes both operands in it. Relative to
+        // 64 bits, results are 2.3e-3 off in bf16 and 2.4e-4 in fp16, their own rounding included; with fp32 weights
+        // 1.7e-3 and 2.0e-4. The sum l is of the weights as they were.
         const float base = m == -INFINITY ? 0.f : m * c - kLift<DT>;
         uint32_t pw[TT][2];
 #pragma unroll
@@ -315,14 +318,16 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_q8_kerne
 // Codes are widened on their way to LDS, once for the workgroup and not by each of its waves: a wave brings 16
 // entries of a tile, loaded while the tile before is worked on, in pieces of 8 codes that become 16 bytes.
 //
-// 4 sequences of up to 2048 tokens over up to 8192, 32 / 8 heads of 128: 340-345 us, 853-866 TFLOP/s (16-bit cache,
-// same inputs: 447), at 1.94 GHz, to which the clock falls under this load. Matrix units are busy 41 % of the time
-// that a CU has work, vector units 52 %; a CU has work 80 % of the time. Left out: widening 13 us (of 411 then), the
-// pieces to LDS 40, these and the loads 80. Tiles of 128 entries and 256 rows to a workgroup: 430-468 us, for jobs
-// are fewer and longer; the jobs of all sequences in order of length: as long, and 5 us more for short calls. Heads
-// of 256: a wave holds all of O, one to a SIMD, and works on 32 entries at once with 4 pieces read ahead: 102-106 us
-// for 12 sequences of up to 513 tokens with a window of 1024; with 8 pieces ahead, whose registers spill, 127-133,
-// with two waves for the same rows, each with half of O, 120-157 (16-bit cache, which has no codes to hold, 86).
+// 4 sequences of up to 2048 tokens over up to 8192, 32 / 8 heads of 128: 338-352 us on five cards, 836-871 TFLOP/s, at
+// 1.94 GHz, to which the clock falls under this load (16-bit cache, same inputs: 447, without parts for sequences of few
+// rows and without their order). Matrix units are busy 41 % of the time that a CU has work, vector units 52 %; a CU has
+// work 78 % of the kernel's clocks. 256 registers are 13 too few, which spill (48 bytes of scratch a lane). Left out:
+// widening 13 us (of 411 then), the pieces to LDS 40, these and the loads 80. Tiles of 128 entries and 256 rows to a
+// workgroup: 430-468 us, for jobs are fewer and longer; the jobs of all sequences in order of length: as long, and 5 us
+// more for short calls. Heads of 256: a wave holds all of O, one to a SIMD, and works on 32 entries at once with 4
+// pieces read ahead, 35 registers spilled: 102-106 us for 12 sequences of up to 513 tokens with a window of 1024; with 8
+// pieces ahead, more of whose registers spill, 127-133, with two waves for the same rows, each with half of O, 120-157
+// (16-bit cache, which has no codes to hold, 86).
 // ---------------------------------------------------------------------------
 template <int DT, int D>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_q8_kernel(AttnArgs a, Cut cut) {
@@ -576,7 +581,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_q8_kerne
             }
             const float base = m == -INFINITY ? 0.f : m * c - kLift<DT>;
             float sum[4] = {};
-            u32x4 pw[2 * T];  // weights of 16 entries each
+            u32x4 pw[2 * T];  // weights of 16 entries each, in the product's type as in the rows kernel
             const auto weigh = [&](int pair) {
               const int r = 2 * (pair % 8);
               const float p_0 = __builtin_amdgcn_exp2f(fmaf(s[pair / 8][r], c, -base));
@@ -657,8 +662,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_tile_q8_kerne
 }
 
 // Where the workgroups of a call would not fill the chip, or histories may be of unequal length, every history is split
-// into parts, by the rules for the 16-bit cache, but for the rows kernel's: 256 KB of keys are twice the entries (64
-// histories of up to 16k entries of 128: 128 us in 9 parts, 130 in 17).
+// into parts, by the rules for the 16-bit cache and with what was measured for them, places included: heads of 64 count
+// 768 workgroups, of which this kernel's registers hold 512 (177, two waves to a SIMD). Measured for this cache are the
+// rows kernel's parts, of 256 KB of keys, which are twice the entries (64 histories of up to 16k entries of 128: 128 us
+// in 9 parts, 130 in 17), and the spread below.
 Cut cut_call(long long all_rows, long long max_rows, int seqs, int kv_heads, int dim, int causal, int window, int max_q,
              int max_kv) {
   Cut c;

@@ -11,7 +11,7 @@
 // tables, slots and positions, with a workgroup for each sequence and part.
 //
 // Both kernels wait for a few loads in a row and a launch: one event each for 64 users, 1024 pages to a row, 3.5 + 3.9
-// us; chunks of 300 users, 300k tokens (4 MB) 4.9 + 6.2; 256 histories of up to 65536 entries dropped 4.0 + 4.3.
+// us; chunks of 300 users, 300k tokens (4 MB) 4.9 + 6.2; 256 histories of up to 65536 entries dropped 4.0 + 4.7.
 #include "history_device.h"
 
 namespace dlrm {
